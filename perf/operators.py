@@ -1,0 +1,461 @@
+"""Cases that measure the position-rotating append and the 4-bit (MXFP4) key-value pool.
+
+Four kinds of call, each a layer's call of a serving engine on a prepared batch:
+  append  rotate q and k by position, write q out and append k / v to the paged pool
+          (bf16, E4M3 or MXFP4);
+  store   quantise k / v into an MXFP4 pool, then read the same rows back as bf16;
+  attend  attention of the batch's tokens over an MXFP4 pool that already holds every key;
+  step    a whole layer call: rotate, append, attend (bf16, E4M3 or MXFP4 pool).
+
+``own`` False computes them with elementary torch operations in fp32 (one rounding at the
+end), True calls the library.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+DEV = "cuda"
+E_LO, E_HI = 105, 140       # E8M0 bytes that a block scale is held to: 2^-22 .. 2^13
+LEVELS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def _case(name, kind, pool, hq, hkv, d, ps, b, n, c, rot=0, inter=False, packed=False, lens=1):
+    """n / c: least and most new / cached tokens a request; lens: seed of the lengths."""
+    return {"name": name, "kind": kind, "pool": pool, "hq": hq, "hkv": hkv, "d": d, "ps": ps, "b": b,
+            "n_lo": n[0], "n_hi": n[1], "c_lo": c[0], "c_hi": c[1], "rot": rot, "inter": inter, "packed": packed,
+            "lens": lens}
+
+
+def listed():
+    return [
+        # one user's next token: latency of the call
+        _case("append 1 token bf16", "append", "bf16", 32, 8, 128, 16, 1, (1, 1), (777, 777), rot=128),
+        # a decode batch over a token-slot E4M3 pool, interleaved pairs
+        _case("append 64 decodes e4m3", "append", "e4m3", 28, 4, 128, 1, 64, (1, 1), (0, 1000), rot=128, inter=True),
+        # a prefill batch, q / k / v slices of one fused projection
+        _case("append prefill bf16", "append", "bf16", 32, 8, 128, 16, 8, (256, 4096), (0, 0), rot=128, packed=True),
+        # chunks of many requests into a 4-bit pool, half of the head rotated
+        _case("append chunks mxfp4", "append", "mxfp4", 32, 8, 128, 16, 16, (1, 1024), (0, 500), rot=64, packed=True),
+        # quantise and read back: a speculative batch's few tokens, and a prefill's many
+        _case("store 64x4 tokens", "store", "mxfp4", 16, 2, 64, 8, 64, (4, 4), (0, 300)),
+        _case("store prefill", "store", "mxfp4", 32, 8, 128, 16, 8, (256, 4096), (0, 0)),
+        # one user's next token over a long conversation: split over the length
+        _case("attend 1 x 16k", "attend", "mxfp4", 32, 8, 128, 16, 1, (1, 1), (16383, 16383)),
+        # the decode benchmark's batch
+        _case("attend 64 decodes", "attend", "mxfp4", 32, 8, 128, 16, 64, (1, 1), (511, 4095)),
+        # few users with very long contexts, group of 7
+        _case("attend 5 long", "attend", "mxfp4", 28, 4, 128, 64, 5, (1, 1), (20011, 100003)),
+        # every head its own keys, token slots, odd lengths from empty caches on
+        _case("attend D64 token slots", "attend", "mxfp4", 16, 16, 64, 1, 40, (1, 1), (0, 4000)),
+        # prefills and chunks on cached prefixes
+        _case("attend chunks", "attend", "mxfp4", 32, 8, 128, 16, 6, (33, 900), (0, 1800)),
+        # the whole layer call of a decode batch
+        _case("step 64 decodes", "step", "mxfp4", 32, 8, 128, 16, 64, (1, 1), (511, 4095), rot=128, packed=True),
+    ]
+
+
+def draw(rng):
+    log = lambda lo, hi: int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    kind = rng.choice(["append", "append", "store", "attend", "attend", "attend", "step"])
+    hq, hkv, d = rng.choice([(32, 8, 128), (28, 4, 128), (32, 32, 128), (16, 1, 128), (32, 2, 128), (64, 16, 128),
+                             (16, 16, 64), (16, 2, 64), (4, 2, 64)])
+    ps = rng.choice([1, 2, 4, 8, 16, 32, 64, 128])
+    pool = rng.choice(["bf16", "e4m3", "mxfp4"]) if kind in ("append", "step") else "mxfp4"
+    rot = rng.choice([d, d, d // 2, 32]) if kind in ("append", "step") else 0
+    inter = bool(rot) and rng.random() < 0.4
+    packed = rng.random() < 0.5
+    if kind in ("append", "store"):
+        total = log(1, 12000)
+        b = min(total, log(1, 100))
+        mean = max(1, total // b)
+        n = (max(1, mean // 2), max(1, mean + mean // 2))
+        c = (0, log(1, 600))
+    elif rng.random() < 0.7 or hq // hkv > 16:   # decode: one token, or a few to verify
+        total = log(1, 120000 * 8 // max(8, hkv))
+        b = min(total, log(1, 100))
+        mean = max(1, total // b)
+        k = rng.choice([1, 1, 1, 2, 4])
+        n, c = (k, k), (mean // 2, mean + mean // 2)
+    else:                                         # chunks and prefills
+        b = log(1, 6)
+        n = (log(1, 40), log(60, 700))
+        c = (0, log(1, 1200))
+    return _case("", kind, pool, hq, hkv, d, ps, b, n, c, rot=rot, inter=inter, packed=packed, lens=rng.randrange(1 << 20))
+
+
+def _lengths(case):
+    r = random.Random(case["lens"])
+    q = [r.randint(case["n_lo"], case["n_hi"]) for _ in range(case["b"])]
+    return q, [n + r.randint(case["c_lo"], case["c_hi"]) for n in q]
+
+
+def _row_bytes(case):
+    raw = case["hkv"] * (case["d"] // 2 + case["d"] // 32)
+    return (raw + 15) // 16 * 16
+
+
+def work(case):
+    q, kv = _lengths(case)
+    hq, hkv, d, kind, pool = case["hq"], case["hkv"], case["d"], case["kind"], case["pool"]
+    T = sum(q)
+    row = {"bf16": hkv * d * 2, "e4m3": hkv * d, "mxfp4": hkv * (d // 2 + d // 32)}[pool]
+    new = 2 * T * hkv * d * 2                     # this step's k and v
+    io = T * hq * d * 2                           # q, or out, or the rotated q
+    if kind == "append":
+        back = 2 * T * (row + hkv * d * 2) if pool == "mxfp4" else 0
+        return {"bytes": new + 2 * io + 2 * T * row + min(T, max(kv)) * case["rot"] * 4 + back, "flops": 0}
+    if kind == "store":
+        return {"bytes": 2 * new + 4 * T * row, "flops": 0}
+    pairs = sum(n * L - n * (n - 1) // 2 for n, L in zip(q, kv))
+    byts = 2 * sum(kv) * row + 2 * io + T * hq * 4
+    if kind == "step":
+        back = 2 * T * (row + hkv * d * 2) if pool == "mxfp4" else 0
+        byts += new + io + 2 * T * row + back
+    return {"bytes": byts, "flops": 4 * d * hq * pairs}
+
+
+# ------------------------------------------------------------------ MXFP4 in torch
+
+def _quantise(x):
+    """fp32 [N, Hkv, D] -> (codes uint8 [N, Hkv, D], scale bytes int32 [N, Hkv, D/32])."""
+    blocks = x.reshape(*x.shape[:-1], -1, 32)
+    amax = blocks.abs().amax(-1)
+    e = torch.frexp(amax).exponent - 1 - 2 + 127
+    e = torch.where(amax == 0, torch.zeros_like(e), e).clamp(E_LO, E_HI)
+    a = torch.ldexp(blocks.abs(), (127 - e).unsqueeze(-1))
+    code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0))
+    code = code + 8 * torch.signbit(blocks).to(torch.uint8)
+    return code.reshape(x.shape).to(torch.uint8), e
+
+
+def _pack(x, case):
+    """fp32 rows [N, Hkv, D] -> pool rows uint8 [N, row_bytes]."""
+    code, e = _quantise(x)
+    rows = torch.zeros(x.shape[0], _row_bytes(case), dtype=torch.uint8, device=x.device)
+    half = case["hkv"] * case["d"] // 2
+    rows[:, :half] = (code[..., 0::2] | (code[..., 1::2] << 4)).reshape(x.shape[0], -1)
+    rows[:, half:half + case["hkv"] * case["d"] // 32] = e.to(torch.uint8).reshape(x.shape[0], -1)
+    return rows
+
+
+def _unpack(rows, case):
+    """Pool rows uint8 [..., row_bytes] -> fp32 [..., Hkv, D]."""
+    hkv, d = case["hkv"], case["d"]
+    half, lead = hkv * d // 2, rows.shape[:-1]
+    table = torch.tensor(LEVELS + tuple(-v for v in LEVELS), dtype=torch.float32, device=rows.device)
+    byte = rows[..., :half].to(torch.int32)
+    x = torch.stack((table[byte & 15], table[byte >> 4]), -1).reshape(*lead, hkv, d // 32, 32)
+    e = rows[..., half:half + hkv * d // 32].to(torch.int32).reshape(*lead, hkv, d // 32, 1)
+    return torch.ldexp(x, e - 127).reshape(*lead, hkv, d)
+
+
+# ------------------------------------------------------------------ inputs
+
+class _State:
+    pass
+
+
+def prepare(case, seed):
+    s = _State()
+    s.case = case
+    q, kv = _lengths(case)
+    hq, hkv, d, ps, B, T = case["hq"], case["hkv"], case["d"], case["ps"], case["b"], sum(q)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed) * 1000003 + 11)
+    randn = lambda *shape: torch.randn(*shape, generator=g, device=DEV)
+    # the batch: lengths, and pages placed at random in the pool
+    s.T, s.max_q, s.max_kv = T, max(q), max(kv)
+    s.q_lens = torch.tensor(q, device=DEV)
+    s.kv_lens = torch.tensor(kv, device=DEV)
+    s.cu = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    s.cu[1:] = torch.cumsum(s.q_lens, 0)
+    s.cache_seqlens = s.kv_lens.to(torch.int32)
+    need = (s.kv_lens + ps - 1) // ps
+    s.pages = sum(-(-L // ps) for L in kv) + 3
+    perm = torch.randperm(s.pages, generator=g, device=DEV)
+    start = torch.cumsum(need, 0) - need
+    j = torch.arange(-(-max(kv) // ps), device=DEV)
+    s.table = torch.where(j < need[:, None], perm[(start[:, None] + j).clamp(max=s.pages - 1)], 0).to(torch.int32)
+    # this step's activations: tensors of their own, or slices of one fused projection
+    if case["packed"]:
+        qkv = randn(T, hq + 2 * hkv, d).to(torch.bfloat16)
+        s.q, s.k, s.v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    else:
+        s.q, s.k, s.v = (randn(T, h, d).to(torch.bfloat16) for h in (hq, hkv, hkv))
+    if case["kind"] in ("attend", "store"):
+        s.q, s.k, s.v = s.q.contiguous(), s.k.contiguous(), s.v.contiguous()
+    # the pool: what earlier steps left, random bytes where no request's key lies
+    slots = s.pages * ps
+    s.k_scale = s.v_scale = None
+    reads = case["kind"] in ("attend", "step")
+    channel = 1.0 + 3.0 * torch.rand(hkv, d, generator=g, device=DEV) ** 4   # some channels are larger
+    if case["pool"] == "bf16":
+        s.k_pool = (randn(slots, hkv, d) * channel).to(torch.bfloat16)
+        s.v_pool = randn(slots, hkv, d).to(torch.bfloat16)
+    elif case["pool"] == "e4m3":
+        s.k_scale = (0.02 + 0.03 * torch.rand(hkv, generator=g, device=DEV))
+        s.v_scale = (0.01 + 0.02 * torch.rand(hkv, generator=g, device=DEV))
+        enc = lambda x, sc: (x / sc[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        s.k_pool = enc(randn(slots, hkv, d) * channel, s.k_scale)
+        s.v_pool = enc(randn(slots, hkv, d), s.v_scale)
+    else:
+        rb = _row_bytes(case)
+        s.k_pool, s.v_pool = (torch.randint(0, 256, (slots, rb), generator=g, device=DEV, dtype=torch.uint8)
+                              for _ in range(2))
+        if reads:
+            at = s.table.long()[:, :, None] * ps + torch.arange(ps, device=DEV)
+            at = at.reshape(B, -1)[torch.arange(at.shape[1] * ps, device=DEV) < s.kv_lens[:, None]]
+            for lo in range(0, at.numel(), 65536):
+                part = at[lo:lo + 65536]
+                s.k_pool[part] = _pack(randn(part.numel(), hkv, d) * channel, case)
+                s.v_pool[part] = _pack(randn(part.numel(), hkv, d), case)
+    # where each new token goes, and its position
+    s.req = torch.repeat_interleave(torch.arange(B, device=DEV), s.q_lens, output_size=T)
+    s.row = torch.arange(T, device=DEV) - s.cu[:-1].long()[s.req]
+    s.pos = (s.kv_lens - s.q_lens)[s.req] + s.row
+    s.slots = s.table.long()[s.req, s.pos // ps] * ps + s.pos % ps
+    # cos and sin of every position's angles, formed in 64 bits
+    if case["rot"]:
+        inv = 10000.0 ** (-torch.arange(0, case["rot"], 2, dtype=torch.float64, device=DEV) / case["rot"])
+        ang = torch.arange(s.max_kv, dtype=torch.float64, device=DEV)[:, None] * inv
+        s.cos_sin = torch.cat((ang.cos(), ang.sin()), 1).to(torch.float32).contiguous()
+    # buffers that a caller keeps from step to step
+    s.q_rot = torch.empty(T, hq, d, dtype=torch.bfloat16, device=DEV)
+    s.out = torch.empty_like(s.q_rot)
+    s.lse = torch.empty(T, hq, dtype=torch.float32, device=DEV)
+    s.k_back, s.v_back = (torch.empty(T, hkv, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    if own:
+        _plan(s)
+    return s
+
+
+def _plan(s):
+    """The engine's handle of this batch, made once a step and used by every layer."""
+    from paged_variable_length_gb300 import pva
+
+    c = s.case
+    dtype = {"bf16": pva.KV_BF16, "e4m3": pva.KV_E4M3, "mxfp4": pva.KV_MXFP4}[c["pool"]]
+    s.engine = pva.PagedAttention(c["hq"], c["hkv"], c["d"], c["ps"], s.pages, max_batch=c["b"], max_tokens=s.T,
+                                  max_kv_len=s.max_kv, device=DEV, kv_dtype=dtype)
+    if c["rot"]:
+        s.rope = pva.Rope(s.cos_sin, rot_dim=c["rot"], interleaved=c["inter"])
+    # attend: every key lies in the pool already, so no new token is stored
+    s.skip = torch.full((s.T,), -1, dtype=torch.int64, device=DEV) if c["kind"] == "attend" else None
+    s.engine.prepare(s.cu, s.cache_seqlens, s.table, s.T, slot_mapping=s.skip, max_q_len=s.max_q)
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(s):
+    kind, pool = s.case["kind"], s.case["pool"]
+    if kind == "append":
+        if own:
+            s.engine.append(s.q, s.k, s.v, s.k_pool, s.v_pool, s.rope, q_out=s.q_rot, k_scale=s.k_scale,
+                            v_scale=s.v_scale)
+        else:
+            _append(s)
+        return {"q": s.q_rot, **_kept(s)}
+    if kind == "store":
+        if own:
+            s.engine.store(s.k, s.v, s.k_pool, s.v_pool)
+        else:
+            s.k_pool[s.slots], s.v_pool[s.slots] = _pack(s.k.float(), s.case), _pack(s.v.float(), s.case)
+        return _kept(s)
+    if kind == "attend":
+        if own:
+            s.engine.forward(s.q, s.k, s.v, s.k_pool, s.v_pool, out=s.out, lse=s.lse)
+            return {"out": s.out, "lse": s.lse}
+        return _attend(s, s.q)
+    if own:
+        s.engine.forward(s.q, s.k, s.v, s.k_pool, s.v_pool, out=s.out, lse=s.lse, k_scale=s.k_scale,
+                         v_scale=s.v_scale, rope=s.rope, q_rot=s.q_rot)
+        got = {"out": s.out, "lse": s.lse}
+    else:
+        _append(s)
+        got = _attend(s, s.q_rot)
+    return {"q": s.q_rot, **got, **_kept(s)}
+
+
+def _kept(s):
+    """The pool after the call: itself, or for the 4-bit pool the new rows' values."""
+    if s.case["pool"] == "bf16":
+        return {"k": s.k_pool, "v": s.v_pool}
+    if s.case["pool"] == "e4m3":
+        return {"k": s.k_pool.view(torch.float8_e4m3fn), "v": s.v_pool.view(torch.float8_e4m3fn)}
+    if own:
+        s.engine.load(s.k_pool, s.v_pool, k=s.k_back, v=s.v_back)
+        return {"k": s.k_back, "v": s.v_back}
+    return {"k": _unpack(s.k_pool[s.slots], s.case).to(torch.bfloat16),
+            "v": _unpack(s.v_pool[s.slots], s.case).to(torch.bfloat16)}
+
+
+def _rotate(x, s):
+    rot = s.case["rot"]
+    x = x.float()
+    cs = s.cos_sin[s.pos]
+    c, sn = cs[:, None, :rot // 2], cs[:, None, rot // 2:]
+    y = x.clone()
+    if s.case["inter"]:
+        a, b = x[..., 0:rot:2], x[..., 1:rot:2]
+        y[..., 0:rot:2], y[..., 1:rot:2] = a * c - b * sn, b * c + a * sn
+    else:
+        a, b = x[..., :rot // 2], x[..., rot // 2:rot]
+        y[..., :rot // 2], y[..., rot // 2:rot] = a * c - b * sn, b * c + a * sn
+    return y
+
+
+def _append(s):
+    pool = s.case["pool"]
+    s.q_rot.copy_(_rotate(s.q, s))
+    k, v = _rotate(s.k, s), s.v.float()
+    if pool == "bf16":
+        s.k_pool[s.slots], s.v_pool[s.slots] = k.to(torch.bfloat16), s.v
+    elif pool == "e4m3":
+        enc = lambda x, sc: (x / sc[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        s.k_pool[s.slots], s.v_pool[s.slots] = enc(k, s.k_scale), enc(v, s.v_scale)
+    else:
+        s.k_pool[s.slots], s.v_pool[s.slots] = _pack(k, s.case), _pack(v, s.case)
+
+
+def _attend(s, q):
+    """Softmax attention of every request at once, padded to the longest, in fp32."""
+    c = s.case
+    hq, hkv, d, ps = c["hq"], c["hkv"], c["d"], c["ps"]
+    j = torch.arange(s.max_kv, device=DEV)
+    held = j < s.kv_lens[:, None]                                                     # [B, L]
+    at = torch.where(held, s.table.long()[:, j // ps] * ps + j % ps, 0)
+    if c["pool"] == "bf16":
+        k, v = s.k_pool[at].float(), s.v_pool[at].float()
+    elif c["pool"] == "e4m3":
+        val = lambda p, sc: p[at].view(torch.float8_e4m3fn).float() * sc[:, None]
+        k, v = val(s.k_pool, s.k_scale), val(s.v_pool, s.v_scale)
+    else:
+        k, v = _unpack(s.k_pool[at], c), _unpack(s.v_pool[at], c)
+    v = torch.where(held[:, :, None, None], v, 0.0)                                   # [B, L, Hkv, D]
+    i = torch.arange(s.max_q, device=DEV)
+    tok = torch.where(i < s.q_lens[:, None], s.cu[:-1].long()[:, None] + i, 0)
+    qp = q[tok].float().reshape(c["b"], s.max_q, hkv, hq // hkv, d)
+    x = torch.einsum("bnhgd,blhd->bhngl", qp, k) * (1.0 / math.sqrt(d))
+    seen = held[:, None, :] & (j <= (s.kv_lens - s.q_lens)[:, None, None] + i[:, None])  # [B, n, L]
+    x = torch.where(seen[:, None, :, None, :], x, -math.inf)
+    m = x.amax(-1, keepdim=True)
+    m = torch.where(m == -math.inf, 0.0, m)
+    p = torch.exp(x - m)
+    l = p.sum(-1, keepdim=True)
+    o = torch.einsum("bhngl,blhd->bhngd", p, v) / l
+    o = o.permute(0, 2, 1, 3, 4).reshape(c["b"], s.max_q, hq, d)[s.req, s.row]
+    lse = (m + torch.log(l))[..., 0].permute(0, 2, 1, 3).reshape(c["b"], s.max_q, hq)[s.req, s.row]
+    return {"out": o.to(torch.bfloat16), "lse": lse}
+
+
+# ------------------------------------------------------------------ the definition, in 64 bits
+
+def _grid4(x):
+    """float64 [N, H, D] -> the MXFP4 values nearest to it, block by block."""
+    y = x.reshape(x.shape[0], x.shape[1], -1, 32)
+    top = y.abs().amax(3, keepdim=True)
+    exp2 = torch.floor(torch.log2(top.clamp(min=2.0 ** -200))) - 2
+    exp2 = exp2.clamp(E_LO - 127, E_HI - 127)
+    unit = y / 2.0 ** exp2
+    mag = unit.abs().clamp(max=6.0)
+    step = torch.where(mag < 2, 0.5, torch.where(mag < 4, 1.0, 2.0))
+    mag = (torch.round(mag / step) * step).clamp(max=6.0)
+    return (torch.sign(unit) * mag * 2.0 ** exp2).reshape(x.shape)
+
+
+def _grid8(x):
+    """float64 -> the E4M3 values nearest to it (saturating)."""
+    a = x.abs()
+    step = 2.0 ** (torch.floor(torch.log2(a.clamp(min=2.0 ** -6))).clamp(-6, 8) - 3)
+    return torch.sign(x) * (torch.round(a / step) * step).clamp(max=448.0)
+
+
+def _turn(x, s):
+    """Each pair as a complex number, times e^(i angle)."""
+    rot = s.case["rot"]
+    w = torch.complex(s.cos_sin[s.pos, :rot // 2].double(), s.cos_sin[s.pos, rot // 2:].double())[:, None]
+    x = x.double()
+    head, tail = x[..., :rot], x[..., rot:]
+    if s.case["inter"]:
+        z = torch.view_as_complex(head.reshape(*head.shape[:-1], rot // 2, 2).contiguous()) * w
+        head = torch.view_as_real(z).reshape(head.shape)
+    else:
+        z = torch.complex(*(h.contiguous() for h in head.chunk(2, -1))) * w
+        head = torch.cat((z.real, z.imag), -1)
+    return torch.cat((head, tail), -1)
+
+
+def _values(rows, which, s):
+    """Pool rows (K: which 0, V: 1) as float64 [N, Hkv, D]."""
+    hkv, d, pool = s.case["hkv"], s.case["d"], s.case["pool"]
+    if pool == "bf16":
+        return rows.double()
+    if pool == "e4m3":
+        return rows.view(torch.float8_e4m3fn).double() * (s.v_scale if which else s.k_scale).double()[:, None]
+    n = rows.shape[0]
+    code = rows[:, :hkv * d // 2].long()
+    code = torch.stack((code % 16, code // 16), 2).reshape(n, hkv, d // 32, 32)
+    mag, ee = code % 8, (code % 8) // 2
+    val = torch.where(ee > 0, (2.0 + mag % 2) * 2.0 ** (ee - 2).double(), 0.5 * (mag % 2).double())
+    scale = 2.0 ** (rows[:, hkv * d // 2:hkv * d // 2 + hkv * d // 32].double() - 127).reshape(n, hkv, d // 32, 1)
+    return (torch.where(code >= 8, -val, val) * scale).reshape(n, hkv, d)
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = was
+    kind, pool, ps = case["kind"], case["pool"], case["ps"]
+    got = {}
+    q, new = s.q.double(), None
+    if kind != "attend":
+        k = _turn(s.k, s) if case["rot"] else s.k.double()
+        v = s.v.double()
+        if pool == "mxfp4":
+            new = (_grid4(k), _grid4(v))
+            got["k"], got["v"] = new
+        else:
+            if pool == "e4m3":
+                k, v = _grid8(k / s.k_scale.double()[:, None]), _grid8(v / s.v_scale.double()[:, None])
+                new = (k * s.k_scale.double()[:, None], v * s.v_scale.double()[:, None])
+                whole = lambda p: p.view(torch.float8_e4m3fn).double()
+            else:
+                new, whole = (k, v), lambda p: p.double()
+            got["k"], got["v"] = whole(s.k_pool), whole(s.v_pool)
+            got["k"][s.slots], got["v"][s.slots] = k, v
+    if kind in ("append", "step"):
+        q = got["q"] = _turn(s.q, s)
+    if kind in ("append", "store"):
+        return got
+    # the attention, request by request; a step reads its own new rows as the pool would hold them
+    hq, hkv, d = case["hq"], case["hkv"], case["d"]
+    if kind == "step":
+        # what the pool holds is rounded: from the rotated values in the pool's type
+        q = q.to(torch.bfloat16).double()
+        if pool == "bf16":
+            new = tuple(x.to(torch.bfloat16).double() for x in new)
+    out, lse = torch.empty(s.T, hq, d, dtype=torch.float64, device=DEV), torch.empty(s.T, hq, dtype=torch.float64, device=DEV)
+    qs, kvs = s.q_lens.tolist(), s.kv_lens.tolist()
+    t = 0
+    for b, (n, L) in enumerate(zip(qs, kvs)):
+        pos = torch.arange(L, device=DEV)
+        at = s.table[b].long()[pos // ps] * ps + pos % ps
+        keys, vals = _values(s.k_pool[at], 0, s), _values(s.v_pool[at], 1, s)
+        if new is not None:
+            keys[L - n:], vals[L - n:] = new[0][t:t + n], new[1][t:t + n]
+        hidden = pos[None, :] > (L - n) + torch.arange(n, device=DEV)[:, None]
+        for h in range(hkv):
+            g = hq // hkv
+            x = q[t:t + n, h * g:(h + 1) * g].reshape(n * g, d) @ keys[:, h].T / math.sqrt(d)
+            x = x.masked_fill(hidden.repeat_interleave(g, 0), -math.inf)
+            lse[t:t + n, h * g:(h + 1) * g] = torch.logsumexp(x, 1).reshape(n, g)
+            out[t:t + n, h * g:(h + 1) * g] = (torch.softmax(x, 1) @ vals[:, h]).reshape(n, g, d)
+        t += n
+    got["out"], got["lse"] = out, lse
+    return got
