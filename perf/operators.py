@@ -131,24 +131,32 @@ def _quantise(x):
     return code.reshape(x.shape).to(torch.uint8), e
 
 
+def _groups(case):
+    """Head groups of a pool row: (groups, heads in each); a group's codes come before its scales."""
+    per = min(case["hkv"], 8)
+    return case["hkv"] // per, per
+
+
 def _pack(x, case):
     """fp32 rows [N, Hkv, D] -> pool rows uint8 [N, row_bytes]."""
     code, e = _quantise(x)
-    rows = torch.zeros(x.shape[0], _row_bytes(case), dtype=torch.uint8, device=x.device)
-    half = case["hkv"] * case["d"] // 2
-    rows[:, :half] = (code[..., 0::2] | (code[..., 1::2] << 4)).reshape(x.shape[0], -1)
-    rows[:, half:half + case["hkv"] * case["d"] // 32] = e.to(torch.uint8).reshape(x.shape[0], -1)
+    (gs, per), n = _groups(case), x.shape[0]
+    rows = torch.zeros(n, _row_bytes(case), dtype=torch.uint8, device=x.device)
+    codes = (code[..., 0::2] | (code[..., 1::2] << 4)).reshape(n, gs, per * case["d"] // 2)
+    both = torch.cat((codes, e.to(torch.uint8).reshape(n, gs, per * case["d"] // 32)), 2).reshape(n, -1)
+    rows[:, :both.shape[1]] = both
     return rows
 
 
 def _unpack(rows, case):
     """Pool rows uint8 [..., row_bytes] -> fp32 [..., Hkv, D]."""
     hkv, d = case["hkv"], case["d"]
-    half, lead = hkv * d // 2, rows.shape[:-1]
+    (gs, per), lead = _groups(case), rows.shape[:-1]
     table = torch.tensor(LEVELS + tuple(-v for v in LEVELS), dtype=torch.float32, device=rows.device)
-    byte = rows[..., :half].to(torch.int32)
+    both = rows[..., :hkv * (d // 2 + d // 32)].reshape(*lead, gs, -1)
+    byte = both[..., :per * d // 2].to(torch.int32)
     x = torch.stack((table[byte & 15], table[byte >> 4]), -1).reshape(*lead, hkv, d // 32, 32)
-    e = rows[..., half:half + hkv * d // 32].to(torch.int32).reshape(*lead, hkv, d // 32, 1)
+    e = both[..., per * d // 2:].to(torch.int32).reshape(*lead, hkv, d // 32, 1)
     return torch.ldexp(x, e - 127).reshape(*lead, hkv, d)
 
 
@@ -396,11 +404,14 @@ def _values(rows, which, s):
     if pool == "e4m3":
         return rows.view(torch.float8_e4m3fn).double() * (s.v_scale if which else s.k_scale).double()[:, None]
     n = rows.shape[0]
-    code = rows[:, :hkv * d // 2].long()
+    parts = [rows[:, i * 8 * (d // 2 + d // 32):] for i in range(max(1, hkv // 8))]      # eight heads at a time
+    h = min(hkv, 8)
+    code = torch.cat([x[:, :h * d // 2] for x in parts], 1).long()
     code = torch.stack((code % 16, code // 16), 2).reshape(n, hkv, d // 32, 32)
     mag, ee = code % 8, (code % 8) // 2
     val = torch.where(ee > 0, (2.0 + mag % 2) * 2.0 ** (ee - 2).double(), 0.5 * (mag % 2).double())
-    scale = 2.0 ** (rows[:, hkv * d // 2:hkv * d // 2 + hkv * d // 32].double() - 127).reshape(n, hkv, d // 32, 1)
+    scale = torch.cat([x[:, h * d // 2:h * d // 2 + h * d // 32] for x in parts], 1)
+    scale = 2.0 ** (scale.double() - 127).reshape(n, hkv, d // 32, 1)
     return (torch.where(code >= 8, -val, val) * scale).reshape(n, hkv, d)
 
 
