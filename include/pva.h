@@ -92,6 +92,7 @@ typedef enum pva_status {
 #define PVA_DEVERR_SLOT       0x08u  /* a slot_mapping entry lies outside [-1, num_pages * page_size) */
 #define PVA_DEVERR_LIMITS     0x10u  /* batch exceeds cfg.max_batch / max_tokens / max_kv_len or the max_q_len hint */
 #define PVA_DEVERR_TIMEOUT    0x20u  /* a bounded wait inside a kernel gave up (internal error) */
+#define PVA_DEVERR_POSITION   0x40u  /* a token's rotary position lies outside [0, max_positions) */
 
 /*
  * Element type of the paged KV pool (pva_config.kv_dtype).  The pages name the
@@ -103,6 +104,22 @@ typedef enum pva_status {
  */
 #define PVA_KV_BF16 0
 #define PVA_KV_E4M3 1
+/*
+ * The 4-bit pool is MXFP4 of the OCP microscaling formats: blocks of 32 consecutive elements
+ * of one head, each element an E2M1 code (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6), each block
+ * with one E8M0 byte e, the power of two 2^(e - 127) that multiplies its codes.  k_pool and
+ * v_pool are uint8 [num_pages * page_size, attn_mxfp4_row_bytes(Hkv, D)].  A slot's row holds
+ * its heads in groups of hb = min(Hkv, 8); a group is hb * D/2 bytes of codes (head by head,
+ * element 2i in the low nibble of byte i, 2i + 1 in the high one), then hb * D/32 scale bytes
+ * (head by head); the row is padded to a multiple of 16 bytes, and the padding is never
+ * looked at.  Storing a block of largest magnitude a sets its scale to 2^(floor(log2 a) - 2),
+ * held to [2^-22, 2^13], and its codes to the nearest E2M1 value of x / scale, ties to the
+ * even code; magnitudes above 6 * scale saturate (so those above 49152 do in any case, and
+ * those below 2^-24 become 0).  A block with an infinity or a NaN is stored as e = 255 with
+ * codes 0, and all its elements read as NaN.  Rows written by others may be read as long as
+ * they keep to these scales.
+ */
+#define PVA_KV_MXFP4 2
 
 /*
  * Static description of the model's attention layer and of the largest batch
@@ -121,7 +138,7 @@ typedef struct pva_config {
     int32_t enable_split_kv;    /* nonzero: split long KV ranges over several CTAs (LSE combine) */
     int32_t enable_cascade;     /* nonzero: read prefixes shared by several decodes once */
     int32_t min_cascade_pages;  /* shortest shared prefix (in pages) worth a cascade pass; <= 0 -> 8 */
-    int32_t kv_dtype;           /* PVA_KV_BF16 (0) or PVA_KV_E4M3: the pool element type */
+    int32_t kv_dtype;           /* PVA_KV_BF16 (0), PVA_KV_E4M3 or PVA_KV_MXFP4: the pool element type */
 } pva_config;
 
 /*
@@ -267,6 +284,74 @@ PVA_API pva_status attn_forward_fp8kv(const pva_meta* meta, const void* q, const
 /* store_kvcache alone into an E4M3 pool (the quantisation of attn_forward_fp8kv). */
 PVA_API pva_status attn_store_kvcache_fp8kv(const pva_meta* meta, const void* k, const void* v, void* k_pool,
                                     void* v_pool, const float* k_scale, const float* v_scale, void* stream);
+
+/*
+ * attn_forward for an MXFP4 pool (PVA_KV_MXFP4 above; the meta must come from a config with
+ * that kv_dtype, and the other forwards refuse it, with PVA_ERR_INVALID_ARG).
+ *   k_pool, v_pool  uint8 [num_pages * page_size, attn_mxfp4_row_bytes], 16-byte aligned,
+ *                   updated in place (a new token's row is written whole but for its padding)
+ *   q, k, v, out, lse as for attn_forward
+ * Attention reads each element as code * scale, otherwise exactly as attn_forward.  The new
+ * tokens' own keys and values are read back from the pool, quantised like all others.
+ */
+PVA_API pva_status attn_forward_mxfp4kv(const pva_meta* meta, const void* q, const void* k, const void* v, void* k_pool,
+                                void* v_pool, void* out, float* lse, void* stream);
+
+/* store_kvcache alone into an MXFP4 pool. */
+PVA_API pva_status attn_store_kvcache_mxfp4kv(const pva_meta* meta, const void* k, const void* v, void* k_pool,
+                                      void* v_pool, void* stream);
+
+/*
+ * The inverse of attn_store_kvcache_mxfp4kv: k[t, h, :] and v[t, h, :] (bf16 [T, Hkv, D],
+ * contiguous, 16-byte aligned) receive the values that the pool holds at every new token's
+ * slot, exactly.  Tokens with slot -1 are left as they were.  With a batch whose requests
+ * have q_len = kv_len it gathers whole requests, contiguous, in order.
+ */
+PVA_API pva_status attn_load_kvcache_mxfp4kv(const pva_meta* meta, const void* k_pool, const void* v_pool, void* k,
+                                     void* v, void* stream);
+
+/* Bytes of one slot's row in an MXFP4 pool; 0 for a head layout that is not built. */
+PVA_API int64_t attn_mxfp4_row_bytes(int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * Rotary position rotation of q and k on their way to the attention and the pool.  For a
+ * token at position p and pair i < rot_dim / 2, with c = cos_sin[p][i] and
+ * s = cos_sin[p][rot_dim/2 + i], (x1, x2) becomes (x1 c - x2 s, x2 c + x1 s): fp32 products
+ * and sums, rounded once into what holds the result.  Head dims from rot_dim on pass.
+ */
+typedef struct pva_rope {
+    const float* cos_sin;       /* DEVICE fp32 [max_positions, rot_dim], 16-byte aligned: a position's
+                                   rot_dim/2 cosines, then its sines */
+    const int32_t* positions;   /* DEVICE int32 [total_tokens], or NULL: a token's position is its index
+                                   in its request (kv_len - q_len + r) */
+    int64_t ld_q, ld_k, ld_v;   /* elements between consecutive tokens of q, k and v (multiples of 8;
+                                   slices of one fused projection need no copy); heads are contiguous */
+    int32_t max_positions;
+    int32_t rot_dim;            /* a multiple of 16, at most head_dim */
+    int32_t interleaved;        /* 0: pairs (x[i], x[i + rot_dim/2]); nonzero: (x[2i], x[2i + 1]) */
+    int32_t reserved;           /* 0 */
+} pva_rope;
+
+/*
+ * store_kvcache with the rotation: q rotated into q_out (bf16 [T, Hq, D], contiguous; q itself
+ * when that is contiguous, else no byte in common with q, k or v), k rotated and stored, v
+ * stored, for every new token, into a pool of the meta's type.  q and q_out may both be NULL
+ * (k and v alone).  k_scale and v_scale as in attn_forward_fp8kv, ignored for the other types.
+ * A token whose position lies outside the table sets PVA_DEVERR_POSITION and nothing of it is
+ * written; a token with slot -1 has its q rotated and nothing stored.
+ */
+PVA_API pva_status attn_append_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k,
+                            const void* v, void* q_out, void* k_pool, void* v_pool, const float* k_scale,
+                            const float* v_scale, void* stream);
+
+/*
+ * attn_forward (of the meta's pool type) with attn_append_rope in place of its store: one
+ * layer's call from projections to attention output.  q_rot receives the rotated q (as q_out
+ * above) and is what the attention reads; out must not overlap it.
+ */
+PVA_API pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k,
+                             const void* v, void* q_rot, void* k_pool, void* v_pool, const float* k_scale,
+                             const float* v_scale, void* out, float* lse, void* stream);
 
 /*
  * Debug/test helper: synchronises the stream of the last prepare/forward on

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "mxfp4.cuh"
 #include "pva_internal.h"
 
 namespace pva {
@@ -40,7 +41,8 @@ pva_status check_config(const pva_config* c) {
     if (!decode_supported(c->num_qo_heads, c->num_kv_heads, c->head_dim)) return PVA_ERR_UNSUPPORTED;
     // the tensor-core kernel's gathers keep a slot in 32 bits (all ones marks a row not copied)
     if ((int64_t)c->num_pages * c->page_size >= ((int64_t)1 << 32)) return PVA_ERR_UNSUPPORTED;
-    if (c->kv_dtype != PVA_KV_BF16 && c->kv_dtype != PVA_KV_E4M3) return PVA_ERR_UNSUPPORTED;
+    if (c->kv_dtype != PVA_KV_BF16 && c->kv_dtype != PVA_KV_E4M3 && c->kv_dtype != PVA_KV_MXFP4)
+        return PVA_ERR_UNSUPPORTED;
     return PVA_OK;
 }
 
@@ -136,6 +138,10 @@ ForwardParams forward_params(const MetaHost* h, const void* q, const void* k, co
     fp.scale_log2 = scale * 1.4426950408889634f;
     fp.ws = h->ws;
     fp.lay = h->lay;
+    fp.kv_fp8 = h->cfg.kv_dtype == PVA_KV_E4M3 ? 1 : 0;
+    if (h->cfg.kv_dtype == PVA_KV_MXFP4) fp.mx_row_bytes = mx::row_bytes(fp.num_kv_heads, h->cfg.head_dim);
+    const int max_tok = kDecRows / fp.group;  // tokens of a decode group
+    fp.dec_rows = fp.group * (h->max_q_len < max_tok ? h->max_q_len : max_tok);
     return fp;
 }
 
@@ -246,7 +252,8 @@ pva_status prepare_in_workspace(const pva_config* cfg, const int32_t* cu_seqlens
     h.sm_count = sms;
     // requests with more than TB new tokens run on the tensor-core prefill kernel, which
     // also runs the prefix pass of shared-prefix groups
-    const bool tc_ok = prefill_supported(cfg->num_qo_heads, cfg->num_kv_heads, cfg->head_dim);
+    const bool tc_ok = prefill_supported(cfg->num_qo_heads, cfg->num_kv_heads, cfg->head_dim) &&
+                       cfg->kv_dtype != PVA_KV_MXFP4;
     h.use_prefill = (mq > TB && tc_ok) ? 1 : 0;
     h.use_cascade = (cfg->enable_cascade && tc_ok && batch >= 2 && batch <= kCascadeMaxBatch) ? 1 : 0;
     h.dec_ctas = lay.dec_ctas;  // sms x decode CTAs per SM; the plan's balanced split assumes it
@@ -327,17 +334,72 @@ pva_status attn_prepare_metadata(const pva_config* cfg, const int32_t* cu_seqlen
 namespace pva {
 namespace {
 
+// store_kvcache into a pool of the config's type.
+cudaError_t launch_store_any(const MetaHost* h, const ForwardParams& fp, cudaStream_t s) {
+    if (h->cfg.kv_dtype != PVA_KV_MXFP4) return launch_store(fp, h->cfg.head_dim, s);
+    RopeParams rp{};  // the append kernel with no q and nothing rotated
+    rp.ld_k = rp.ld_v = (int64_t)h->cfg.num_kv_heads * h->cfg.head_dim;
+    rp.row_bytes = fp.mx_row_bytes;
+    rp.batch = h->batch;
+    return launch_append(fp, rp, h->cfg.head_dim, PVA_KV_MXFP4, s);
+}
+
 pva_status store_impl(const MetaHost* h, const void* k, const void* v, void* k_pool, void* v_pool,
                       const float* k_scale, const float* v_scale, void* stream) {
     if (h->total_tokens > 0 && (k == nullptr || v == nullptr)) return PVA_ERR_INVALID_ARG;
     if (k_pool == nullptr || v_pool == nullptr) return PVA_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool)) return PVA_ERR_INVALID_ARG;
     ForwardParams fp = forward_params(h, nullptr, k, v, k_pool, v_pool, nullptr, nullptr);
-    fp.kv_fp8 = h->cfg.kv_dtype == PVA_KV_E4M3 ? 1 : 0;
     fp.k_scale = k_scale;
     fp.v_scale = v_scale;
-    if (launch_store(fp, h->cfg.head_dim, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PVA_ERR_CUDA;
+    if (launch_store_any(h, fp, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PVA_ERR_CUDA;
     return PVA_OK;
+}
+
+// Host checks of a pva_rope and the activations it goes with.
+pva_status check_rope(const MetaHost* h, const pva_rope* rope, const void* q, const void* k, const void* v,
+                      const void* q_out, const void* k_scale, const void* v_scale) {
+    if (rope == nullptr || rope->cos_sin == nullptr) return PVA_ERR_INVALID_ARG;
+    const int64_t T = h->total_tokens, Hq = h->cfg.num_qo_heads, Hkv = h->cfg.num_kv_heads, D = h->cfg.head_dim;
+    if (T > 0 && (k == nullptr || v == nullptr || (q != nullptr && q_out == nullptr))) return PVA_ERR_INVALID_ARG;
+    if (rope->max_positions <= 0 || rope->rot_dim <= 0 || rope->rot_dim > D || rope->reserved != 0)
+        return PVA_ERR_INVALID_ARG;
+    if (rope->rot_dim % 16 != 0) return PVA_ERR_UNSUPPORTED;
+    if ((q != nullptr && rope->ld_q < Hq * D) || rope->ld_k < Hkv * D || rope->ld_v < Hkv * D)
+        return PVA_ERR_INVALID_ARG;
+    if ((q != nullptr && rope->ld_q % 8 != 0) || rope->ld_k % 8 != 0 || rope->ld_v % 8 != 0) return PVA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope->cos_sin) ||
+        (reinterpret_cast<uintptr_t>(rope->positions) & 3u) != 0)
+        return PVA_ERR_INVALID_ARG;
+    if (h->cfg.kv_dtype == PVA_KV_E4M3 && (k_scale == nullptr || v_scale == nullptr)) return PVA_ERR_INVALID_ARG;
+    if (T == 0 || q == nullptr) return PVA_OK;
+    // q_out is q itself (then contiguous), or shares no byte with q, k or v
+    const uintptr_t o0 = reinterpret_cast<uintptr_t>(q_out), o1 = o0 + (uintptr_t)(T * Hq * D * 2);
+    auto overlaps = [&](const void* x, int64_t ld, int64_t heads) {
+        const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), x1 = x0 + (uintptr_t)(((T - 1) * ld + heads * D) * 2);
+        return x0 < o1 && o0 < x1;
+    };
+    const bool in_place = q == q_out && rope->ld_q == Hq * D;
+    if ((!in_place && overlaps(q, rope->ld_q, Hq)) || overlaps(k, rope->ld_k, Hkv) || overlaps(v, rope->ld_v, Hkv))
+        return PVA_ERR_INVALID_ARG;
+    return PVA_OK;
+}
+
+RopeParams rope_params(const MetaHost* h, const pva_rope* rope, const void* q, void* q_out) {
+    RopeParams rp{};
+    rp.q = static_cast<const uint16_t*>(q);
+    rp.q_out = static_cast<uint16_t*>(q_out);
+    rp.ld_q = rope->ld_q;
+    rp.ld_k = rope->ld_k;
+    rp.ld_v = rope->ld_v;
+    rp.cos_sin = rope->cos_sin;
+    rp.positions = rope->positions;
+    rp.max_positions = rope->max_positions;
+    rp.rot_dim = rope->rot_dim;
+    rp.interleaved = rope->interleaved ? 1 : 0;
+    rp.row_bytes = mx::row_bytes(h->cfg.num_kv_heads, h->cfg.head_dim);
+    rp.batch = h->batch;
+    return rp;
 }
 
 }  // namespace
@@ -357,6 +419,50 @@ pva_status attn_store_kvcache_fp8kv(const pva_meta* meta, const void* k, const v
     if (h == nullptr) return PVA_ERR_NOT_PREPARED;
     if (h->cfg.kv_dtype != PVA_KV_E4M3 || k_scale == nullptr || v_scale == nullptr) return PVA_ERR_INVALID_ARG;
     return store_impl(h, k, v, k_pool, v_pool, k_scale, v_scale, stream);
+}
+
+pva_status attn_store_kvcache_mxfp4kv(const pva_meta* meta, const void* k, const void* v, void* k_pool, void* v_pool,
+                                      void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    if (h->cfg.kv_dtype != PVA_KV_MXFP4) return PVA_ERR_INVALID_ARG;
+    return store_impl(h, k, v, k_pool, v_pool, nullptr, nullptr, stream);
+}
+
+pva_status attn_load_kvcache_mxfp4kv(const pva_meta* meta, const void* k_pool, const void* v_pool, void* k, void* v,
+                                     void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    if (h->cfg.kv_dtype != PVA_KV_MXFP4 || k_pool == nullptr || v_pool == nullptr) return PVA_ERR_INVALID_ARG;
+    if (h->total_tokens > 0 && (k == nullptr || v == nullptr)) return PVA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool)) return PVA_ERR_INVALID_ARG;
+    const ForwardParams fp = forward_params(h, nullptr, nullptr, nullptr, const_cast<void*>(k_pool),
+                                            const_cast<void*>(v_pool), nullptr, nullptr);
+    if (launch_load_mx(fp, k, v, h->cfg.head_dim, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return PVA_ERR_CUDA;
+    return PVA_OK;
+}
+
+pva_status attn_append_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k, const void* v,
+                            void* q_out, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                            void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    const pva_status st = check_rope(h, rope, q, k, v, q_out, k_scale, v_scale);
+    if (st != PVA_OK) return st;
+    if (k_pool == nullptr || v_pool == nullptr || !aligned16(k_pool) || !aligned16(v_pool)) return PVA_ERR_INVALID_ARG;
+    ForwardParams fp = forward_params(h, nullptr, k, v, k_pool, v_pool, nullptr, nullptr);
+    fp.k_scale = k_scale;
+    fp.v_scale = v_scale;
+    if (launch_append(fp, rope_params(h, rope, q, q_out), h->cfg.head_dim, h->cfg.kv_dtype,
+                      static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return PVA_ERR_CUDA;
+    return PVA_OK;
+}
+
+int64_t attn_mxfp4_row_bytes(int32_t num_kv_heads, int32_t head_dim) {
+    if (!decode_supported(num_kv_heads, num_kv_heads, head_dim)) return 0;
+    return mx::row_bytes(num_kv_heads, head_dim);
 }
 
 pva_status attn_prepare_metadata_static(const pva_config* cfg, const int32_t* cu_seqlens_q,
@@ -402,8 +508,10 @@ pva_status attn_prepare_metadata_static(const pva_config* cfg, const int32_t* cu
 namespace pva {
 namespace {
 
+// With `rope`, q is rotated into q_rot (which the attention reads) and k on its way to the pool.
 pva_status forward_impl(const MetaHost* h, const void* q, const void* k, const void* v, void* k_pool, void* v_pool,
-                        const float* k_scale, const float* v_scale, void* out, float* lse, void* stream) {
+                        const float* k_scale, const float* v_scale, void* out, float* lse, void* stream,
+                        const pva_rope* rope = nullptr, void* q_rot = nullptr) {
     if (h->total_tokens > 0 && (q == nullptr || k == nullptr || v == nullptr || out == nullptr))
         return PVA_ERR_INVALID_ARG;
     if (k_pool == nullptr || v_pool == nullptr) return PVA_ERR_INVALID_ARG;
@@ -412,8 +520,7 @@ pva_status forward_impl(const MetaHost* h, const void* q, const void* k, const v
         return PVA_ERR_INVALID_ARG;
     if (h->total_tokens == 0) return PVA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ForwardParams fp = forward_params(h, q, k, v, k_pool, v_pool, out, lse);
-    fp.kv_fp8 = h->cfg.kv_dtype == PVA_KV_E4M3 ? 1 : 0;
+    ForwardParams fp = forward_params(h, rope != nullptr ? q_rot : q, k, v, k_pool, v_pool, out, lse);
     fp.k_scale = k_scale;
     fp.v_scale = v_scale;
     fp.dec_wait_late = (h->use_prefill || h->use_cascade) ? 1 : 0;
@@ -427,12 +534,16 @@ pva_status forward_impl(const MetaHost* h, const void* q, const void* k, const v
                                                         : cudaEventRecord(ev, s);
     };
     if (mark(0) != cudaSuccess) return PVA_ERR_CUDA;
-    if (launch_store(fp, h->cfg.head_dim, s) != cudaSuccess) return PVA_ERR_CUDA;
+    if ((rope != nullptr ? launch_append(fp, rope_params(h, rope, q, q_rot), h->cfg.head_dim, h->cfg.kv_dtype, s)
+                         : launch_store_any(h, fp, s)) != cudaSuccess)
+        return PVA_ERR_CUDA;
     if (mark(1) != cudaSuccess) return PVA_ERR_CUDA;
     if ((h->use_prefill || h->use_cascade) && launch_prefill(fp, h->cfg.head_dim, h->pre_ctas, s) != cudaSuccess)
         return PVA_ERR_CUDA;
     if (mark(2) != cudaSuccess) return PVA_ERR_CUDA;
-    if (launch_decode(fp, h->cfg.head_dim, h->dec_ctas, s) != cudaSuccess) return PVA_ERR_CUDA;
+    if ((h->cfg.kv_dtype == PVA_KV_MXFP4 ? launch_decode_mx(fp, h->cfg.head_dim, h->dec_ctas, s)
+                                         : launch_decode(fp, h->cfg.head_dim, h->dec_ctas, s)) != cudaSuccess)
+        return PVA_ERR_CUDA;
     if (mark(3) != cudaSuccess) return PVA_ERR_CUDA;
     if (h->use_merge && launch_merge(fp, h->cfg.head_dim, h->sm_count, s) != cudaSuccess) return PVA_ERR_CUDA;
     if (mark(4) != cudaSuccess) return PVA_ERR_CUDA;
@@ -457,6 +568,25 @@ pva_status attn_forward_fp8kv(const pva_meta* meta, const void* q, const void* k
     if (h == nullptr) return PVA_ERR_NOT_PREPARED;
     if (h->cfg.kv_dtype != PVA_KV_E4M3 || k_scale == nullptr || v_scale == nullptr) return PVA_ERR_INVALID_ARG;
     return forward_impl(h, q, k, v, k_pool, v_pool, k_scale, v_scale, out, lse, stream);
+}
+
+pva_status attn_forward_mxfp4kv(const pva_meta* meta, const void* q, const void* k, const void* v, void* k_pool,
+                                void* v_pool, void* out, float* lse, void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    if (h->cfg.kv_dtype != PVA_KV_MXFP4) return PVA_ERR_INVALID_ARG;
+    return forward_impl(h, q, k, v, k_pool, v_pool, nullptr, nullptr, out, lse, stream);
+}
+
+pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k, const void* v,
+                             void* q_rot, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                             void* out, float* lse, void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    if (h->total_tokens > 0 && (q == nullptr || q_rot == nullptr)) return PVA_ERR_INVALID_ARG;
+    const pva_status st = check_rope(h, rope, q, k, v, q_rot, k_scale, v_scale);
+    if (st != PVA_OK) return st;
+    return forward_impl(h, q, k, v, k_pool, v_pool, k_scale, v_scale, out, lse, stream, rope, q_rot);
 }
 
 pva_status attn_get_device_status(const pva_meta* meta, uint32_t* error_bits) {

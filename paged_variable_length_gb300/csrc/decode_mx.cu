@@ -1,0 +1,557 @@
+// K7: decode / small-row attention streaming an MXFP4 pool (layout: mxfp4.cuh).
+//
+// For every q head h of kv head g: S = scale q K^T over the request's keys, the bottom-right
+// causal mask, softmax, O = P V, with K and V elements code * 2^(e - 127), block by block.  The
+// plan, the split of long key ranges over CTAs and their join by log-sum-exp (merge kernel) are
+// those of the other pool types (decode.cu).
+//
+// What bounds it: a key of one kv head is D + D/16 bytes for K and V together, a quarter of a
+// bf16 pool's, so at HBM's rate an SM has to take in about four times as many elements a clock
+// (some 40) and the conversion of codes, not HBM, is what the inner loop is arranged around:
+//   * the MMAs take the keys as their 16 rows and the query rows as their 8 columns
+//     (S^T = K Q^T, O^T = V^T P^T), so that up to 8 query rows (G = 4 and one token use 4 of
+//     them) cost one n8 tile, half of what they would as the 16 rows;
+//   * codes become f16 pairs with one exact conversion per pair.  K's block scales are applied
+//     to the fp32 partial sums, block by block (4 per 32 elements of a key) rather than to the
+//     elements; V's, which belong to the contraction's index, to the f16 pairs (exact: every
+//     code * scale the store writes is an f16 value);
+//   * the head dimension may be summed in any order and the output dims may sit in any tile
+//     row, so a lane's K fragments are 4 consecutive bytes of a block (as ldmatrix gives them)
+//     and its V rows D/16 consecutive bytes of a key; two keys' V nibbles are interleaved with
+//     a bit select, so that one conversion gives the pair of keys the MMA wants;
+//   * P^T comes from S^T's accumulators by an 8x8 transpose in registers (movmatrix).
+// Each query row enters as f16 after a multiplication by the power of two that brings its
+// largest element to [1, 2) (undone in the softmax scale), so that its range is bf16's; P is
+// rounded to f16 (2^-11 of a weight, below the output's bf16 rounding; kPShift), sums are fp32.
+// Every wait is bounded, as in decode.cu.
+#include <cuda_runtime.h>
+
+#include "decode_common.cuh"
+#include "device_utils.cuh"
+#include "mxfp4.cuh"
+#include "pva_internal.h"
+
+namespace pva {
+namespace {
+
+constexpr int kMaxHeads = kDecHeadBlock;
+constexpr int kKeys = 32;  // keys per ring stage
+constexpr int kMT = kKeys / 16;
+constexpr float kLn2 = 0.69314718055994530942f;
+// P enters its f16 operand as 2^15 times the weight: the largest weight (1) stays below f16's
+// maximum, and weights down to 2^-29 of it keep all of f16's bits.
+constexpr float kPShift = 15.f;
+
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// (a & m) | (b & ~m)
+__device__ __forceinline__ uint32_t bitsel(uint32_t a, uint32_t b, uint32_t m) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
+    return r;
+}
+
+// NQ: n8 tiles of query rows (rows of the batch's decode groups <= 8 NQ).
+template <int D, int NQ>
+__global__ void __launch_bounds__(32 * (kMaxHeads + 1), 1)
+    decode_mx_kernel(const ForwardParams p, const int stages, const int stride) {
+    constexpr int NB = D / mx::kBlock;  // blocks of a head
+    constexpr int OT = D / 16;          // m16 tiles of the output dims
+    constexpr int VW = D / 64;          // words of a lane's run of V codes (D/8 dims)
+    extern __shared__ __align__(128) uint8_t smem[];
+    DecSmemHead* sh = reinterpret_cast<DecSmemHead*>(smem);
+    uint8_t* ring = smem + ((sizeof(DecSmemHead) + 127) / 128) * 128;
+    PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
+    uint32_t* err = &hdr->error_bits;
+    const uint64_t wlim = dev::wait_limit(hdr->wait_override);
+
+    const int Hkv = p.num_kv_heads, G = p.group, Hq = p.num_qo_heads;
+    const int HB = Hkv < kMaxHeads ? Hkv : kMaxHeads;
+    const int n_hb = Hkv / HB;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stage_bytes = 2 * kKeys * stride;
+    dev::grid_dep_launch();
+    // grid order and waits: as in decode.cu (wait_late: after a tensor-core kernel with units)
+    const int n_units = hdr->n_dec_units * n_hb;
+    const bool wait_late = p.dec_wait_late && hdr->n_pre_tiles > 0;
+    if ((hdr->error_bits & kErrFatal) || n_units == 0) {
+        dev::grid_dep_wait();
+        return;
+    }
+    const DecUnit* units = reinterpret_cast<const DecUnit*>(p.ws + p.lay.dec_units);
+    const DecGroup* dgroups = reinterpret_cast<const DecGroup*>(p.ws + p.lay.dec_groups);
+    // this CTA's share of the key line (balanced split), or a queue of units (share 0)
+    const int share = hdr->dec_share;
+    const int n_groups = hdr->n_dec_groups;
+    const int line_lo = (int)blockIdx.x * share, line_hi = line_lo + share;
+    auto piece = [&](int g, const DecGroup& dg, DecUnit& du) -> bool {
+        const int ext = dg.kv_end - dg.tail0;
+        const int a = max(dg.g0, line_lo), e = min(dg.g0 + ext, line_hi);
+        if (a >= e) return false;
+        du.group = g;
+        du.k0 = dg.tail0 + (a - dg.g0);
+        du.k1 = dg.tail0 + (e - dg.g0);
+        du.split = a == dg.g0 ? 0 : (int)blockIdx.x - dg.g0 / share;
+        du.req = dg.req;
+        du.tok0 = dg.tok0;
+        du.ntok = dg.ntok;
+        du.qpos0 = dg.qpos0;
+        du.nsplit = dg.nsplit;
+        du.pbase = dg.pbase;
+        du.nparts = dg.nparts;
+        du.pad1 = 0;
+        return true;
+    };
+    const bool static_first = !wait_late || share > 0;
+    DecUnit du_first{};
+    bool have_first = false;
+    int g_first = -1;
+    int32_t page_first_raw = 0;
+    if (static_first && warp == HB) {
+        if (share > 0) {
+            int g = reinterpret_cast<const int32_t*>(p.ws + p.lay.dec_first)[blockIdx.x];
+            if (g < n_groups) {
+                have_first = piece(g, dgroups[g], du_first);
+                if (!have_first && ++g < n_groups) have_first = piece(g, dgroups[g], du_first);
+            }
+            g_first = g;
+        } else if ((int)blockIdx.x < n_units) {
+            du_first = units[blockIdx.x / n_hb];
+            have_first = true;
+        }
+        const int key = du_first.k0 + lane;
+        if (have_first && key < du_first.k1)
+            page_first_raw = p.page_table[(int64_t)du_first.req * p.ld + (key >> p.page_shift)];
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            dev::mbar_init(&sh->full[s], 1);
+            dev::mbar_init(&sh->empty[s], HB);
+        }
+        sh->abort_flag = 0;
+        dev::fence_barrier_init();
+    }
+    __syncthreads();
+    if (!wait_late) dev::grid_dep_wait();
+
+    int32_t* sched = &hdr->pad[0];
+    const int sched_base = static_first ? (int)gridDim.x : 0;
+
+    if (warp == HB) {
+        // ================================================================ producer
+        int stage = 0;
+        uint32_t phase = 0;
+        const uint64_t policy = dev::policy_evict_first();
+        const int ps_mask = p.page_size - 1;
+        uint32_t armed = 0, armed_par = 0;
+        auto page_of = [&](const int32_t* prow, int key) -> int64_t {
+            int64_t page = prow[key >> p.page_shift];
+            if (page < 0 || page >= p.num_pages) {
+                dev::set_error(err, kErrPage);
+                page = 0;  // keep the transaction count; the result is flagged
+            }
+            return page;
+        };
+        const int r = lane;
+        int u;
+        DecUnit du{};
+        int64_t page_first = -1;
+        int g_cur = g_first;
+        if (static_first) {
+            u = have_first ? (share > 0 ? 0 : (int)blockIdx.x) : n_units;
+            if (u < n_units) {
+                du = du_first;
+                if (du.k0 + r < du.k1) {
+                    page_first = page_first_raw;
+                    if (page_first < 0 || page_first >= p.num_pages) {
+                        dev::set_error(err, kErrPage);
+                        page_first = 0;
+                    }
+                }
+            }
+        } else {
+            u = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(sched, 1) : 0, 0);
+            if (u < n_units) du = units[u / n_hb];
+        }
+        while (true) {
+            if (!warp_wait(&sh->empty[stage], phase ^ 1, wlim, sh, err)) break;
+            if (u >= n_units) {
+                if (lane == 0) {
+                    sh->info[stage].flags = kEnd;
+                    dev::mbar_arrive(&sh->full[stage]);
+                }
+                armed &= ~(1u << stage);
+                break;
+            }
+            const int hb = u % n_hb;
+            const int32_t* prow = p.page_table + (int64_t)du.req * p.ld;
+            {
+                const char* qbase = reinterpret_cast<const char*>(p.q + (int64_t)du.tok0 * Hq * D);
+                const int qbytes = du.ntok * Hq * D * 2;
+                for (int off = lane * 128; off < qbytes; off += 32 * 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(qbase + off));
+            }
+            int64_t page_next = page_first >= 0 ? page_first : ((du.k0 + r < du.k1) ? page_of(prow, du.k0 + r) : 0);
+            page_first = -1;
+            const int nst = (du.k1 - du.k0 + kKeys - 1) / kKeys;
+            int ticket = 0, u_next = n_units, g_next = g_cur;
+            DecUnit du_next{};
+            for (int si_ = 0; si_ < nst; ++si_) {
+                const int k = du.k0 + si_ * kKeys;
+                // the next unit: ticket, then its record, then its first page ids (see decode.cu)
+                if (share == 0 && si_ == max(nst - 4, 0) && lane == 0) ticket = sched_base + atomicAdd(sched, 1);
+                if (si_ == max(nst - 2, 0)) {
+                    if (share > 0) {
+                        const int gn = g_cur + 1;
+                        if (gn < n_groups && piece(gn, dgroups[gn], du_next)) {
+                            u_next = 0;
+                            g_next = gn;
+                        }
+                    } else {
+                        u_next = __shfl_sync(0xffffffffu, ticket, 0);
+                        if (u_next < n_units) du_next = units[u_next / n_hb];
+                    }
+                }
+                const int64_t page = page_next;
+                if (k + kKeys + r < du.k1) {
+                    page_next = page_of(prow, k + kKeys + r);
+                } else if (si_ == nst - 1 && u_next < n_units && du_next.k0 + r < du_next.k1) {
+                    page_first = page_of(p.page_table + (int64_t)du_next.req * p.ld, du_next.k0 + r);
+                }
+                if (si_ != 0 && !warp_wait(&sh->empty[stage], phase ^ 1, wlim, sh, err)) goto producer_done;
+                const int nk = min(kKeys, du.k1 - k);
+                if (lane == 0) {
+                    StageInfo& si = sh->info[stage];
+                    si.unit = u;
+                    si.group = du.group;
+                    si.k = k;
+                    si.k1 = du.k1;
+                    si.tok0 = du.tok0;
+                    si.ntok = du.ntok;
+                    si.qpos0 = du.qpos0;
+                    si.nsplit = du.nsplit;
+                    si.pbase = du.pbase;
+                    si.split = du.split;
+                    si.hb = hb;
+                    si.nparts = du.nparts;
+                    si.flags = (si_ == 0 ? kFirst : 0) | (si_ == nst - 1 ? kLast : 0);
+                    dev::mbar_arrive_expect_tx(&sh->full[stage], (uint32_t)(2 * nk * stride));
+                }
+                armed |= 1u << stage;
+                armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+                __syncwarp();
+                if (r < nk) {
+                    // with every head in the CTA, the rows of one page are contiguous in the pool
+                    // and in the stage: the lane of a page's first row copies them all
+                    const int in_page = (k + r) & ps_mask;
+                    const int run = n_hb == 1 ? min(p.page_size - in_page, nk - r) : 1;
+                    if (n_hb > 1 || r == 0 || in_page == 0) {
+                        const int64_t src = ((page << p.page_shift) + in_page) * p.mx_row_bytes + (int64_t)hb * stride;
+                        uint8_t* dst = ring + stage * stage_bytes + r * stride;
+                        const uint32_t bytes = (uint32_t)(run * stride);
+                        dev::bulk_g2s_hint(dst, reinterpret_cast<const uint8_t*>(p.k_pool) + src, bytes,
+                                           &sh->full[stage], policy);
+                        dev::bulk_g2s_hint(dst + kKeys * stride, reinterpret_cast<const uint8_t*>(p.v_pool) + src,
+                                           bytes, &sh->full[stage], policy);
+                    }
+                }
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            u = u_next;
+            du = du_next;
+            g_cur = g_next;
+        }
+    producer_done:
+        // every copy issued must land before the CTA may exit
+        for (int s = 0; s < stages; ++s)
+            if (armed & (1u << s)) (void)dev::mbar_wait(&sh->full[s], (armed_par >> s) & 1u);
+        if (wait_late) dev::grid_dep_wait();
+        return;
+    }
+
+    // ==================================================================== consumers
+    const int gl = warp;      // kv head within the head group
+    const int gq = lane >> 2; // MMA row group: a key of S^T, a run of dims of O^T, a query row of Q / P
+    const int cq = lane & 3;  // MMA column pair
+    uint32_t qb[NQ][NB][4];   // query rows: per block two k-steps of B fragments
+    float o[OT][NQ][4];
+    float m[NQ][2], l[NQ][2], sl[NQ][2];
+    int lim[NQ][2];
+    int stage = 0;
+    uint32_t phase = 0;
+
+    while (true) {
+        if (!warp_wait(&sh->full[stage], phase, wlim, sh, err)) return;
+        const StageInfo si = sh->info[stage];
+        if (si.flags & kEnd) break;
+        const int rows = si.ntok * G;
+        const int g = si.hb * HB + gl;
+        if (si.flags & kFirst) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                // B fragments of query row 8n + gq: block b, k-step t, columns (2cq, 2cq+1 | +8, +9) <-
+                // dims 32b + 8cq + 4t + (0, 1 | 2, 3), the order the K fragments come in
+                const int r = 8 * n + gq;
+                uint4 w[NB];
+                uint32_t amax = 0;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    w[b] = make_uint4(0, 0, 0, 0);
+                    if (r < rows)
+                        w[b] = *reinterpret_cast<const uint4*>(
+                            p.q + ((int64_t)(si.tok0 + r / G) * Hq + g * G + r % G) * D + 32 * b + 8 * cq);
+                    const uint32_t ww[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        amax = max(amax, max((ww[i] << 16) & 0x7FFFFFFFu, ww[i] & 0x7FFF0000u));
+                }
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const int ex = min(max((int)(amax >> 23), 1), 253);
+                const float f = __uint_as_float((uint32_t)(254 - ex) << 23);
+                const float qs = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t ww[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        qb[n][b][i] = dev::pack_f16x2(__uint_as_float(ww[i] << 16) * f,
+                                                      __uint_as_float(ww[i] & 0xFFFF0000u) * f);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = 2 * cq + i;  // score columns of the lane: query rows 8n + c
+                    sl[n][i] = p.scale_log2 * __shfl_sync(0xffffffffu, qs, 4 * c);
+                    m[n][i] = -INFINITY;
+                    l[n][i] = 0.f;
+                    lim[n][i] = 8 * n + c < rows ? si.qpos0 + (8 * n + c) / G : -1;
+                }
+#pragma unroll
+                for (int t = 0; t < OT; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+            }
+        }
+        const uint8_t* Ks = ring + stage * stage_bytes;
+        const uint8_t* Vs = Ks + kKeys * stride;
+
+        // ---- S^T = K Q^T, 16 keys a tile
+        float s[kMT][NQ][4];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+            const uint32_t ka = dev::smem_u32(Ks) + (mt * 16 + (lane & 15)) * stride + gl * (D / 2) + (lane >> 4) * 16;
+            const uint8_t* kr = Ks + (mt * 16 + gq) * stride + HB * (D / 2) + gl * NB;
+            uint32_t e0, e1;  // scale bytes of keys gq, gq + 8
+            if constexpr (NB == 4) {
+                e0 = *reinterpret_cast<const uint32_t*>(kr);
+                e1 = *reinterpret_cast<const uint32_t*>(kr + 8 * stride);
+            } else {
+                e0 = *reinterpret_cast<const uint16_t*>(kr);
+                e1 = *reinterpret_cast<const uint16_t*>(kr + 8 * stride);
+            }
+#pragma unroll
+            for (int b2 = 0; b2 < NB; b2 += 2) {
+                uint32_t w[2][2];  // [block][keys 0-7 | 8-15]
+                dev::ldsm_x4(ka + b2 * 16, w[0][0], w[0][1], w[1][0], w[1][1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int b = b2 + i;
+                    const uint32_t a0[4] = {mx::e2m1x2_to_f16x2<0>(w[i][0]), mx::e2m1x2_to_f16x2<0>(w[i][1]),
+                                            mx::e2m1x2_to_f16x2<1>(w[i][0]), mx::e2m1x2_to_f16x2<1>(w[i][1])};
+                    const uint32_t a1[4] = {mx::e2m1x2_to_f16x2<2>(w[i][0]), mx::e2m1x2_to_f16x2<2>(w[i][1]),
+                                            mx::e2m1x2_to_f16x2<3>(w[i][0]), mx::e2m1x2_to_f16x2<3>(w[i][1])};
+                    const float f0 = mx::scale_f32((e0 >> (8 * b)) & 255u), f1 = mx::scale_f32((e1 >> (8 * b)) & 255u);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        float c[4] = {0.f, 0.f, 0.f, 0.f};
+                        dev::mma_f16_16816(c, a0, qb[n][b][0], qb[n][b][1]);
+                        dev::mma_f16_16816(c, a1, qb[n][b][2], qb[n][b][3]);
+                        if (b == 0) {
+                            s[mt][n][0] = c[0] * f0, s[mt][n][1] = c[1] * f0;
+                            s[mt][n][2] = c[2] * f1, s[mt][n][3] = c[3] * f1;
+                        } else {
+                            s[mt][n][0] += c[0] * f0, s[mt][n][1] += c[1] * f0;
+                            s[mt][n][2] += c[2] * f1, s[mt][n][3] += c[3] * f1;
+                        }
+                    }
+                }
+            }
+        }
+
+        // ---- scale, mask (range end and causal diagonal), online softmax
+        uint32_t pb[kMT][NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float al[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int last = min(lim[n][i], si.k1 - 1);  // last key the row sees here
+                float mx = -INFINITY;
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = si.k + mt * 16 + 8 * h + gq;
+                        float x = s[mt][n][2 * h + i] * sl[n][i];
+                        if (key > last) x = -INFINITY;
+                        s[mt][n][2 * h + i] = x;
+                        mx = fmaxf(mx, x);
+                    }
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float mn = fmaxf(m[n][i], mx);
+                const float mu = mn == -INFINITY ? 0.f : mn;
+                al[i] = dev::fast_exp2(m[n][i] - mu);
+                m[n][i] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float e = dev::fast_exp2(s[mt][n][2 * h + i] - (mu - kPShift));
+                        s[mt][n][2 * h + i] = e;
+                        sum += e;
+                    }
+                }
+                l[n][i] = l[n][i] * al[i] + sum;
+            }
+#pragma unroll
+            for (int t = 0; t < OT; ++t) {
+                o[t][n][0] *= al[0], o[t][n][1] *= al[1];
+                o[t][n][2] *= al[0], o[t][n][3] *= al[1];
+            }
+            // (key gq, rows 2cq, 2cq+1) -> (row gq, keys 2cq, 2cq+1)
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+                pb[mt][n][0] = movmatrix_t(dev::pack_f16x2(s[mt][n][0], s[mt][n][1]));
+                pb[mt][n][1] = movmatrix_t(dev::pack_f16x2(s[mt][n][2], s[mt][n][3]));
+            }
+        }
+
+        // ---- O^T += V^T P^T: the lane's keys 2cq, 2cq+1 | 2cq+8, 2cq+9, dims gq*D/8 .. +D/8-1
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+            uint32_t vw[4][VW], ve[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int kk = mt * 16 + 2 * cq + (i & 1) + (i >> 1) * 8;
+                const uint8_t* vr = Vs + kk * stride;
+                if constexpr (VW == 2) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(vr + gl * (D / 2) + gq * (D / 16));
+                    vw[i][0] = w.x, vw[i][1] = w.y;
+                } else {
+                    vw[i][0] = *reinterpret_cast<const uint32_t*>(vr + gl * (D / 2) + gq * (D / 16));
+                }
+                // a row past the range's end holds what an earlier stage left: scale 0 (its P is 0)
+                ve[i] = si.k + kk < si.k1 ? vr[HB * (D / 2) + gl * NB + gq * (D / 8) / mx::kBlock] : 0u;
+            }
+            const uint32_t f01 = dev::pack_f16x2(mx::scale_f32(ve[0]), mx::scale_f32(ve[1]));
+            const uint32_t f89 = dev::pack_f16x2(mx::scale_f32(ve[2]), mx::scale_f32(ve[3]));
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                // bytes (dim 2i: x, dim 2i + 1: y) holding two keys' codes
+                const uint32_t x01 = bitsel(vw[0][w], vw[1][w] << 4, 0x0F0F0F0Fu);
+                const uint32_t y01 = bitsel(vw[0][w] >> 4, vw[1][w], 0x0F0F0F0Fu);
+                const uint32_t x89 = bitsel(vw[2][w], vw[3][w] << 4, 0x0F0F0F0Fu);
+                const uint32_t y89 = bitsel(vw[2][w] >> 4, vw[3][w], 0x0F0F0F0Fu);
+                auto tile = [&](auto byte) {
+                    constexpr int B = decltype(byte)::value;
+                    const uint32_t a[4] = {hmul2(mx::e2m1x2_to_f16x2<B>(x01), f01), hmul2(mx::e2m1x2_to_f16x2<B>(y01), f01),
+                                           hmul2(mx::e2m1x2_to_f16x2<B>(x89), f89), hmul2(mx::e2m1x2_to_f16x2<B>(y89), f89)};
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) dev::mma_f16_16816(o[4 * w + B][n], a, pb[mt][n][0], pb[mt][n][1]);
+                };
+                tile(IntTag<0>{});
+                tile(IntTag<1>{});
+                tile(IntTag<2>{});
+                tile(IntTag<3>{});
+            }
+        }
+
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&sh->empty[stage]);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        if (!(si.flags & kLast)) continue;
+
+        // ================================================================ unit epilogue
+        // dim gq*D/8 + 2t (+1) of query row 8n + 2cq + i: o[t][n][i] (o[t][n][2 + i])
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float lt = l[n][i];
+                lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+                lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+                lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+                const int r = 8 * n + 2 * cq + i;
+                if (r >= rows) continue;
+                const float inv = lt > 0.f ? 1.f / lt : lt;  // (a NaN stays one)
+                const float lse = lt > 0.f ? m[n][i] + (__log2f(lt) - kPShift) : (lt == 0.f ? -INFINITY : lt);  // log2 domain
+                if (si.nparts == 1) {
+                    const int64_t orow = (int64_t)(si.tok0 + r / G) * Hq + g * G + r % G;
+                    uint4* d4 = reinterpret_cast<uint4*>(p.out + orow * D + gq * (D / 8));
+#pragma unroll
+                    for (int t = 0; t < OT; t += 4)
+                        d4[t / 4] = make_uint4(dev::pack_bf16x2(o[t][n][i] * inv, o[t][n][2 + i] * inv),
+                                               dev::pack_bf16x2(o[t + 1][n][i] * inv, o[t + 1][n][2 + i] * inv),
+                                               dev::pack_bf16x2(o[t + 2][n][i] * inv, o[t + 2][n][2 + i] * inv),
+                                               dev::pack_bf16x2(o[t + 3][n][i] * inv, o[t + 3][n][2 + i] * inv));
+                    if (p.lse != nullptr && gq == 0) p.lse[orow] = lse * kLn2;
+                } else {
+                    // split group: fp32 partial (normalised O, log2 LSE) for the merge kernel
+                    const int64_t slot = (int64_t)(si.pbase + si.split) * p.lay.rows_per_slot;
+                    const int prow = (r / G) * Hq + g * G + r % G;
+                    float4* d4 = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.ws + p.lay.partial_o) +
+                                                           (slot + prow) * D + gq * (D / 8));
+#pragma unroll
+                    for (int t = 0; t < OT; t += 2)
+                        d4[t / 2] = make_float4(o[t][n][i] * inv, o[t][n][2 + i] * inv, o[t + 1][n][i] * inv,
+                                                o[t + 1][n][2 + i] * inv);
+                    if (gq == 0) reinterpret_cast<float*>(p.ws + p.lay.partial_lse)[slot + prow] = lse;
+                }
+            }
+        }
+    }
+}
+
+template <int D, int NQ>
+cudaError_t launch_q(const ForwardParams& p, int ctas, cudaStream_t s) {
+    const int hb = p.num_kv_heads < kMaxHeads ? p.num_kv_heads : kMaxHeads;
+    // with all heads in the CTA a stage's rows are laid out as the pool's, padding included
+    const int stride = p.num_kv_heads > kMaxHeads ? mx::group_bytes(p.num_kv_heads, D) : p.mx_row_bytes;
+    const int head = (int)((sizeof(DecSmemHead) + 127) / 128 * 128);
+    const int stage_bytes = 2 * kKeys * stride;
+    int stages = (220 * 1024 / decode_ctas_per_sm(p.num_kv_heads, D) - 1024 - head) / stage_bytes;
+    stages = stages < 2 ? 2 : (stages > 8 ? 8 : stages);
+    const size_t smem = (size_t)head + (size_t)stages * stage_bytes;
+    const cudaError_t e =
+        cudaFuncSetAttribute(decode_mx_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_programmatic(decode_mx_kernel<D, NQ>, (unsigned)ctas, 32u * (hb + 1), smem, s, p, stages, stride);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s) {
+    if (head_dim == 128) return p.dec_rows <= 8 ? launch_q<128, 1>(p, ctas, s) : launch_q<128, 2>(p, ctas, s);
+    if (head_dim == 64) return p.dec_rows <= 8 ? launch_q<64, 1>(p, ctas, s) : launch_q<64, 2>(p, ctas, s);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pva

@@ -1,0 +1,102 @@
+// MXFP4 pool rows: the layout, and the conversions of its elements and block scales.
+//
+// A block is 32 consecutive elements of one head: 32 E2M1 codes (sign, 2 exponent bits, 1
+// mantissa bit; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one E8M0 byte e, the power of two
+// 2^(e - 127) that multiplies them (e = 255: NaN), as the OCP microscaling formats define them.
+// A slot's row (one for K, one for V) holds its heads in groups of hb = min(Hkv, 8):
+//   [hb * D/2 bytes of codes, element 2i in the low nibble | hb * D/32 scale bytes]
+// and is padded to a multiple of 16 bytes, so that any run of consecutive slots is one bulk
+// copy and a decode CTA's head group is one contiguous piece of a row.
+#pragma once
+
+#include <cstdint>
+
+#ifdef __CUDACC__
+#include "device_utils.cuh"
+#endif
+
+namespace pva {
+namespace mx {
+
+constexpr int kBlock = 32;
+// Block scales that the store writes: 2^-22 .. 2^13.  Every code times such a scale is an f16
+// value, which is what the MMAs of the attention kernels take.
+constexpr int kScaleLo = 105, kScaleHi = 140, kScaleNan = 255;
+
+#ifdef __CUDACC__
+#define PVA_HD __host__ __device__
+#else
+#define PVA_HD
+#endif
+
+// Bytes of one head group's codes and scales in a row.
+PVA_HD inline int group_bytes(int num_kv_heads, int D) {
+    const int hb = num_kv_heads < 8 ? num_kv_heads : 8;
+    return hb * (D / 2 + D / kBlock);
+}
+
+PVA_HD inline int row_bytes(int num_kv_heads, int D) {
+    const int hb = num_kv_heads < 8 ? num_kv_heads : 8;
+    const int raw = num_kv_heads / hb * group_bytes(num_kv_heads, D);
+    return (raw + 15) / 16 * 16;
+}
+
+// Byte offsets of head h's codes and scales inside a row.
+PVA_HD inline int codes_at(int h, int num_kv_heads, int D) {
+    const int hb = num_kv_heads < 8 ? num_kv_heads : 8;
+    return h / hb * group_bytes(num_kv_heads, D) + h % hb * (D / 2);
+}
+PVA_HD inline int scales_at(int h, int num_kv_heads, int D) {
+    const int hb = num_kv_heads < 8 ? num_kv_heads : 8;
+    return h / hb * group_bytes(num_kv_heads, D) + hb * (D / 2) + h % hb * (D / kBlock);
+}
+
+#ifdef __CUDACC__
+
+// The two codes of byte I of x -> an f16 pair (low nibble -> low half).  Exact.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t x) {
+    uint32_t r;
+    if constexpr (I == 0)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(x));
+    else if constexpr (I == 1)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(x));
+    else if constexpr (I == 2)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(x));
+    else
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Two fp32 -> two codes in one byte (lo in the low nibble): nearest, ties to even, magnitudes
+// above 6 saturate.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\t.reg .b16 u;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tmov.b16 u, {t, 0};\n\t"
+        "cvt.u32.u16 %0, u;\n\t}"
+        : "=r"(r)
+        : "f"(lo), "f"(hi));
+    return r;
+}
+
+// Scale byte -> fp32 (255 -> +inf: a NaN block's codes are stored as zeros, so that its
+// elements become 0 * inf = NaN).
+__device__ __forceinline__ float scale_f32(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Scale byte of a block whose largest magnitude has the fp32 bits `amax` (sign cleared):
+// floor(log2 amax) - 2 (the exponent of E2M1's largest binade), held to the range above; a
+// block with an infinity or a NaN is a NaN block.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+    const int e = (int)(amax >> 23);
+    return e == 255 ? kScaleNan : (uint32_t)min(max(e - 2, kScaleLo), kScaleHi);
+}
+
+// 1 / scale, the factor that takes an element to its code's range (0 for a NaN block).
+__device__ __forceinline__ float inv_scale_f32(uint32_t e) {
+    return e == kScaleNan ? 0.f : __uint_as_float((254u - e) << 23);
+}
+
+#endif  // __CUDACC__
+
+}  // namespace mx
+}  // namespace pva

@@ -45,6 +45,7 @@ constexpr uint32_t kErrPage = PVA_DEVERR_PAGE_ID;
 constexpr uint32_t kErrSlot = PVA_DEVERR_SLOT;
 constexpr uint32_t kErrLimits = PVA_DEVERR_LIMITS;
 constexpr uint32_t kErrTimeout = PVA_DEVERR_TIMEOUT;
+constexpr uint32_t kErrPosition = PVA_DEVERR_POSITION;
 // Errors that make the whole batch description untrustworthy: nothing runs.
 constexpr uint32_t kErrFatal = kErrCu | kErrQgtKv | kErrLimits;
 
@@ -236,6 +237,23 @@ struct ForwardParams {
     // then starts on SMs the tensor-core kernel has left and waits for that grid only
     // before it exits
     int32_t dec_wait_late;
+    // MXFP4 pools: bytes of a pool row (mx::row_bytes), zero for the other types
+    int32_t mx_row_bytes;
+    int32_t dec_rows;            // most query rows (tokens x G) of a decode group of this batch
+};
+
+// What the append kernel takes besides ForwardParams (by value).
+struct RopeParams {
+    const uint16_t* q;           // [T, Hq, D], ld_q elements between tokens; null: k and v alone
+    uint16_t* q_out;             // [T, Hq, D] contiguous
+    int64_t ld_q, ld_k, ld_v;
+    const float* cos_sin;        // [max_positions][rot_dim]: cos of the rot_dim / 2 angles, their sin
+    const int32_t* positions;    // [T] or null: derived from the lengths
+    int32_t max_positions;
+    int32_t rot_dim;             // 0: nothing is rotated
+    int32_t interleaved;
+    int32_t row_bytes;           // MXFP4: bytes of a pool row
+    int32_t batch;
 };
 
 // Host view of a prepared batch, stored inside pva_meta::opaque.
@@ -361,6 +379,9 @@ cudaError_t launch_prepare(const PrepareParams& p, cudaStream_t s);
 size_t prepare_smem_bytes(int smem_batch, bool cascade);
 cudaError_t launch_store(const ForwardParams& p, int head_dim, cudaStream_t s);
 cudaError_t launch_decode(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
+cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
+cudaError_t launch_append(const ForwardParams& p, const RopeParams& rp, int head_dim, int kv_dtype, cudaStream_t s);
+cudaError_t launch_load_mx(const ForwardParams& p, void* k, void* v, int head_dim, cudaStream_t s);
 cudaError_t launch_merge(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_prefill(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 bool prefill_supported(int num_qo_heads, int num_kv_heads, int head_dim);

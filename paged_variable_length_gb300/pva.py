@@ -22,12 +22,14 @@ STATUS_NAMES = {
 DEVERR = {
     0x01: "PVA_DEVERR_CU_SEQLENS", 0x02: "PVA_DEVERR_Q_GT_KV", 0x04: "PVA_DEVERR_PAGE_ID",
     0x08: "PVA_DEVERR_SLOT", 0x10: "PVA_DEVERR_LIMITS", 0x20: "PVA_DEVERR_TIMEOUT",
+    0x40: "PVA_DEVERR_POSITION",
 }
 # Every function include/pva.h declares; the CPU tests check the library exports each one.
 EXPORTS = ("attn_abi_version", "attn_status_string", "attn_workspace_size", "attn_prepare_metadata",
            "attn_forward", "attn_store_kvcache", "attn_get_device_status", "attn_debug_plan_counts",
            "attn_set_timing_events", "attn_prepare_metadata_static", "attn_forward_fp8kv", "attn_store_kvcache_fp8kv",
-           "attn_debug_set_wait_limit")
+           "attn_debug_set_wait_limit", "attn_forward_mxfp4kv", "attn_store_kvcache_mxfp4kv",
+           "attn_load_kvcache_mxfp4kv", "attn_mxfp4_row_bytes", "attn_append_rope", "attn_forward_rope")
 
 
 class PvaError(RuntimeError):
@@ -50,6 +52,15 @@ class Config(ctypes.Structure):
 class Meta(ctypes.Structure):
     """Mirror of pva_meta (opaque, caller-owned, host memory)."""
     _fields_ = [("opaque", ctypes.c_uint64 * 64)]
+
+
+class RopeArgs(ctypes.Structure):
+    """Mirror of pva_rope."""
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("ld_q", ctypes.c_int64),
+        ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("max_positions", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
 
 
 _lock = threading.Lock()
@@ -83,6 +94,18 @@ def load(path: str | None = None):
         lib.attn_forward_fp8kv.restype = ctypes.c_int
         lib.attn_store_kvcache_fp8kv.argtypes = [MP, P, P, P, P, P, P, P]
         lib.attn_store_kvcache_fp8kv.restype = ctypes.c_int
+        lib.attn_forward_mxfp4kv.argtypes = [MP, P, P, P, P, P, P, P, P]
+        lib.attn_forward_mxfp4kv.restype = ctypes.c_int
+        lib.attn_store_kvcache_mxfp4kv.argtypes = [MP, P, P, P, P, P]
+        lib.attn_store_kvcache_mxfp4kv.restype = ctypes.c_int
+        lib.attn_load_kvcache_mxfp4kv.argtypes = [MP, P, P, P, P, P]
+        lib.attn_load_kvcache_mxfp4kv.restype = ctypes.c_int
+        lib.attn_mxfp4_row_bytes.argtypes, lib.attn_mxfp4_row_bytes.restype = [i32, i32], i64
+        RP = ctypes.POINTER(RopeArgs)
+        lib.attn_append_rope.argtypes = [MP, RP, P, P, P, P, P, P, P, P, P]
+        lib.attn_append_rope.restype = ctypes.c_int
+        lib.attn_forward_rope.argtypes = [MP, RP, P, P, P, P, P, P, P, P, P, P, P]
+        lib.attn_forward_rope.restype = ctypes.c_int
         lib.attn_get_device_status.argtypes = [MP, ctypes.POINTER(ctypes.c_uint32)]
         lib.attn_get_device_status.restype = ctypes.c_int
         lib.attn_set_timing_events.argtypes = [MP, ctypes.POINTER(ctypes.c_void_p), i32]
@@ -122,7 +145,7 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-KV_BF16, KV_E4M3 = 0, 1
+KV_BF16, KV_E4M3, KV_MXFP4 = 0, 1, 2
 
 
 def make_config(num_qo_heads, num_kv_heads, head_dim, page_size, num_pages, max_batch, max_tokens, max_kv_len,
@@ -181,6 +204,102 @@ def attn_store_kvcache_fp8kv(meta: Meta, k, v, k_pool, v_pool, k_scale, v_scale,
     st = load().attn_store_kvcache_fp8kv(ctypes.byref(meta), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
                                          _ptr(k_scale), _ptr(v_scale), _stream(stream))
     _check(st, "attn_store_kvcache_fp8kv")
+
+
+def attn_forward_mxfp4kv(meta: Meta, q, k, v, k_pool, v_pool, out, lse=None, stream=None) -> None:
+    """attn_forward over MXFP4 pools (uint8 [slots, mxfp4_row_bytes] tensors)."""
+    st = load().attn_forward_mxfp4kv(ctypes.byref(meta), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
+                                     _ptr(out), _ptr(lse), _stream(stream))
+    _check(st, "attn_forward_mxfp4kv")
+
+
+def attn_store_kvcache_mxfp4kv(meta: Meta, k, v, k_pool, v_pool, stream=None) -> None:
+    st = load().attn_store_kvcache_mxfp4kv(ctypes.byref(meta), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
+                                           _stream(stream))
+    _check(st, "attn_store_kvcache_mxfp4kv")
+
+
+def attn_load_kvcache_mxfp4kv(meta: Meta, k_pool, v_pool, k, v, stream=None) -> None:
+    """The values the pools hold at the batch's new tokens' slots, into bf16 k / v [T, Hkv, D]."""
+    st = load().attn_load_kvcache_mxfp4kv(ctypes.byref(meta), _ptr(k_pool), _ptr(v_pool), _ptr(k), _ptr(v),
+                                          _stream(stream))
+    _check(st, "attn_load_kvcache_mxfp4kv")
+
+
+def mxfp4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one slot's row in an MXFP4 pool (pools: uint8 [slots, row_bytes])."""
+    n = int(load().attn_mxfp4_row_bytes(int(num_kv_heads), int(head_dim)))
+    if n == 0:
+        raise PvaError(2, "attn_mxfp4_row_bytes")
+    return n
+
+
+class Rope:
+    """A rotary position rotation: fp32 cos_sin [max_positions, rot_dim] on the device (a position's
+    cosines, then its sines; see rope_table), how elements pair, and positions (int32 [T] on the
+    device) when they are not the tokens' indices in their requests."""
+
+    def __init__(self, cos_sin, rot_dim: int | None = None, interleaved: bool = False, positions=None):
+        import torch
+
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin is a contiguous fp32 [max_positions, rot_dim] tensor")
+        if rot_dim is not None and rot_dim != cos_sin.shape[1]:
+            raise ValueError(f"cos_sin has {cos_sin.shape[1]} columns, rot_dim is {rot_dim}")
+        self.cos_sin = cos_sin
+        self.rot_dim = int(cos_sin.shape[1])
+        self.interleaved = bool(interleaved)
+        self.set_positions(positions)
+
+    def set_positions(self, positions) -> None:
+        """Explicit positions of the batch's tokens, or None."""
+        import torch
+
+        if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
+            raise ValueError("positions is a contiguous int32 tensor")
+        self.positions = positions
+
+    def args(self, q, k, v) -> RopeArgs:
+        if self.positions is not None and self.positions.numel() != k.shape[0]:
+            raise ValueError(f"{self.positions.numel()} positions for {k.shape[0]} tokens")
+        return RopeArgs(self.cos_sin.data_ptr(), None if self.positions is None else self.positions.data_ptr(),
+                        0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
+                        self.cos_sin.shape[0], self.rot_dim, int(self.interleaved), 0)
+
+
+def _token_stride(x, name: str) -> int:
+    if x.stride(2) != 1 or (x.stride(1) != x.shape[2] and x.shape[1] > 1):
+        raise ValueError(f"{name} [T, heads, D] has contiguous heads (only the token stride is free)")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """cos_sin of angles p * base^(-2i / rot_dim), formed in 64 bits (a far position's angle has lost
+    its fraction in 32), rounded once to fp32 [max_positions, rot_dim]."""
+    import torch
+
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    ang = torch.arange(max_positions, dtype=torch.float64)[:, None] * inv
+    return torch.cat((ang.cos(), ang.sin()), 1).to(torch.float32).to(device)
+
+
+def attn_append_rope(meta: Meta, rope: Rope, q, k, v, q_out, k_pool, v_pool, k_scale=None, v_scale=None,
+                     stream=None) -> None:
+    """q rotated into q_out, k rotated and stored, v stored; q, k, v may be strided by token."""
+    args = rope.args(q, k, v)
+    st = load().attn_append_rope(ctypes.byref(meta), ctypes.byref(args), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out),
+                                 _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _stream(stream))
+    _check(st, "attn_append_rope")
+
+
+def attn_forward_rope(meta: Meta, rope: Rope, q, k, v, q_rot, k_pool, v_pool, out, lse=None, k_scale=None,
+                      v_scale=None, stream=None) -> None:
+    """attn_append_rope, then the attention of the rotated q."""
+    args = rope.args(q, k, v)
+    st = load().attn_forward_rope(ctypes.byref(meta), ctypes.byref(args), _ptr(q), _ptr(k), _ptr(v), _ptr(q_rot),
+                                  _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse),
+                                  _stream(stream))
+    _check(st, "attn_forward_rope")
 
 
 def attn_get_device_status(meta: Meta) -> int:
@@ -266,19 +385,58 @@ class PagedAttention:
         """Once per batch.  The index tensors are kept referenced until the next prepare."""
         batch = int(cache_seqlens.numel())
         self._keep = (cu_seqlens_q, cache_seqlens, page_table, slot_mapping)
+        self.total_tokens = int(total_tokens)
         self.meta = attn_prepare_metadata(self.cfg, cu_seqlens_q, cache_seqlens, page_table, slot_mapping, batch,
                                           total_tokens, max_q_len, self.workspace, stream)
         return self.meta
 
-    def forward(self, q, k, v, k_pool, v_pool, out=None, lse=None, stream=None, k_scale=None, v_scale=None):
+    def forward(self, q, k, v, k_pool, v_pool, out=None, lse=None, stream=None, k_scale=None, v_scale=None,
+                rope: Rope | None = None, q_rot=None):
         """One layer.  With an E4M3 config the pools are uint8 and k_scale / v_scale (fp32 [Hkv],
-        on the device) are required."""
+        on the device) are required; with an MXFP4 config they are uint8 [slots, mxfp4_row_bytes].
+        With ``rope``, q and k are rotated by position first (q into q_rot, a new tensor when None)
+        and q, k, v may be strided by token."""
         import torch
 
         if out is None:
-            out = torch.empty_like(q)
-        if self.cfg.kv_dtype == KV_E4M3:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if rope is not None:
+            if q_rot is None:
+                q_rot = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            attn_forward_rope(self.meta, rope, q, k, v, q_rot, k_pool, v_pool, out, lse, k_scale, v_scale, stream)
+        elif self.cfg.kv_dtype == KV_E4M3:
             attn_forward_fp8kv(self.meta, q, k, v, k_pool, v_pool, k_scale, v_scale, out, lse, stream)
+        elif self.cfg.kv_dtype == KV_MXFP4:
+            attn_forward_mxfp4kv(self.meta, q, k, v, k_pool, v_pool, out, lse, stream)
         else:
             attn_forward(self.meta, q, k, v, k_pool, v_pool, out, lse, stream)
         return out
+
+    def append(self, q, k, v, k_pool, v_pool, rope: Rope, q_out=None, k_scale=None, v_scale=None, stream=None):
+        """attn_append_rope of one layer; returns the rotated q (q_out, a new tensor when None; None
+        without q)."""
+        import torch
+
+        if q_out is None and q is not None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        attn_append_rope(self.meta, rope, q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, stream)
+        return q_out
+
+    def store(self, k, v, k_pool, v_pool, k_scale=None, v_scale=None, stream=None) -> None:
+        """store_kvcache of one layer, into pools of the config's type."""
+        if self.cfg.kv_dtype == KV_E4M3:
+            attn_store_kvcache_fp8kv(self.meta, k, v, k_pool, v_pool, k_scale, v_scale, stream)
+        elif self.cfg.kv_dtype == KV_MXFP4:
+            attn_store_kvcache_mxfp4kv(self.meta, k, v, k_pool, v_pool, stream)
+        else:
+            attn_store_kvcache(self.meta, k, v, k_pool, v_pool, stream)
+
+    def load(self, k_pool, v_pool, k=None, v=None, stream=None):
+        """What MXFP4 pools hold at the batch's new tokens' slots, as bf16 (k, v) [T, Hkv, D]."""
+        import torch
+
+        shape = (self.total_tokens, self.cfg.num_kv_heads, self.cfg.head_dim)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if v is None else v
+        attn_load_kvcache_mxfp4kv(self.meta, k_pool, v_pool, k, v, stream)
+        return k, v
