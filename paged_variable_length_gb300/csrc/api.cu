@@ -545,7 +545,9 @@ pva_status forward_impl(const MetaHost* h, const void* q, const void* k, const v
                                          : launch_decode(fp, h->cfg.head_dim, h->dec_ctas, s)) != cudaSuccess)
         return PVA_ERR_CUDA;
     if (mark(3) != cudaSuccess) return PVA_ERR_CUDA;
-    if (h->use_merge && launch_merge(fp, h->cfg.head_dim, h->sm_count, s) != cudaSuccess) return PVA_ERR_CUDA;
+    if (h->use_merge && (h->cfg.kv_dtype == PVA_KV_MXFP4 ? launch_join_mx(fp, h->cfg.head_dim, 2 * h->sm_count, s)
+                                                         : launch_merge(fp, h->cfg.head_dim, h->sm_count, s)) != cudaSuccess)
+        return PVA_ERR_CUDA;
     if (mark(4) != cudaSuccess) return PVA_ERR_CUDA;
     return PVA_OK;
 }

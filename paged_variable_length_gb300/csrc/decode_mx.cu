@@ -530,6 +530,134 @@ __global__ void __launch_bounds__(32 * (kMaxHeads + 1), 1)
     }
 }
 
+// K8: log-sum-exp join of a group's partials (and of the prefix-pass partials of shared-prefix
+// members), as merge_kernel in decode.cu, for many parts over few rows: a long request alone is
+// cut into as many parts as there are decode CTAs, and one warp per row read them one after
+// another (128 parts of 32 rows: 28 us; here 5).  kW warps share a row, each joins every kW-th
+// part with loads of several parts in flight, and the row's warps are joined through shared
+// memory, in a fixed order.  kW follows the plan's parts per group: 1 up to 4 (the rows of many
+// groups fill the SMs by themselves), 4 up to 16, else 16.
+constexpr int kJoinWarps = 16;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const ForwardParams p) {
+    constexpr int C = D / 32;  // output columns per lane
+    __shared__ float s_acc[kJoinWarps][D];
+    __shared__ float2 s_ml[kJoinWarps];
+    dev::grid_dep_launch();
+    PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
+    const int n_groups = hdr->n_dec_groups, n_parts = hdr->n_partial_slots;
+    if ((hdr->error_bits & kErrFatal) || n_groups == 0 || n_parts == 0) {
+        dev::grid_dep_wait();
+        return;
+    }
+    const DecGroup* groups = reinterpret_cast<const DecGroup*>(p.ws + p.lay.dec_groups);
+    const float* plse = reinterpret_cast<const float*>(p.ws + p.lay.partial_lse);
+    const float* pout = reinterpret_cast<const float*>(p.ws + p.lay.partial_o);
+    const int rps = p.lay.rows_per_slot, Hq = p.num_qo_heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kw = n_parts <= 4 * n_groups ? 1 : n_parts <= 16 * n_groups ? 4 : 16;
+    const int rows_cta = kJoinWarps / kw, wi = warp % kw;  // rows a CTA joins at a time; the warp's place in its row
+    const int chunks = (min(rps, max(hdr->max_group_tokens, 1) * Hq) + rows_cta - 1) / rows_cta;
+    const int n_items = n_groups * chunks;
+    DecGroup dg_next{};
+    if ((int)blockIdx.x < n_items) dg_next = groups[blockIdx.x % n_groups];
+    dev::grid_dep_wait();
+    for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
+        const DecGroup dg = dg_next;
+        if (it + (int)gridDim.x < n_items) dg_next = groups[(it + gridDim.x) % n_groups];
+        const int np = dg.nparts;
+        const int row = (it / n_groups) * rows_cta + warp / kw;
+        const bool live = np > 1 && row < dg.ntok * Hq;
+        float m = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = 0.f;
+        if (live) {
+            const float* plb = plse + (int64_t)dg.pbase * rps + row;
+            const float* pob = pout + ((int64_t)dg.pbase * rps + row) * D + lane * C;
+            // parts wi, wi + kw, ...: 32 a round, lane s holding the s-th one's LSE
+            for (int s0 = wi; s0 < np; s0 += 32 * kw) {
+                const int mine = s0 + lane * kw;
+                const float ls = mine < np ? __ldcg(plb + (int64_t)mine * rps) : -INFINITY;
+                const int cnt = min(32, (np - s0 + kw - 1) / kw);
+                float mr = ls;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+                const float mn = fmaxf(m, mr), mu = mn == -INFINITY ? 0.f : mn;
+                const float al = dev::fast_exp2(m - mu);
+                const float w = mine < np ? dev::fast_exp2(ls - mu) : 0.f;
+                float ws = w;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+                m = mn;
+                l = l * al + ws;
+#pragma unroll
+                for (int c = 0; c < C; ++c) acc[c] *= al;
+                const float* src = pob + (int64_t)s0 * rps * D;
+                const int64_t step = (int64_t)kw * rps * D;
+#pragma unroll 1
+                for (int k0 = 0; k0 < cnt; k0 += 4) {
+                    float v[4][C];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float* sp = src + (k0 + k) * step;
+#pragma unroll
+                        for (int c = 0; c < C; ++c) v[k][c] = 0.f;
+                        if (k0 + k < cnt) {
+                            if constexpr (C == 4) {
+                                const float4 x = __ldcg(reinterpret_cast<const float4*>(sp));
+                                v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+                            } else {
+                                const float2 x = __ldcg(reinterpret_cast<const float2*>(sp));
+                                v[k][0] = x.x, v[k][1] = x.y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+                        if (k0 + k < cnt) {
+#pragma unroll
+                            for (int c = 0; c < C; ++c) acc[c] += wk * v[k][c];
+                        }
+                    }
+                }
+            }
+        }
+        if (kw > 1) {  // the row's other warps, in order
+            __syncthreads();
+            if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+            for (int c = 0; c < C; ++c) s_acc[warp][lane * C + c] = acc[c];
+            __syncthreads();
+            if (wi != 0 || !live) continue;
+            float mx = m;
+            for (int w = 1; w < kw; ++w) mx = fmaxf(mx, s_ml[warp + w].x);
+            const float mu = mx == -INFINITY ? 0.f : mx;
+            const float a0 = dev::fast_exp2(m - mu);
+            l *= a0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] *= a0;
+            for (int w = 1; w < kw; ++w) {
+                const float2 ml = s_ml[warp + w];
+                const float a = dev::fast_exp2(ml.x - mu);
+                l += ml.y * a;
+#pragma unroll
+                for (int c = 0; c < C; ++c) acc[c] += a * s_acc[warp + w][lane * C + c];
+            }
+            m = mu;
+        }
+        if (!live) continue;
+        const float inv = l > 0.f ? 1.f / l : l;  // (a NaN stays one)
+        const int64_t orow = (int64_t)(dg.tok0 + row / Hq) * Hq + row % Hq;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * C);
+#pragma unroll
+        for (int c = 0; c < C; c += 2) dst[c / 2] = dev::pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+        if (p.lse != nullptr && lane == 0)
+            p.lse[orow] = l > 0.f ? (m + __log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+    }
+}
+
 template <int D, int NQ>
 cudaError_t launch_q(const ForwardParams& p, int ctas, cudaStream_t s) {
     const int hb = p.num_kv_heads < kMaxHeads ? p.num_kv_heads : kMaxHeads;
@@ -547,6 +675,12 @@ cudaError_t launch_q(const ForwardParams& p, int ctas, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_join_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s) {
+    if (head_dim == 128) return launch_programmatic(join_kernel<128>, (unsigned)ctas, 32u * kJoinWarps, 0, s, p);
+    if (head_dim == 64) return launch_programmatic(join_kernel<64>, (unsigned)ctas, 32u * kJoinWarps, 0, s, p);
+    return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s) {
     if (head_dim == 128) return p.dec_rows <= 8 ? launch_q<128, 1>(p, ctas, s) : launch_q<128, 2>(p, ctas, s);

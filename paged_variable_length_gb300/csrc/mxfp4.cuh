@@ -41,14 +41,14 @@ PVA_HD inline int row_bytes(int num_kv_heads, int D) {
     return (raw + 15) / 16 * 16;
 }
 
-// Byte offsets of head h's codes and scales inside a row.
+// Byte offsets of head h's codes and scales inside a row.  (h / hb is h >> 3: with fewer than
+// eight heads there is one group.)
 PVA_HD inline int codes_at(int h, int num_kv_heads, int D) {
-    const int hb = num_kv_heads < 8 ? num_kv_heads : 8;
-    return h / hb * group_bytes(num_kv_heads, D) + h % hb * (D / 2);
+    return (h >> 3) * group_bytes(num_kv_heads, D) + (h & 7) * (D / 2);
 }
 PVA_HD inline int scales_at(int h, int num_kv_heads, int D) {
     const int hb = num_kv_heads < 8 ? num_kv_heads : 8;
-    return h / hb * group_bytes(num_kv_heads, D) + hb * (D / 2) + h % hb * (D / kBlock);
+    return (h >> 3) * group_bytes(num_kv_heads, D) + hb * (D / 2) + (h & 7) * (D / kBlock);
 }
 
 #ifdef __CUDACC__
@@ -68,14 +68,21 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t x) {
     return r;
 }
 
-// Two fp32 -> two codes in one byte (lo in the low nibble): nearest, ties to even, magnitudes
+// Eight fp32 times f -> eight codes (x[0] in the lowest nibble): nearest, ties to even, magnitudes
 // above 6 saturate.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float* x, float f) {
     uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\t.reg .b16 u;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tmov.b16 u, {t, 0};\n\t"
-        "cvt.u32.u16 %0, u;\n\t}"
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b64 f, p, q, s, t;\n\t.reg .f32 x0, x1, x2, x3, x4, x5, x6, x7;\n\t"
+        "mov.b64 f, {%9, %9};\n\t"
+        "mov.b64 p, {%1, %2};\n\tmul.rn.f32x2 p, p, f;\n\tmov.b64 {x0, x1}, p;\n\t"
+        "mov.b64 q, {%3, %4};\n\tmul.rn.f32x2 q, q, f;\n\tmov.b64 {x2, x3}, q;\n\t"
+        "mov.b64 s, {%5, %6};\n\tmul.rn.f32x2 s, s, f;\n\tmov.b64 {x4, x5}, s;\n\t"
+        "mov.b64 t, {%7, %8};\n\tmul.rn.f32x2 t, t, f;\n\tmov.b64 {x6, x7}, t;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, x1, x0;\n\tcvt.rn.satfinite.e2m1x2.f32 b, x3, x2;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, x5, x4;\n\tcvt.rn.satfinite.e2m1x2.f32 d, x7, x6;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r)
-        : "f"(lo), "f"(hi));
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(f));
     return r;
 }
 

@@ -359,10 +359,10 @@ inline int casc_hash_bits(int batch) {
 // grid_dep_wait.  This hides the launch and set-up of the attention kernels behind the
 // kernel before them.
 template <class... Params, class... Args>
-cudaError_t launch_programmatic(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+cudaError_t launch_programmatic(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
                                 cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -380,6 +380,7 @@ size_t prepare_smem_bytes(int smem_batch, bool cascade);
 cudaError_t launch_store(const ForwardParams& p, int head_dim, cudaStream_t s);
 cudaError_t launch_decode(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
+cudaError_t launch_join_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_append(const ForwardParams& p, const RopeParams& rp, int head_dim, int kv_dtype, cudaStream_t s);
 cudaError_t launch_load_mx(const ForwardParams& p, void* k, void* v, int head_dim, cudaStream_t s);
 cudaError_t launch_merge(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);

@@ -70,6 +70,8 @@ _lib = None
 def load(path: str | None = None):
     """Load libpva.so (once).  Raises FileNotFoundError when it was not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -132,17 +134,26 @@ def _check(status: int, where: str) -> None:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = None
 
 
 def _stream(stream):
     if stream is None:
-        import torch
+        # the current stream's handle without a stream object (which costs more than the launch it
+        # is for)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
 
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+            torch.cuda.current_stream()  # initialises CUDA
+            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        return _raw_stream[0](_raw_stream[1]())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 KV_BF16, KV_E4M3, KV_MXFP4 = 0, 1, 2
@@ -247,7 +258,8 @@ class Rope:
         if rot_dim is not None and rot_dim != cos_sin.shape[1]:
             raise ValueError(f"cos_sin has {cos_sin.shape[1]} columns, rot_dim is {rot_dim}")
         self.cos_sin = cos_sin
-        self.rot_dim = int(cos_sin.shape[1])
+        self._cos_sin_ptr = cos_sin.data_ptr()
+        self.max_positions, self.rot_dim = (int(n) for n in cos_sin.shape)
         self.interleaved = bool(interleaved)
         self.set_positions(positions)
 
@@ -260,17 +272,20 @@ class Rope:
         self.positions = positions
 
     def args(self, q, k, v) -> RopeArgs:
-        if self.positions is not None and self.positions.numel() != k.shape[0]:
-            raise ValueError(f"{self.positions.numel()} positions for {k.shape[0]} tokens")
-        return RopeArgs(self.cos_sin.data_ptr(), None if self.positions is None else self.positions.data_ptr(),
+        pos = self.positions
+        if pos is not None and pos.numel() != k.shape[0]:
+            raise ValueError(f"{pos.numel()} positions for {k.shape[0]} tokens")
+        return RopeArgs(self._cos_sin_ptr, None if pos is None else pos.data_ptr(),
                         0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
-                        self.cos_sin.shape[0], self.rot_dim, int(self.interleaved), 0)
+                        self.max_positions, self.rot_dim, self.interleaved, 0)
 
 
 def _token_stride(x, name: str) -> int:
-    if x.stride(2) != 1 or (x.stride(1) != x.shape[2] and x.shape[1] > 1):
+    T, heads, dim = x.shape
+    st, sh, sd = x.stride()
+    if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"{name} [T, heads, D] has contiguous heads (only the token stride is free)")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return st if T > 1 else heads * dim
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
