@@ -252,8 +252,7 @@ pva_status prepare_in_workspace(const pva_config* cfg, const int32_t* cu_seqlens
     h.sm_count = sms;
     // requests with more than TB new tokens run on the tensor-core prefill kernel, which
     // also runs the prefix pass of shared-prefix groups
-    const bool tc_ok = prefill_supported(cfg->num_qo_heads, cfg->num_kv_heads, cfg->head_dim) &&
-                       cfg->kv_dtype != PVA_KV_MXFP4;
+    const bool tc_ok = prefill_supported(cfg->num_qo_heads, cfg->num_kv_heads, cfg->head_dim);
     h.use_prefill = (mq > TB && tc_ok) ? 1 : 0;
     h.use_cascade = (cfg->enable_cascade && tc_ok && batch >= 2 && batch <= kCascadeMaxBatch) ? 1 : 0;
     h.dec_ctas = lay.dec_ctas;  // sms x decode CTAs per SM; the plan's balanced split assumes it
@@ -297,7 +296,7 @@ pva_status prepare_in_workspace(const pva_config* cfg, const int32_t* cu_seqlens
     pp.pre_tokens = kPreRows / G;
     pp.use_prefill = h.use_prefill;
     pp.use_cascade = h.use_cascade;
-    pp.kv_fp8 = cfg->kv_dtype == PVA_KV_E4M3 ? 1 : 0;
+    pp.kv_fp8 = cfg->kv_dtype != PVA_KV_BF16 ? 1 : 0;  // (4-bit pools are weighed as 8-bit ones)
     pp.min_cascade_pages = h.cfg.min_cascade_pages;
     pp.smem_batch = batch <= kPrepareSmemBatch ? batch : 0;
     pp.split_kv = cfg->enable_split_kv ? 1 : 0;

@@ -48,12 +48,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // (a & m) | (b & ~m)
 __device__ __forceinline__ uint32_t bitsel(uint32_t a, uint32_t b, uint32_t m) {
     uint32_t r;
@@ -469,8 +463,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeads + 1), 1)
                 const uint32_t y89 = bitsel(vw[2][w] >> 4, vw[3][w], 0x0F0F0F0Fu);
                 auto tile = [&](auto byte) {
                     constexpr int B = decltype(byte)::value;
-                    const uint32_t a[4] = {hmul2(mx::e2m1x2_to_f16x2<B>(x01), f01), hmul2(mx::e2m1x2_to_f16x2<B>(y01), f01),
-                                           hmul2(mx::e2m1x2_to_f16x2<B>(x89), f89), hmul2(mx::e2m1x2_to_f16x2<B>(y89), f89)};
+                    const uint32_t a[4] = {mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(x01), f01), mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(y01), f01),
+                                           mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(x89), f89), mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(y89), f89)};
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) dev::mma_f16_16816(o[4 * w + B][n], a, pb[mt][n][0], pb[mt][n][1]);
                 };

@@ -68,6 +68,12 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t x) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Eight fp32 times f -> eight codes (x[0] in the lowest nibble): nearest, ties to even, magnitudes
 // above 6 saturate.
 __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float* x, float f) {

@@ -34,6 +34,9 @@
 // swizzled operand tiles; Q lands as bf16 and each softmax thread converts its own row
 // in place at the start of a unit (exact inside f16's range); P is packed as f16.
 // k_scale of the unit's kv head folds into the softmax scale, v_scale into 1/l.
+// MXFP4 pools take the same form with two staged tiles (their codes are half as long), the
+// block's scale applied as the codes are converted, a power of two per Q row, and P held
+// 2^7 times the weight; see the producer.
 // Every wait is bounded; a timeout sets PVA_DEVERR_TIMEOUT and the CTA winds
 // down (outstanding copies and MMAs waited for, TMEM freed) without trapping.
 #include <cuda.h>  // CUtensorMap and the tensor-map encoder's types (resolved through the runtime)
@@ -43,6 +46,7 @@
 #include <mutex>
 
 #include "device_utils.cuh"
+#include "mxfp4.cuh"
 #include "pva_internal.h"
 #include "tc_utils.cuh"
 
@@ -70,7 +74,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-template <int D, bool F8 = false>
+template <int D, int KV = PVA_KV_BF16>
 struct SmemMap {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kRegion * kHalves;
@@ -78,9 +82,10 @@ struct SmemMap {
     static constexpr int kK = kQ + 2 * kTile;    // two K stages
     static constexpr int kV = kK + 2 * kTile;    // two V stages
     static constexpr int kOff = kV + 2 * kTile;  // per producer warp: source offsets of its rows (64 x int64)
-    // FP8: the raw E4M3 rows of one K tile and one V tile (row r at r * D)
+    // FP8: the raw E4M3 rows of one K tile and one V tile (row r at r * D); MXFP4: the codes of
+    // two K and two V tiles (row r at r * D/2)
     static constexpr int kStage8 = kOff + 3 * 64 * 8;
-    static constexpr int kBytes = kStage8 + (F8 ? 2 * kPreRows * D : 0);
+    static constexpr int kBytes = kStage8 + (KV != PVA_KV_BF16 ? 2 * kPreRows * D : 0);
 };
 
 struct Bars {
@@ -141,6 +146,11 @@ __device__ __forceinline__ int queue_read(Bars* b, int k, int lane, uint64_t wli
     return v;
 }
 
+template <int I>
+struct IntTag {
+    static constexpr int value = I;
+};
+
 template <bool B>
 struct BoolTag {
     static constexpr bool value = B;
@@ -171,10 +181,13 @@ __device__ __forceinline__ UnitView unit_view(const PreTile& pt) {
 
 // q_map: Q as a 3-D tensor (D, Hq, T) whose box is one 64-column half of a Q tile (64
 // columns x G heads x TM tokens, rows in tile order); used when q_tma is nonzero.
-template <int D, bool F8>
+// KV: the pool type (PVA_KV_BF16, PVA_KV_E4M3, PVA_KV_MXFP4).
+template <int D, int KV>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const ForwardParams p, const __grid_constant__ CUtensorMap q_map, const int q_tma) {
-    using L = SmemMap<D, F8>;
+    using L = SmemMap<D, KV>;
+    constexpr bool F8 = KV != PVA_KV_BF16;  // 8- and 4-bit pools: f16 operands, converted by the producers
+    constexpr bool MX = KV == PVA_KV_MXFP4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Bars bars;
@@ -372,7 +385,108 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int kv_end = uv.key_end;
             const int nkt = (kv_end - uv.key_base + kPreKeys - 1) / kPreKeys;
             bool ok = true;
-            if constexpr (F8) {
+            if constexpr (MX) {
+                // MXFP4 rows: LPR lanes cover a row's head, a lane one block: 16 bytes of codes by async
+                // copy into a staging area of two tiles, the block's scale byte into a register.  Tile
+                // j + 1 is requested before tile j is converted, so a lane waits for copies that a whole
+                // conversion ago went out.  A lane converts exactly the bytes it copied: codes to f16
+                // pairs (exact), times the scale (exact for every scale the store writes), into the
+                // swizzled operand tiles.
+                constexpr int LPR = D / mx::kBlock, RPI = 32 / LPR, RPS = 3 * RPI;
+                constexpr int NS = (kPreRows + RPS - 1) / RPS;
+                constexpr int kBuf = kPreRows * (D / 2);  // bytes of a staged K or V tile
+                const int sub = lane / LPR, lb = lane % LPR;
+                const uint32_t region = (uint32_t)(lb >> 1) * kRegion;  // 64 columns: two blocks
+                const int c0 = (lb & 1) * 4;                            // first 16-byte chunk in it
+                const int codes = mx::codes_at(pt.kvh, p.num_kv_heads, D) + lb * 16;
+                const int scales = mx::scales_at(pt.kvh, p.num_kv_heads, D) + lb;
+                const uint32_t stage0 = dev::smem_u32(smem + L::kStage8) + lb * 16;
+                const uint8_t* kp = reinterpret_cast<const uint8_t*>(p.k_pool);
+                const uint8_t* vp = reinterpret_cast<const uint8_t*>(p.v_pool);
+                auto row_of4 = [&](int m) { return pwarp * RPI + sub + RPS * m; };
+                auto tile_pages = [&](int j, int32_t (&pg)[NS]) {
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) {
+                        const int key = uv.key_base + j * kPreKeys + row_of4(m);
+                        pg[m] = (j < nkt && row_of4(m) < kPreRows && key < kv_end) ? prow[key >> p.page_shift] : 0;
+                    }
+                };
+                // the copies of tile j (page ids pg) into its buffer; ks / vs: the scale bytes; returns
+                // the rows copied
+                auto load_tile = [&](int j, int32_t (&pg)[NS], uint32_t (&ks)[NS], uint32_t (&vs)[NS]) -> uint32_t {
+                    uint32_t valid = 0;
+                    bool bad = false;
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) {
+                        const int r = row_of4(m);
+                        const int key = uv.key_base + j * kPreKeys + r;
+                        ks[m] = vs[m] = 0;
+                        if (r >= kPreRows || key >= kv_end) continue;
+                        valid |= 1u << m;
+                        int64_t page = pg[m];
+                        if (page < 0 || page >= p.num_pages) {
+                            bad = true;
+                            page = 0;
+                        }
+                        const int64_t off = ((page << p.page_shift) + (key & ps_mask)) * p.mx_row_bytes;
+                        const uint32_t dk = stage0 + (j & 1) * 2 * kBuf + r * (D / 2);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dk), "l"(kp + off + codes));
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dk + kBuf), "l"(vp + off + codes));
+                        ks[m] = kp[off + scales];
+                        vs[m] = vp[off + scales];
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (bad) dev::set_error(err, kErrPage);
+                    return valid;
+                };
+                // staged rows -> f16 tile, then the tile's barrier.  A row past the keys' end becomes
+                // zeros, so that its weight 0 meets no infinity or NaN.
+                auto convert = [&](uint32_t valid, uint32_t src, const uint32_t (&sc)[NS], uint8_t* tile, uint64_t* full) {
+                    const uint32_t t0 = dev::smem_u32(tile) + region;
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) {
+                        const int r = row_of4(m);
+                        if (r >= kPreRows) continue;
+                        uint32_t w[4] = {0, 0, 0, 0};
+                        if (valid >> m & 1)
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                         : "r"(src + r * (D / 2)));
+                        const float f = mx::scale_f32(sc[m]);
+                        const uint32_t f2 = dev::pack_f16x2(f, f);
+                        const uint32_t row = t0 + r * 128;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dev::st_shared_v4(row + (((c0 + i) ^ (r & 7)) << 4), mx::mul_f16x2(mx::e2m1x2_to_f16x2<0>(w[i]), f2),
+                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<1>(w[i]), f2),
+                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<2>(w[i]), f2),
+                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<3>(w[i]), f2));
+                    }
+                    // these generic-proxy stores -> the tensor core's operand reads
+                    tc::fence_proxy_async_smem();
+                    dev::mbar_arrive(full);
+                };
+                int32_t pg[NS];
+                uint32_t ks[NS], vs[NS], ks_next[NS], vs_next[NS];
+                tile_pages(0, pg);
+                uint32_t valid = load_tile(0, pg, ks, vs);
+                tile_pages(1, pg);
+                for (int j = 0; j < nkt && ok; ++j, ++it) {
+                    const int st = it & 1;
+                    const uint32_t ph = (it >> 1) & 1;
+                    const uint32_t valid_next = load_tile(j + 1, pg, ks_next, vs_next);  // (no rows past the last tile)
+                    tile_pages(j + 2, pg);
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");  // this lane's copies of tile j
+                    const uint32_t src = stage0 + (j & 1) * 2 * kBuf;
+                    if (!(ok = wait_or_abort(&b->k_empty[st], ph ^ 1, wlim, b, err))) break;
+                    convert(valid, src, ks, smem + L::kK + st * L::kTile, &b->k_full[st]);
+                    if (!(ok = wait_or_abort(&b->v_empty[st], ph ^ 1, wlim, b, err))) break;
+                    convert(valid, src + kBuf, vs, smem + L::kV + st * L::kTile, &b->v_full[st]);
+                    valid = valid_next;
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) ks[m] = ks_next[m], vs[m] = vs_next[m];
+                }
+            } else if constexpr (F8) {
                 // E4M3 rows: each lane async-copies 16 bytes (16 elements) of its rows of a tile's
                 // K and V into a staging area, and once its own copies have landed converts
                 // exactly those bytes to f16 (exact) into the swizzled operand tiles -- no
@@ -670,6 +784,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_s = tmem + 256 * h + lane_base;
         const uint32_t t_o = t_s + 128;
         const float sl_base = p.scale_log2;
+        // MXFP4: P enters f16 as 2^7 times the weight (at most 2^8, see kRescaleThreshold, so below
+        // f16's maximum), and weights down to 2^-21 keep all of f16's bits
+        constexpr float kPUp = MX ? 7.f : 0.f;
         uint32_t n_s = 0;   // S tiles seen by this warpgroup
         uint32_t n_u = 0;   // units with this Q tile
         for (int k = 0;; ++k) {
@@ -679,19 +796,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             const UnitView uv = unit_view(pt);
             const int ntok = h ? pt.ntok1 : pt.ntok0;
             const int nk = uv.nk[h];
+            float q_scale = 1.f;  // MXFP4: the power of two taken out of this thread's row of Q
             if constexpr (F8) {
                 // this thread's row of Q tile h, bf16 -> f16 in place (both regions; every
                 // warp takes part in every unit: q_full counts the eight softmax warps)
                 if (!wait_or_abort(&b->q_raw, k & 1, wlim, b, err)) break;
+                auto chunk = [&](int i) {
+                    return reinterpret_cast<uint4*>(smem + L::kQ + h * L::kTile + (i >> 3) * kRegion + row * 128 +
+                                                    (i & 7) * 16);
+                };
+                if constexpr (MX) {
+                    // times the power of two that brings the row's largest element to [1, 2), which
+                    // the softmax scale takes back: q keeps its bits whatever its magnitude
+                    uint32_t amax = 0;
 #pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = *chunk(i);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint4* q16 = reinterpret_cast<uint4*>(smem + L::kQ + h * L::kTile + x * kRegion + row * 128 +
-                                                              c * 16);
-                        const uint4 v = *q16;
-                        *q16 = make_uint4(dev::bf16x2_to_f16x2(v.x), dev::bf16x2_to_f16x2(v.y),
-                                          dev::bf16x2_to_f16x2(v.z), dev::bf16x2_to_f16x2(v.w));
+                        for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+                    }
+                    const int ex = min(max((int)(amax >> 23), 1), 253);
+                    const float f = __uint_as_float((uint32_t)(254 - ex) << 23);
+                    q_scale = __uint_as_float((uint32_t)ex << 23);
+                    auto two = [&](uint32_t w) {
+                        return dev::pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+                    };
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = *chunk(i);
+                        *chunk(i) = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = *chunk(i);
+                        *chunk(i) = make_uint4(dev::bf16x2_to_f16x2(v.x), dev::bf16x2_to_f16x2(v.y),
+                                               dev::bf16x2_to_f16x2(v.z), dev::bf16x2_to_f16x2(v.w));
                     }
                 }
                 tc::fence_proxy_async_smem();
@@ -699,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) dev::mbar_arrive(&b->q_full);
             }
             if (nk == 0) continue;
-            const float sl = F8 ? sl_base * p.k_scale[pt.kvh] : sl_base;
+            const float sl = MX ? sl_base * q_scale : F8 ? sl_base * p.k_scale[pt.kvh] : sl_base;
             const bool valid = row < ntok * G;
             // last visible key of this row, and the first key some row may not see
             const int qpos = pt.qpos0 + h * TM;
@@ -753,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = m_new;
                     }
                 }
-                const float nmu = m == -INFINITY ? 0.f : -m;
+                const float nmu = (m == -INFINITY ? 0.f : -m) + kPUp;
                 float lsa[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) lsa[i] = 0.f;
@@ -798,7 +939,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- epilogue: O / l -> bf16 rows of out, LSE
             if (!wait_or_abort(&b->o_ready[h], n_u & 1, wlim, b, err)) break;
             tc::fence_after_sync();
-            const float inv = l > 0.f ? (F8 ? p.v_scale[pt.kvh] : 1.f) / l : 0.f;
+            // (MXFP4 pools may hold NaN blocks: a NaN row stays one)
+            const float inv = l > 0.f ? (F8 && !MX ? p.v_scale[pt.kvh] : 1.f) / l : (MX ? l : 0.f);
             const int64_t orow = (valid && !uv.casc)
                                      ? ((int64_t)(pt.tok0 + h * TM + row / G) * Hq + pt.kvh * G + row % G)
                                      : 0;
@@ -828,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         o[c][q4 * 4 + 3] * inv);
                 }
                 reinterpret_cast<float*>(p.ws + p.lay.partial_lse)[(int64_t)slot * p.lay.rows_per_slot + prow] =
-                    l > 0.f ? m + __log2f(l) : -INFINITY;
+                    l > 0.f ? m + (__log2f(l) - kPUp) : (MX && l != 0.f ? l : -INFINITY);
             } else if (valid) {
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -843,7 +985,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[q4] = w;
                     }
                 }
-                if (p.lse != nullptr) p.lse[orow] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                if (p.lse != nullptr)
+                    p.lse[orow] = l > 0.f ? (m + (__log2f(l) - kPUp)) * kLn2 : (MX && l != 0.f ? l : -INFINITY);
             }
         }
     }
@@ -888,12 +1031,12 @@ bool encode_q_map(const ForwardParams& p, int D, CUtensorMap* m) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool F8>
+template <int D, int KV>
 cudaError_t launch_p(const ForwardParams& p, int ctas, cudaStream_t s) {
-    const size_t smem = SmemMap<D, F8>::kBytes + 1024;
-    static_assert(SmemMap<D, F8>::kBytes + 1024 + 512 <= 227 * 1024, "shared memory per block");
+    const size_t smem = SmemMap<D, KV>::kBytes + 1024;
+    static_assert(SmemMap<D, KV>::kBytes + 1024 + 512 <= 227 * 1024, "shared memory per block");
     cudaError_t e =
-        cudaFuncSetAttribute(prefill_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(prefill_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // The register split inside the kernel assumes the launch allocates exactly
     // kRegsLaunch registers per thread; with fewer, the softmax warps' increase
@@ -901,7 +1044,7 @@ cudaError_t launch_p(const ForwardParams& p, int ctas, cudaStream_t s) {
     static int launch_regs = -1;
     if (launch_regs < 0) {
         cudaFuncAttributes attr{};
-        e = cudaFuncGetAttributes(&attr, prefill_kernel<D, F8>);
+        e = cudaFuncGetAttributes(&attr, prefill_kernel<D, KV>);
         if (e != cudaSuccess) return e;
         launch_regs = attr.numRegs;
     }
@@ -909,7 +1052,7 @@ cudaError_t launch_p(const ForwardParams& p, int ctas, cudaStream_t s) {
     CUtensorMap q_map;
     memset(&q_map, 0, sizeof(q_map));
     const int q_tma = encode_q_map(p, D, &q_map) ? 1 : 0;
-    return launch_programmatic(prefill_kernel<D, F8>, (unsigned)ctas, (unsigned)kThreads, smem, s, p, q_map,
+    return launch_programmatic(prefill_kernel<D, KV>, (unsigned)ctas, (unsigned)kThreads, smem, s, p, q_map,
                                q_tma);
 }
 
@@ -923,8 +1066,13 @@ bool prefill_supported(int num_qo_heads, int num_kv_heads, int head_dim) {
 
 cudaError_t launch_prefill(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s) {
     if (ctas <= 0) return cudaSuccess;
-    if (head_dim == 128) return p.kv_fp8 ? launch_p<128, true>(p, ctas, s) : launch_p<128, false>(p, ctas, s);
-    if (head_dim == 64) return p.kv_fp8 ? launch_p<64, true>(p, ctas, s) : launch_p<64, false>(p, ctas, s);
+    auto go = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if (p.mx_row_bytes > 0) return launch_p<D, PVA_KV_MXFP4>(p, ctas, s);
+        return p.kv_fp8 ? launch_p<D, PVA_KV_E4M3>(p, ctas, s) : launch_p<D, PVA_KV_BF16>(p, ctas, s);
+    };
+    if (head_dim == 128) return go(IntTag<128>{});
+    if (head_dim == 64) return go(IntTag<64>{});
     return cudaErrorInvalidValue;
 }
 

@@ -129,13 +129,14 @@ def tolerances(out, lse, spread, reach, small, D):
     - a score is a sum of D products in fp32, in any order: off by at most (D + 8) 2^-24 of the
       sum of magnitudes (`reach`); a weight p_j is then off by e^(2 x that) at most, plus 2^-20 for
       exp2 and its argument;
-    - P, held as 2^15 times a weight relative to the row's largest, is rounded to f16: 2^-11
-      relative, and below f16's normal range half of its smallest step, 2^-25 / 2^15 = 2^-40 of
-      the largest weight (so at most 2^-40 sum_j |v_j| in all); products and sums in fp32 add
-      less than 2^-13;
+    - P, held as 2^7 (tensor cores; at most 2^8 under their lazily raised maximum) or 2^15 (decode)
+      times a weight relative to a maximum not above the row's largest, is rounded to f16: 2^-11
+      relative, and below f16's normal range half of its smallest step, 2^-25 / 2^7 = 2^-32 of the
+      largest weight (so at most 2^-32 sum_j |v_j| in all); products and sums in fp32 add less
+      than 2^-13;
     - out is rounded to bf16 (2^-8, and half a step of its subnormals)."""
     ds = (D + 8) * 2.0 ** -24 * reach
     dp = np.expm1(2 * ds) + 2.0 ** -20
     tol = 2.0 ** -8 * np.abs(out) + (dp[..., None] + 2.0 ** -11 + 2.0 ** -13) * spread * (1 + 2.0 ** -8) \
-        + 2.0 ** -40 * small + 2.0 ** -134
+        + 2.0 ** -32 * small + 2.0 ** -134
     return tol, ds + 2.0 ** -20 * (1 + np.abs(lse))

@@ -369,3 +369,46 @@ def test_rotated_step_over_the_pool():
         pos = np.concatenate([np.arange(L - n, L) for n, L in zip(ql, kl)])
         yk = R.rotate(k.float().cpu().numpy(), rope.cos_sin.cpu().numpy(), pos, False, np.float32)
         np.testing.assert_array_equal(k2.float().cpu().numpy(), R.unpack_rows(R.pack_rows(yk), Hkv, D).astype(np.float32))
+
+
+def _shared(wl, **kw):
+    """A batch with shared prefixes: with the prefix pass and without, both against 64 bits."""
+    t = make(wl, wl.seed)
+    counts = []
+    for cascade in (True, False):
+        eng = prepared(wl, enable_cascade=cascade, **kw)
+        out, lse = run(wl, t, eng)
+        check(wl, t, out, lse)
+        counts.append(pva.attn_debug_plan_counts(eng.meta))
+    assert counts[0]["casc_groups"] > 0 and counts[1]["casc_groups"] == 0
+    return counts[0]
+
+
+def test_shared_prefix_groups():
+    from test_parity_gpu import _cascade_batch
+
+    _shared(_cascade_batch(seed=4))
+
+
+def test_shared_prefix_trees():
+    from test_parity_gpu import _deep_tree, _tree3_batch
+
+    _shared(_tree3_batch(seed=4))
+    assert _shared(_deep_tree(31, 4, 2))["casc_levels"] == 4
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(32, 8, 128, 16), (28, 4, 128, 1), (16, 1, 64, 64), (16, 16, 128, 4),
+                                         (32, 2, 64, 128)])
+def test_prefill_lengths_around_a_tile(Hq, Hkv, D, ps):
+    """Chunks whose queries and keys end around the tensor cores' 128-row and 128-key tiles."""
+    ql = [17, 31, 32, 33, 64, 65, 127, 128, 129]
+    kl = [17, 128, 160, 161, 64, 300, 127, 256, 385]
+    eng, _ = full_case(W.custom(ql, kl, Hq, Hkv, D, ps, seed=ps))
+    assert pva.attn_debug_plan_counts(eng.meta)["pre_tiles"] > 0
+
+
+def test_many_chunks_share_the_queue_with_decodes():
+    rng = np.random.default_rng(5)
+    ql = [int(x) for x in rng.integers(1, 90, 40)]
+    kl = [n + int(x) for n, x in zip(ql, rng.integers(0, 200, 40))]
+    full_case(W.custom(ql + [1] * 20, kl + [1 + 13 * i for i in range(20)], 8, 2, 64, 16, seed=5))
