@@ -34,8 +34,7 @@
 // swizzled operand tiles; Q lands as bf16 and each softmax thread converts its own row
 // in place at the start of a unit (exact inside f16's range); P is packed as f16.
 // k_scale of the unit's kv head folds into the softmax scale, v_scale into 1/l.
-// MXFP4 pools take the same form with two staged tiles (their codes are half as long), the
-// block's scale applied as the codes are converted, a power of two per Q row, and P held
+// MXFP4 pools take the same form with a ring of staged half tiles, the block's scale applied as the codes are converted, a power of two per Q row, and P held
 // 2^7 times the weight; see the producer.
 // Every wait is bounded; a timeout sets PVA_DEVERR_TIMEOUT and the CTA winds
 // down (outstanding copies and MMAs waited for, TMEM freed) without trapping.
@@ -59,16 +58,23 @@ namespace {
 // each, the control warps drop to kRegsCtrl and the softmax warps rise to kRegsSoftmax
 // (8 x kRegsSoftmax + 4 x kRegsCtrl == 12 x kRegsLaunch, so the increase never waits
 // for registers that are not there).
-constexpr int kThreads = 384;
-constexpr int kRegsLaunch = 168;
-constexpr int kRegsSoftmax = 200;
-constexpr int kRegsCtrl = 104;
-static_assert(8 * kRegsSoftmax + 4 * kRegsCtrl == 12 * kRegsLaunch, "register split must balance");
+// MXFP4 pools take three more producer warps (a fourth warpgroup), since every element is
+// converted; the registers a thread are then fewer on both sides.
 constexpr int kMmaWarp = 8;
 constexpr int kProducerWarp0 = 9;
-constexpr int kProducerThreads = 96;
-// Readers of every work-queue entry: 3 producer warps, the MMA warp, 8 softmax warps.
-constexpr int kQueueReaders = 3 + 1 + 8;
+template <int KV>
+struct Roles {
+    static constexpr bool kWide = KV == PVA_KV_MXFP4;
+    static constexpr int kThreads = kWide ? 512 : 384;
+    static constexpr int kRegsLaunch = kWide ? 128 : 168;
+    static constexpr int kRegsSoftmax = kWide ? 184 : 200;
+    static constexpr int kRegsCtrl = kWide ? 72 : 104;
+    static constexpr int kProducers = kWide ? 6 : 3;  // producer warps
+    // Readers of every work-queue entry: the producer warps, the MMA warp, 8 softmax warps.
+    static constexpr int kQueueReaders = kProducers + 1 + 8;
+    static_assert(8 * kRegsSoftmax + (kThreads / 32 - 8) * kRegsCtrl == kThreads / 32 * kRegsLaunch,
+                  "register split must balance");
+};
 constexpr int kRegion = 128 * 128;  // one 128-row x 128-byte swizzled region (64 bf16 columns)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -82,10 +88,11 @@ struct SmemMap {
     static constexpr int kK = kQ + 2 * kTile;    // two K stages
     static constexpr int kV = kK + 2 * kTile;    // two V stages
     static constexpr int kOff = kV + 2 * kTile;  // per producer warp: source offsets of its rows (64 x int64)
-    // FP8: the raw E4M3 rows of one K tile and one V tile (row r at r * D); MXFP4: the codes of
-    // two K and two V tiles (row r at r * D/2)
+    // FP8: the raw E4M3 rows of one K tile and one V tile (row r at r * D); MXFP4: a ring of
+    // three tiles (K, V, K, ...) of codes and scale words
     static constexpr int kStage8 = kOff + 3 * 64 * 8;
-    static constexpr int kBytes = kStage8 + (KV != PVA_KV_BF16 ? 2 * kPreRows * D : 0);
+    static constexpr int kMxStep = kPreRows * (D / 2 + 4);  // codes and scale words of a K or V tile
+    static constexpr int kBytes = kStage8 + (KV == PVA_KV_E4M3 ? 2 * kPreRows * D : KV == PVA_KV_MXFP4 ? 3 * kMxStep : 0);
 };
 
 struct Bars {
@@ -183,11 +190,13 @@ __device__ __forceinline__ UnitView unit_view(const PreTile& pt) {
 // columns x G heads x TM tokens, rows in tile order); used when q_tma is nonzero.
 // KV: the pool type (PVA_KV_BF16, PVA_KV_E4M3, PVA_KV_MXFP4).
 template <int D, int KV>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
     prefill_kernel(const ForwardParams p, const __grid_constant__ CUtensorMap q_map, const int q_tma) {
     using L = SmemMap<D, KV>;
     constexpr bool F8 = KV != PVA_KV_BF16;  // 8- and 4-bit pools: f16 operands, converted by the producers
     constexpr bool MX = KV == PVA_KV_MXFP4;
+    using R = Roles<KV>;
+    constexpr int kThreads = R::kThreads, kProducerThreads = 32 * R::kProducers;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Bars bars;
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         dev::mbar_init(&b->drain, 1);
         for (int s = 0; s < 4; ++s) {
             dev::mbar_init(&b->uq_full[s], 1);
-            dev::mbar_init(&b->uq_empty[s], kQueueReaders);
+            dev::mbar_init(&b->uq_empty[s], R::kQueueReaders);
         }
         b->abort_flag = 0;
         b->wait_limit = dev::wait_limit(hdr->wait_override);
@@ -258,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) {
         // control warpgroups: give registers to the softmax warpgroups
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
-    if (warp >= kProducerWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kRegsCtrl));
+    if (warp >= kProducerWarp0 && warp < kProducerWarp0 + R::kProducers) {
         // ============================================================== producer (cp.async gathers)
         // The three producer warps move the rows of every Q / K / V tile: a row is one kv
         // head of one slot (or one q head of one token), D*2 bytes, copied as 16-byte async
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kStride = 3 * kRowsPerCopy;   // rows the three warps move per step
         constexpr int kCopyIters = (kPreRows + kStride - 1) / kStride;
         static_assert(kCopyIters * kRowsPerCopy <= 64, "two row offsets per lane");
-        const int pwarp = warp - kProducerWarp0;  // 0..2
+        const int pwarp = warp - kProducerWarp0;  // 0..2 (MXFP4: 0..5, of which 0..2 gather Q rows)
         const int chunk = lane % kChunks, sub = lane / kChunks;
         const int ps_mask = p.page_size - 1;
         // row of a tile held by this warp's row index k (k = copy step * kRowsPerCopy + sub)
@@ -300,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and lane + 32, -1 for a row that is not copied
         // table entry of row index k: the rows one lane copies (k = i * kRowsPerCopy + sub)
         // sit next to each other, so that the unrolled copy loop reads them as vectors
-        int64_t* offs = reinterpret_cast<int64_t*>(smem + L::kOff) + pwarp * 64;
+        int64_t* offs = reinterpret_cast<int64_t*>(smem + L::kOff) + (pwarp % 3) * 64;
         auto slot_of = [](int k) { return (k % kRowsPerCopy) * kCopyIters + k / kRowsPerCopy; };
         auto copy_tile = [&](uint8_t* tile, int64_t o0, int64_t o1, const uint16_t* base) {
             __syncwarp();  // the previous tile's copy loop has read the table
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tma_pending = uc & 1;
                 }
-            } else
+            } else if (pwarp < 3)
             for (int h = 0; h < 2; ++h) {
                 const int ntok = h ? pt.ntok1 : pt.ntok0;
                 int64_t oq[2];
@@ -386,105 +395,119 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nkt = (kv_end - uv.key_base + kPreKeys - 1) / kPreKeys;
             bool ok = true;
             if constexpr (MX) {
-                // MXFP4 rows: LPR lanes cover a row's head, a lane one block: 16 bytes of codes by async
-                // copy into a staging area of two tiles, the block's scale byte into a register.  Tile
-                // j + 1 is requested before tile j is converted, so a lane waits for copies that a whole
-                // conversion ago went out.  A lane converts exactly the bytes it copied: codes to f16
-                // pairs (exact), times the scale (exact for every scale the store writes), into the
-                // swizzled operand tiles.
-                constexpr int LPR = D / mx::kBlock, RPI = 32 / LPR, RPS = 3 * RPI;
-                constexpr int NS = (kPreRows + RPS - 1) / RPS;
-                constexpr int kBuf = kPreRows * (D / 2);  // bytes of a staged K or V tile
+                // MXFP4 rows: LPR lanes cover a row's head, a lane one block, a warp RPI rows at a time.  A
+                // K or V tile is a step, in the order K(0) V(0) K(1) ...: its codes (16 bytes a lane)
+                // and the rows' scale words come by async copy into a ring of three steps, two steps
+                // ahead of their conversion; its page ids were read a tile earlier.  Codes become f16
+                // pairs (exact), times the scale (exact for every scale the store writes), in the
+                // swizzled operand tiles.  Three producer warps took 5 200 cycles a tile for this, twice
+                // the tensor core's time (one warp a scheduler, every instruction waiting for the one
+                // before); six in a fourth warpgroup share it.
+                constexpr int LPR = D / mx::kBlock, RPI = 32 / LPR, RPS = R::kProducers * RPI;
+                constexpr int NS = (kPreRows + RPS - 1) / RPS;  // rows a lane takes of a step
+                constexpr int kCodes = kPreRows * (D / 2);
                 const int sub = lane / LPR, lb = lane % LPR;
                 const uint32_t region = (uint32_t)(lb >> 1) * kRegion;  // 64 columns: two blocks
-                const int c0 = (lb & 1) * 4;                            // first 16-byte chunk in it
+                // first 16-byte chunk in it; the lanes of the second region take their chunks in
+                // another order, so that the lanes that store together meet no bank conflict
+                const int c0 = (lb & 1) * 4, flip = lb & 2;
                 const int codes = mx::codes_at(pt.kvh, p.num_kv_heads, D) + lb * 16;
-                const int scales = mx::scales_at(pt.kvh, p.num_kv_heads, D) + lb;
-                const uint32_t stage0 = dev::smem_u32(smem + L::kStage8) + lb * 16;
-                const uint8_t* kp = reinterpret_cast<const uint8_t*>(p.k_pool);
-                const uint8_t* vp = reinterpret_cast<const uint8_t*>(p.v_pool);
+                // the scale word holds the row's scale bytes (D 64: two heads' bytes, aligned down)
+                const int scales = mx::scales_at(pt.kvh, p.num_kv_heads, D);
+                const int my_byte = 8 * ((scales & 3) + lb);
+                const uint32_t ring = dev::smem_u32(smem + L::kStage8);
                 auto row_of4 = [&](int m) { return pwarp * RPI + sub + RPS * m; };
                 auto tile_pages = [&](int j, int32_t (&pg)[NS]) {
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
                         const int key = uv.key_base + j * kPreKeys + row_of4(m);
-                        pg[m] = (j < nkt && row_of4(m) < kPreRows && key < kv_end) ? prow[key >> p.page_shift] : 0;
+                        pg[m] = (row_of4(m) < kPreRows && key < kv_end) ? prow[key >> p.page_shift] : 0;
                     }
                 };
-                // the copies of tile j (page ids pg) into its buffer; ks / vs: the scale bytes; returns
-                // the rows copied
-                auto load_tile = [&](int j, int32_t (&pg)[NS], uint32_t (&ks)[NS], uint32_t (&vs)[NS]) -> uint32_t {
-                    uint32_t valid = 0;
+                // the copies of tile j of a pool (page ids pg) into ring slot buf; rows past the keys' end
+                // are not copied
+                auto load_step = [&](const void* pool, int j, const int32_t (&pg)[NS], uint32_t buf) {
                     bool bad = false;
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
                         const int r = row_of4(m);
                         const int key = uv.key_base + j * kPreKeys + r;
-                        ks[m] = vs[m] = 0;
                         if (r >= kPreRows || key >= kv_end) continue;
-                        valid |= 1u << m;
                         int64_t page = pg[m];
                         if (page < 0 || page >= p.num_pages) {
                             bad = true;
                             page = 0;
                         }
-                        const int64_t off = ((page << p.page_shift) + (key & ps_mask)) * p.mx_row_bytes;
-                        const uint32_t dk = stage0 + (j & 1) * 2 * kBuf + r * (D / 2);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dk), "l"(kp + off + codes));
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dk + kBuf), "l"(vp + off + codes));
-                        ks[m] = kp[off + scales];
-                        vs[m] = vp[off + scales];
+                        const uint8_t* src = static_cast<const uint8_t*>(pool) +
+                                             ((page << p.page_shift) + (key & ps_mask)) * p.mx_row_bytes;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(buf + r * (D / 2) + lb * 16), "l"(src + codes));
+                        if (lb == 0)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(buf + kCodes + 4 * r), "l"(src + (scales & ~3)));
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     if (bad) dev::set_error(err, kErrPage);
-                    return valid;
                 };
-                // staged rows -> f16 tile, then the tile's barrier.  A row past the keys' end becomes
-                // zeros, so that its weight 0 meets no infinity or NaN.
-                auto convert = [&](uint32_t valid, uint32_t src, const uint32_t (&sc)[NS], uint8_t* tile, uint64_t* full) {
+                // a step's staged rows (tile j) -> f16 operand rows, then the tile's barrier.  A row past
+                // the keys' end becomes zeros, so that its weight 0 meets no infinity or NaN.
+                auto convert = [&](int j, uint32_t buf, uint8_t* tile, uint64_t* full) {
                     const uint32_t t0 = dev::smem_u32(tile) + region;
+                    uint32_t w[NS][4], e[NS];
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) {
+                        const int r = row_of4(m);
+                        w[m][0] = w[m][1] = w[m][2] = w[m][3] = e[m] = 0;
+                        if (r < kPreRows && uv.key_base + j * kPreKeys + r < kv_end) {
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[m][0]), "=r"(w[m][1]), "=r"(w[m][2]), "=r"(w[m][3])
+                                         : "r"(buf + r * (D / 2) + lb * 16));
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(e[m]) : "r"(buf + kCodes + 4 * r));
+                        }
+                    }
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
                         const int r = row_of4(m);
                         if (r >= kPreRows) continue;
-                        uint32_t w[4] = {0, 0, 0, 0};
-                        if (valid >> m & 1)
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                         : "r"(src + r * (D / 2)));
-                        const float f = mx::scale_f32(sc[m]);
+                        const float f = mx::scale_f32((e[m] >> my_byte) & 255u);
                         const uint32_t f2 = dev::pack_f16x2(f, f);
-                        const uint32_t row = t0 + r * 128;
+                        const uint32_t x[4] = {flip ? w[m][2] : w[m][0], flip ? w[m][3] : w[m][1],
+                                               flip ? w[m][0] : w[m][2], flip ? w[m][1] : w[m][3]};
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            dev::st_shared_v4(row + (((c0 + i) ^ (r & 7)) << 4), mx::mul_f16x2(mx::e2m1x2_to_f16x2<0>(w[i]), f2),
-                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<1>(w[i]), f2),
-                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<2>(w[i]), f2),
-                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<3>(w[i]), f2));
+                            dev::st_shared_v4(t0 + r * 128 + (((c0 + (i ^ flip)) ^ (r & 7)) << 4),
+                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<0>(x[i]), f2),
+                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<1>(x[i]), f2),
+                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<2>(x[i]), f2),
+                                              mx::mul_f16x2(mx::e2m1x2_to_f16x2<3>(x[i]), f2));
                     }
                     // these generic-proxy stores -> the tensor core's operand reads
                     tc::fence_proxy_async_smem();
                     dev::mbar_arrive(full);
                 };
-                int32_t pg[NS];
-                uint32_t ks[NS], vs[NS], ks_next[NS], vs_next[NS];
+                int32_t pg[NS], pg_next[NS];
+                uint32_t b0 = ring, b1 = ring + L::kMxStep, b2 = ring + 2 * L::kMxStep;  // this step's slot, the next two
                 tile_pages(0, pg);
-                uint32_t valid = load_tile(0, pg, ks, vs);
+                load_step(p.k_pool, 0, pg, b0);
+                load_step(p.v_pool, 0, pg, b1);
                 tile_pages(1, pg);
                 for (int j = 0; j < nkt && ok; ++j, ++it) {
                     const int st = it & 1;
                     const uint32_t ph = (it >> 1) & 1;
-                    const uint32_t valid_next = load_tile(j + 1, pg, ks_next, vs_next);  // (no rows past the last tile)
-                    tile_pages(j + 2, pg);
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");  // this lane's copies of tile j
-                    const uint32_t src = stage0 + (j & 1) * 2 * kBuf;
-                    if (!(ok = wait_or_abort(&b->k_empty[st], ph ^ 1, wlim, b, err))) break;
-                    convert(valid, src, ks, smem + L::kK + st * L::kTile, &b->k_full[st]);
-                    if (!(ok = wait_or_abort(&b->v_empty[st], ph ^ 1, wlim, b, err))) break;
-                    convert(valid, src + kBuf, vs, smem + L::kV + st * L::kTile, &b->v_full[st]);
-                    valid = valid_next;
+                    auto step = [&](const void* pool, uint64_t* empty, uint64_t* full, uint8_t* tile) {
+                        __syncwarp();  // every lane has read the step before, whose slot is filled again
+                        load_step(pool, j + 1, pg, b2);
+                        asm volatile("cp.async.wait_group 2;" ::: "memory");  // this lane's copies of this step
+                        __syncwarp();                                        // and the row's other lanes'
+                        if (!wait_or_abort(empty, ph ^ 1, wlim, b, err)) return false;
+                        convert(j, b0, tile, full);
+                        const uint32_t t = b0;
+                        b0 = b1, b1 = b2, b2 = t;
+                        return true;
+                    };
+                    tile_pages(j + 2, pg_next);
+                    if (!(ok = step(p.k_pool, &b->k_empty[st], &b->k_full[st], smem + L::kK + st * L::kTile))) break;
+                    if (!(ok = step(p.v_pool, &b->v_empty[st], &b->v_full[st], smem + L::kV + st * L::kTile))) break;
 #pragma unroll
-                    for (int m = 0; m < NS; ++m) ks[m] = ks_next[m], vs[m] = vs_next[m];
+                    for (int m = 0; m < NS; ++m) pg[m] = pg_next[m];
                 }
             } else if constexpr (F8) {
                 // E4M3 rows: each lane async-copies 16 bytes (16 elements) of its rows of a tile's
@@ -775,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     }  // warps 10-11: idle
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kRegsSoftmax));
         // ============================================================== softmax (one row per thread)
         const int h = warp >> 2;  // Q tile of this warpgroup
         const int quarter = warp & 3;
@@ -1048,11 +1071,11 @@ cudaError_t launch_p(const ForwardParams& p, int ctas, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         launch_regs = attr.numRegs;
     }
-    if (launch_regs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (launch_regs != Roles<KV>::kRegsLaunch) return cudaErrorInvalidConfiguration;
     CUtensorMap q_map;
     memset(&q_map, 0, sizeof(q_map));
     const int q_tma = encode_q_map(p, D, &q_map) ? 1 : 0;
-    return launch_programmatic(prefill_kernel<D, KV>, (unsigned)ctas, (unsigned)kThreads, smem, s, p, q_map,
+    return launch_programmatic(prefill_kernel<D, KV>, (unsigned)ctas, (unsigned)Roles<KV>::kThreads, smem, s, p, q_map,
                                q_tma);
 }
 
