@@ -56,7 +56,7 @@ Layout make_layout(const pva_config* c, int sm_count, int target_units = 0) {
     const int G = c->num_qo_heads / c->num_kv_heads;
     const int TB = kDecRows / G;
     const int TM = kPreRows / G;
-    const int cps = decode_ctas_per_sm(c->num_kv_heads, c->head_dim);
+    const int cps = c->kv_dtype == PVA_KV_MXFP4 ? 1 : decode_ctas_per_sm(c->num_kv_heads, c->head_dim);
     L.dec_ctas = sm_count * cps;
     L.target_units = target_units > 0 ? target_units : 4 * L.dec_ctas;
     L.max_dec_groups = (int32_t)(c->max_tokens / TB + c->max_batch + 1);
@@ -110,6 +110,12 @@ const MetaHost* meta_of(const pva_meta* m) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Most query rows (tokens x G) of a decode group of the batch.
+int dec_rows(const MetaHost* h) {
+    const int G = h->cfg.num_qo_heads / h->cfg.num_kv_heads, tokens = kDecRows / G;
+    return G * (h->max_q_len < tokens ? h->max_q_len : tokens);
+}
+
 ForwardParams forward_params(const MetaHost* h, const void* q, const void* k, const void* v, void* k_pool,
                              void* v_pool, void* out, float* lse) {
     ForwardParams fp{};
@@ -140,8 +146,7 @@ ForwardParams forward_params(const MetaHost* h, const void* q, const void* k, co
     fp.lay = h->lay;
     fp.kv_fp8 = h->cfg.kv_dtype == PVA_KV_E4M3 ? 1 : 0;
     if (h->cfg.kv_dtype == PVA_KV_MXFP4) fp.mx_row_bytes = mx::row_bytes(fp.num_kv_heads, h->cfg.head_dim);
-    const int max_tok = kDecRows / fp.group;  // tokens of a decode group
-    fp.dec_rows = fp.group * (h->max_q_len < max_tok ? h->max_q_len : max_tok);
+    fp.dec_rows = dec_rows(h);
     return fp;
 }
 
@@ -297,6 +302,10 @@ pva_status prepare_in_workspace(const pva_config* cfg, const int32_t* cu_seqlens
     pp.use_prefill = h.use_prefill;
     pp.use_cascade = h.use_cascade;
     pp.kv_fp8 = cfg->kv_dtype != PVA_KV_BF16 ? 1 : 0;  // (4-bit pools are weighed as 8-bit ones)
+    const bool mx4 = cfg->kv_dtype == PVA_KV_MXFP4;
+    pp.dec_piece_cost = mx4 ? kMxPieceCost : kDecPieceCost;
+    pp.dec_min_share = mx4 ? kMxMinShare : kMinDecShare;
+    pp.dec_head_blocks = (int)cdiv(cfg->num_kv_heads, mx4 ? decode_mx_heads(cfg->num_kv_heads, cfg->head_dim, dec_rows(&h)) : kDecHeadBlock);
     pp.min_cascade_pages = h.cfg.min_cascade_pages;
     pp.smem_batch = batch <= kPrepareSmemBatch ? batch : 0;
     pp.split_kv = cfg->enable_split_kv ? 1 : 0;

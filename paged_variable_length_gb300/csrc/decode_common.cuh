@@ -14,7 +14,9 @@ struct StageInfo {
     int32_t unit, group, k, k1;
     int32_t tok0, ntok, qpos0, nsplit;
     int32_t pbase, split, flags, hb;
-    int32_t nparts, pad0, pad1, pad2;
+    int32_t nparts;
+    int32_t index;  // decode_mx.cu: the stage's number in its unit
+    int32_t pad1, pad2;
 };
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;
 

@@ -96,6 +96,24 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float* x, float f) {
 // elements become 0 * inf = NaN).
 __device__ __forceinline__ float scale_f32(uint32_t e) { return __uint_as_float(e << 23); }
 
+// The NB scale bytes of a head (2 or 4, a row's address) -> fp32; 255 -> NaN.
+template <int NB>
+__device__ __forceinline__ void scales_f32(const uint8_t* at, float (&f)[NB]) {
+    uint32_t w[NB / 2];  // bf16 pairs
+    if constexpr (NB == 4) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+            : "=r"(w[0]), "=r"(w[1])
+            : "r"(*reinterpret_cast<const uint32_t*>(at)));
+    } else {
+        asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(w[0]) : "h"(*reinterpret_cast<const uint16_t*>(at)));
+    }
+#pragma unroll
+    for (int i = 0; i < NB; i += 2) {
+        f[i] = __uint_as_float(w[i / 2] * 65536u);
+        f[i + 1] = __uint_as_float(w[i / 2] & 0xFFFF0000u);
+    }
+}
+
 // Scale byte of a block whose largest magnitude has the fp32 bits `amax` (sign cleared):
 // floor(log2 amax) - 2 (the exponent of E2M1's largest binade), held to the range above; a
 // block with an infinity or a NaN is a NaN block.

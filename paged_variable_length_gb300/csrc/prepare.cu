@@ -639,7 +639,7 @@ __device__ __forceinline__ void emit_balanced_groups(const PrepareParams& p, con
             dg.g0 = g0;
             dg.pad1 = dg.pad2 = dg.pad3 = dg.pad4 = dg.pad5 = 0;
             store_record(&groups[gi], dg);
-            const int e16 = g0 + (kv_end + kDecKeysPerStage - 1) / kDecKeysPerStage * kDecKeysPerStage + kDecPieceCost;
+            const int e16 = g0 + (kv_end + kDecKeysPerStage - 1) / kDecKeysPerStage * kDecKeysPerStage + p.dec_piece_cost;
             #pragma unroll 1
             for (int c = (g0 + share - 1) / share; c * share < e16 && c <= p.lay.dec_ctas; ++c) dec_first[c] = gi;
             g0 = e16;
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(PrepareParams p) {
                 const int ext = L - n + min((g + 1) * TB, n) - lp;
                 work += (unsigned long long)ext;
                 line += (unsigned long long)((ext + kDecKeysPerStage - 1) / kDecKeysPerStage * kDecKeysPerStage +
-                                             kDecPieceCost);
+                                             p.dec_piece_cost);
             }
         }
     }
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(PrepareParams p) {
     }
     // ---- balanced split: with no tensor-core unit every decode CTA starts at once, so the
     // decode groups' keys (each group padded to whole 16-key stages and followed by a gap of
-    // kDecPieceCost keys, the cost of starting a piece) are laid end to end on one line and
+    // dec_piece_cost keys, the cost of starting a piece) are laid end to end on one line and
     // CTA c takes the line's keys [c * share, (c + 1) * share): equal work per CTA, and a
     // group is cut only where a CTA's share ends (fewer partials than queued
     // units of one chunk each, which also left the grid's last units as a tail).  The
@@ -952,10 +952,10 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(PrepareParams p) {
         int share = 0;
         const bool fits = p.lay.max_dec_units >= tot3[0] + p.lay.dec_ctas + 1 &&
                           p.lay.max_partial >= 2 * p.lay.dec_ctas + 2;
-        if (p.split_kv && tiles_total == 0 && Hkv <= kDecHeadBlock && s_work > 0 && s_work < kLineLimit / 2 &&
+        if (p.split_kv && tiles_total == 0 && p.dec_head_blocks == 1 && s_work > 0 && s_work < kLineLimit / 2 &&
             fits) {
             const int per_cta = (tot3[2] + p.lay.dec_ctas - 1) / p.lay.dec_ctas;
-            share = max(kMinDecShare, (per_cta + kDecKeysPerStage - 1) / kDecKeysPerStage * kDecKeysPerStage);
+            share = max(p.dec_min_share, (per_cta + kDecKeysPerStage - 1) / kDecKeysPerStage * kDecKeysPerStage);
         }
         s_share = share;
         s_line = tot3[2];
@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1) prepare_kernel(PrepareParams p) {
                     const int pieces = 1 + (g0 + ext - 1) / share - g0 / share;
                     cnt2[0] += pieces;
                     if (pieces > 1) cnt2[1] += pieces;
-                    g0 += (ext + kDecKeysPerStage - 1) / kDecKeysPerStage * kDecKeysPerStage + kDecPieceCost;
+                    g0 += (ext + kDecKeysPerStage - 1) / kDecKeysPerStage * kDecKeysPerStage + p.dec_piece_cost;
                     continue;
                 }
                 int per;

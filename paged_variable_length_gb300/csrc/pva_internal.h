@@ -37,6 +37,9 @@ constexpr int kMinDecShare = 128;    // fewest keys a decode CTA gets in the bal
 // time of 9 keys of 4 KiB at one SM's streaming rate; measured per CTA: one piece 111.0 us,
 // two 112.1, three 113.0).
 constexpr int kDecPieceCost = 16;
+// The same for MXFP4 pools, whose keys stream in a quarter of the time.
+constexpr int kMxPieceCost = 64;
+constexpr int kMxMinShare = 64;
 
 // Error bits the kernels OR into the plan's error word (same values as pva.h).
 constexpr uint32_t kErrCu = PVA_DEVERR_CU_SEQLENS;
@@ -194,6 +197,9 @@ struct PrepareParams {
     int32_t smem_batch;          // per-request arrays live in shared memory when batch <= this
     int32_t split_kv;
     int32_t kv_fp8;              // 1: E4M3 pools (weighs the prefix pass against the tails)
+    int32_t dec_piece_cost;      // balanced split: keys charged for starting a piece
+    int32_t dec_min_share;       // balanced split: fewest keys of a decode CTA
+    int32_t dec_head_blocks;     // head blocks of a decode unit (the balanced split needs 1)
     int32_t max_kv_len;
     int32_t max_tokens;
     int32_t max_batch;
@@ -379,6 +385,8 @@ cudaError_t launch_prepare(const PrepareParams& p, cudaStream_t s);
 size_t prepare_smem_bytes(int smem_batch, bool cascade);
 cudaError_t launch_store(const ForwardParams& p, int head_dim, cudaStream_t s);
 cudaError_t launch_decode(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
+bool decode_mx_small_pages(int num_kv_heads, int page_size, int head_dim);
+int decode_mx_heads(int num_kv_heads, int head_dim, int rows);
 cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_join_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_append(const ForwardParams& p, const RopeParams& rp, int head_dim, int kv_dtype, cudaStream_t s);
