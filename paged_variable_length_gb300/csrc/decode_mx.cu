@@ -34,12 +34,15 @@
 namespace pva {
 namespace {
 
-constexpr int kKeys = 64;  // keys per ring stage
-constexpr int kMT = kKeys / 16;
+// Keys per ring stage, and the keys a consumer warp takes at a time (the wider row tile, and 16
+// consumer warps, have registers for fewer scores).
+constexpr __host__ __device__ int mx_stage_keys(int NQ) { return NQ == 1 ? 64 : 32; }
+constexpr __host__ __device__ int mx_part_keys(int D, int NQ) { return D == 128 && NQ == 1 ? 64 : 32; }
 constexpr float kLn2 = 0.69314718055994530942f;
-// P enters its f16 operand as 2^15 times the weight: the largest weight (1) stays below f16's
-// maximum, and weights down to 2^-29 of it keep all of f16's bits.
-constexpr float kPShift = 15.f;
+// P enters its f16 operand as 2^7 times the weight relative to a reference that the row's maximum
+// may outgrow by 2^8: the largest stays below f16's maximum, and weights down to 2^-21 of the
+// reference keep all of f16's bits.
+constexpr float kPShift = 7.f, kSlack = 8.f;
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     uint32_t r;
@@ -49,11 +52,17 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
 
 // D = A B (m16n8k16, f16 in, fp32 out).
 __device__ __forceinline__ void mma_f16_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// C += A B.  (Neither is volatile: the compiler may place loads and conversions between them.)
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // (a & m) | (b & ~m)
@@ -63,39 +72,104 @@ __device__ __forceinline__ uint32_t bitsel(uint32_t a, uint32_t b, uint32_t m) {
     return r;
 }
 
-// Barriers of the CTA beyond the ring's: a head's warps hand their partial results to its first.
+// Bounded wait on a barrier that lets the hardware suspend the warp (up to 100 us at a time) until
+// the phase completes: 16 warps polling without the hint issued a third of the kernel's
+// instructions.  As warp_wait otherwise.
+__device__ __forceinline__ bool wait_suspended(uint64_t* bar, uint32_t parity, uint64_t limit, uint32_t* err) {
+    bool ok;
+    if (limit == 0) {
+        ok = dev::mbar_test_wait(bar, parity);
+    } else {
+        auto attempt = [&] {
+            uint32_t done;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(dev::smem_u32(bar)), "r"(parity), "r"(100000u)
+                : "memory");
+            return done != 0;
+        };
+        ok = attempt();
+        if (!ok) {
+            const uint64_t t0 = dev::globaltimer();
+            do ok = attempt();
+            while (!ok && dev::globaltimer() - t0 <= limit);
+        }
+    }
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((threadIdx.x & 31) == 0) dev::set_error(err, kErrTimeout);
+    __syncwarp();
+    return false;
+}
+
+// What the producers say of a stage: the unit it belongs to (its keys k .. min(k + stage, k1) - 1
+// are staged), its number in it, and the query rows of the unit after it (0 tokens: not known yet,
+// or none).
+struct MxStage {
+    int32_t k, k1, tok0, ntok;
+    int32_t qpos0, nparts, slot, hb;  // slot: the unit's partial slot
+    int32_t index, flags, next_tok0, next_ntok;
+    int32_t next_hb, pad0, pad1, pad2;
+};
+
+// The ring's barriers, and those by which a head's warps hand their results to its first.
+constexpr int kMaxStages = 16;
 struct MxSmem {
-    DecSmemHead ring;
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t xfull[kDecHeadBlock], xempty[kDecHeadBlock];
+    MxStage info[kMaxStages];
 };
 
-// Launch shape: heads of a CTA (hb), consumer warps a head (kw), producer warps (pw), ring stages.
+// Launch shape: heads of a CTA (hb), consumer warps a head (kw), ring stages; bytes of a staged row
+// (the pool's row, or a block of its head groups).
 struct MxShape {
-    int hb, kw, pw, stages, stride;
+    int hb, kw, stages, stride;
     int exch;  // byte offset of the exchange area
+    int cp;    // the producers copy rows with 16-byte async copies, not one bulk copy a page run
 };
 
-// Consumer warps of a CTA, one CTA an SM: the wider head and the wider row tile have registers for
-// eight.
-constexpr __host__ __device__ int mx_consumers(int D, int NQ) { return D == 64 && NQ == 1 ? 16 : 8; }
+// Bytes of a staged row of hb heads.
+constexpr __host__ __device__ int mx_stride(int hb, int D) { return (hb * (D / 2 + D / mx::kBlock) + 15) / 16 * 16; }
 
-// D: head dim.  NQ: n8 tiles of query rows (rows of the batch's decode groups <= 8 NQ).  CP: the
-// producers copy rows with 16-byte async copies (small pages) instead of one bulk copy a page run.
-template <int D, int NQ, bool CP>
-__global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_kernel(const ForwardParams p, const MxShape sp) {
+// Warps of the one CTA an SM holds: consumers, and a warpgroup of producers, from which registers
+// move to the consumers.
+template <int D, int NQ>
+struct MxWarps {
+    static constexpr bool kMany = D == 64 && NQ == 1;  // the only tile small enough for 16 consumers
+    static constexpr int kConsumers = kMany ? 16 : 8;
+    static constexpr int kProducers = 4;
+    static constexpr int kThreads = 32 * (kConsumers + kProducers);
+    static constexpr int kRegsLaunch = kMany ? 96 : 168;
+    static constexpr int kRegsConsumer = kMany ? 104 : 208;
+    static constexpr int kRegsProducer = kMany ? 64 : 88;
+    static_assert(kConsumers * kRegsConsumer + kProducers * kRegsProducer == (kConsumers + kProducers) * kRegsLaunch,
+                  "register split must balance");
+};
+
+// D: head dim.  NQ: n8 tiles of query rows (rows of the batch's decode groups <= 8 NQ).  HBT: heads
+// of the CTA, 0: not known at compile time.  (A known row size makes the fragment addresses of a
+// stage one register and constants; computed, they were a quarter of the loop's instructions.)
+template <int D, int NQ, int HBT>
+__global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(const ForwardParams p, const MxShape sp) {
+    using MW = MxWarps<D, NQ>;
+    const bool CP = sp.cp;
+    const int kCopyWarps = CP ? 4 : 1;  // producer warps at work
+    constexpr int kKeys = mx_stage_keys(NQ), kHalf = kKeys / 2;
+    constexpr int kPart = mx_part_keys(D, NQ), kMT = kPart / 16;
     constexpr int NB = D / mx::kBlock;  // blocks of a head
     constexpr int OT = D / 16;          // m16 tiles of the output dims
     constexpr int VW = D / 64;          // words of a lane's run of V codes (D/8 dims)
     extern __shared__ __align__(128) uint8_t smem[];
-    MxSmem* xs = reinterpret_cast<MxSmem*>(smem);
-    DecSmemHead* sh = &xs->ring;
+    MxSmem* sh = reinterpret_cast<MxSmem*>(smem);
     uint8_t* ring = smem + ((sizeof(MxSmem) + 127) / 128) * 128;
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
     uint32_t* err = &hdr->error_bits;
     const uint64_t wlim = dev::wait_limit(hdr->wait_override);
 
     const int Hkv = p.num_kv_heads, G = p.group, Hq = p.num_qo_heads;
-    const int HB = sp.hb, KW = sp.kw, stages = sp.stages, stride = sp.stride;
+    const int HB = HBT ? HBT : sp.hb, KW = sp.kw, stages = sp.stages, stride = HBT ? mx_stride(HBT, D) : sp.stride;
     const int n_hb = Hkv / HB, consumers = HB * KW;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int stage_bytes = 2 * kKeys * stride;
@@ -137,8 +211,9 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
     DecUnit du_first{};
     bool have_first = false;
     int g_first = -1;
-    int32_t page_first_raw[2] = {0, 0};  // of the stage's keys lane, lane + 32
-    if (static_first && warp >= consumers) {
+    constexpr int kPL = kKeys / 32;       // keys of a stage a producer lane looks up: lane, lane + 32
+    int32_t page_first_raw[kPL] = {};
+    if (static_first) {  // (the consumers too: their first query rows)
         if (share > 0) {
             int g = reinterpret_cast<const int32_t*>(p.ws + p.lay.dec_first)[blockIdx.x];
             if (g < n_groups) {
@@ -151,22 +226,21 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
             have_first = true;
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kPL; ++h) {
             const int key = du_first.k0 + lane + 32 * h;
-            if (have_first && key < du_first.k1)
+            if (warp >= MW::kConsumers && have_first && key < du_first.k1)
                 page_first_raw[h] = p.page_table[(int64_t)du_first.req * p.ld + (key >> p.page_shift)];
         }
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            dev::mbar_init(&sh->full[s], CP ? 32 * sp.pw + 1 : 1);
+            dev::mbar_init(&sh->full[s], CP ? 32 * kCopyWarps + 1 : 1);
             dev::mbar_init(&sh->empty[s], consumers);
         }
         for (int h = 0; h < kDecHeadBlock; ++h) {
-            dev::mbar_init(&xs->xfull[h], KW > 1 ? KW - 1 : 1);
-            dev::mbar_init(&xs->xempty[h], 1);
+            dev::mbar_init(&sh->xfull[h], KW > 1 ? KW - 1 : 1);
+            dev::mbar_init(&sh->xempty[h], 1);
         }
-        sh->abort_flag = 0;
         dev::fence_barrier_init();
     }
     __syncthreads();
@@ -175,19 +249,21 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
     int32_t* sched = &hdr->pad[0];
     const int sched_base = static_first ? (int)gridDim.x : 0;
 
-    if (warp >= consumers) {
+    if (warp >= MW::kConsumers) {
         // ================================================================ producers
-        const int pwarp = warp - consumers;  // CP: 0 copies K rows, 1 V rows
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MW::kRegsProducer));
+        const int pwarp = warp - MW::kConsumers;  // CP: pool (bit 0) and half of the stage (bit 1)
+        if (pwarp >= kCopyWarps) return;
         const int r = lane;
         int stage = 0;
         uint32_t phase = 0;
         const uint64_t policy = dev::policy_evict_first();
         const int ps_mask = p.page_size - 1;
         uint32_t armed = 0, armed_par = 0;
-        // page ids of the keys k + lane, k + lane + 32 below k1 (0 past it)
-        auto pages_of = [&](int32_t (&pg)[2], const int32_t* prow, int k, int k1) {
+        // page ids of the keys k + lane (, k + lane + 32) below k1 (0 past it)
+        auto pages_of = [&](int32_t (&pg)[kPL], const int32_t* prow, int k, int k1) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) pg[h] = k + r + 32 * h < k1 ? prow[(k + r + 32 * h) >> p.page_shift] : 0;
+            for (int h = 0; h < kPL; ++h) pg[h] = k + r + 32 * h < k1 ? prow[(k + r + 32 * h) >> p.page_shift] : 0;
         };
         // a bad page id is flagged and read as page 0, which keeps the transaction count
         auto checked = [&](int32_t page) -> int64_t {
@@ -202,7 +278,9 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
         const int nch = stride / 16, ch_q = 32 / nch, ch_r = 32 % nch;  // CP: 16-byte chunks of a row
         int u;
         DecUnit du{};
-        int32_t pg[2] = {page_first_raw[0], page_first_raw[1]};  // page ids of the coming stage's keys
+        int32_t pg[kPL];  // page ids of the coming stage's keys
+#pragma unroll
+        for (int h = 0; h < kPL; ++h) pg[h] = page_first_raw[h];
         int g_cur = g_first;
         if (static_first) {
             u = have_first ? (share > 0 ? 0 : (int)blockIdx.x) : n_units;
@@ -215,13 +293,13 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
             }
         }
         while (true) {
-            if (!warp_wait(&sh->empty[stage], phase ^ 1, wlim, sh, err)) break;
+            if (!wait_suspended(&sh->empty[stage], phase ^ 1, wlim, err)) break;
             if (u >= n_units) {
                 if (lane == 0 && pwarp == 0) {
                     sh->info[stage].flags = kEnd;
                     dev::mbar_arrive(&sh->full[stage]);
                 }
-                if constexpr (CP) arrive_copies(stage);
+                if (CP) arrive_copies(stage);
                 armed &= ~(1u << stage);
                 break;
             }
@@ -252,48 +330,53 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                         if (u_next < n_units) du_next = units[u_next / n_hb];
                     }
                 }
-                const int32_t cur[2] = {pg[0], pg[1]};
+                int32_t cur[kPL];
+#pragma unroll
+                for (int h = 0; h < kPL; ++h) cur[h] = pg[h];
                 if (si_ < nst - 1) pages_of(pg, prow, k + kKeys, du.k1);
                 else if (u_next < n_units) pages_of(pg, p.page_table + (int64_t)du_next.req * p.ld, du_next.k0, du_next.k1);
-                if (si_ != 0 && !warp_wait(&sh->empty[stage], phase ^ 1, wlim, sh, err)) goto producer_done;
+                if (si_ != 0 && !wait_suspended(&sh->empty[stage], phase ^ 1, wlim, err)) goto producer_done;
                 const int nk = min(kKeys, du.k1 - k);
                 if (lane == 0 && pwarp == 0) {
-                    StageInfo& si = sh->info[stage];
-                    si.unit = u;
-                    si.group = du.group;
+                    MxStage& si = sh->info[stage];
                     si.k = k;
                     si.k1 = du.k1;
                     si.tok0 = du.tok0;
                     si.ntok = du.ntok;
                     si.qpos0 = du.qpos0;
-                    si.nsplit = du.nsplit;
-                    si.pbase = du.pbase;
-                    si.split = du.split;
-                    si.hb = hb;
                     si.nparts = du.nparts;
+                    si.slot = du.pbase + du.split;
+                    si.hb = hb;
                     si.index = si_;
                     si.flags = (si_ == 0 ? kFirst : 0) | (si_ == nst - 1 ? kLast : 0);
-                    if constexpr (CP) dev::mbar_arrive(&sh->full[stage]);
+                    si.next_tok0 = du_next.tok0;
+                    si.next_ntok = u_next < n_units ? du_next.ntok : 0;
+                    si.next_hb = u_next % n_hb;
+                    if (CP) dev::mbar_arrive(&sh->full[stage]);
                     else dev::mbar_arrive_expect_tx(&sh->full[stage], (uint32_t)(2 * nk * stride));
                 }
                 armed |= 1u << stage;
                 armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
                 __syncwarp();
-                uint32_t slot[2];  // of the keys k + lane, k + lane + 32 (a pool has fewer than 2^32)
+                uint32_t slot[kPL];  // (a pool has fewer than 2^32)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < kPL; ++h)
                     slot[h] = r + 32 * h < nk ? (uint32_t)((checked(cur[h]) << p.page_shift) + ((k + r + 32 * h) & ps_mask)) : 0u;
-                if constexpr (CP) {
-                    // this warp's pool: rows 0 .. nk-1 of the stage, their chunks dealt to the lanes in order
-                    const uint8_t* pool = reinterpret_cast<const uint8_t*>(pwarp ? p.v_pool : p.k_pool) + (int64_t)hb * stride;
-                    const uint32_t dst = dev::smem_u32(ring) + stage * stage_bytes + pwarp * kKeys * stride;
+                if (CP) {
+                    // this warp's half of the stage's rows in one pool, their chunks dealt to the lanes in
+                    // order
+                    const int half = pwarp >> 1, nr = min(nk - half * kHalf, kHalf);
+                    const uint8_t* pool = reinterpret_cast<const uint8_t*>(pwarp & 1 ? p.v_pool : p.k_pool) + (int64_t)hb * stride;
+                    const uint32_t dst = dev::smem_u32(ring) + stage * stage_bytes + ((pwarp & 1) * kKeys + half * kHalf) * stride;
+                    // the half's first row is key lane 0 (64 keys: slot[half]) or lane kHalf * half
+                    const uint32_t mine = kPL == 2 && half ? slot[kPL - 1] : slot[0];
+                    const int lane0 = kPL == 2 ? 0 : half * kHalf;
                     int row = lane / nch, ch = lane % nch;
-                    for (int e = 0; e < nk * nch; e += 32) {
-                        const uint32_t s0 = __shfl_sync(0xffffffffu, slot[0], row & 31);
-                        const uint32_t s1 = __shfl_sync(0xffffffffu, slot[1], row & 31);
-                        if (row < nk)
+                    for (int e = 0; e < nr * nch; e += 32) {
+                        const uint32_t sl = __shfl_sync(0xffffffffu, mine, (lane0 + row) & 31);
+                        if (row < nr)
                             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + row * stride + ch * 16),
-                                         "l"(pool + (int64_t)(row < 32 ? s0 : s1) * p.mx_row_bytes + ch * 16));
+                                         "l"(pool + (int64_t)sl * p.mx_row_bytes + ch * 16));
                         row += ch_q;
                         ch += ch_r;
                         if (ch >= nch) ch -= nch, ++row;
@@ -303,7 +386,7 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                     // every head in the CTA: the rows of one page are contiguous in the pool and in the
                     // stage, and the lane of a page's first row copies them all
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < kPL; ++h) {
                         const int row = r + 32 * h, in_page = (k + row) & ps_mask;
                         if (row < nk && (row == 0 || in_page == 0)) {
                             const int64_t src = (int64_t)slot[h] * p.mx_row_bytes;
@@ -327,7 +410,7 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
         }
     producer_done:
         // every copy issued must land before the CTA may exit
-        if constexpr (CP) {
+        if (CP) {
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
             for (int s = 0; s < stages; ++s)
@@ -339,7 +422,12 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
 
     // ==================================================================== consumers
     // A head's KW warps take a unit's stages in turn, each with its own running maximum, sum and
-    // output; at the unit's end the others hand theirs to the first, which joins them.
+    // output; at the unit's end the others hand theirs to the first, which joins them.  (Computing
+    // the next stage's scores among the products P V of the current one holds two of the ring's few
+    // stages and measured no better: 53 us either way for 64 decodes, 67 against 54 for 16 heads of
+    // D 64.)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MW::kRegsConsumer));
+    if (warp >= consumers) return;
     const int gl = warp % HB;  // kv head within the CTA's
     const int kw = warp / HB;
     const int gq = lane >> 2;  // MMA row group: a key of S^T, a run of dims of O^T, a query row of Q / P
@@ -347,34 +435,113 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
     const int group_bytes = min(HB, 8) * (D / 2 + NB);
     const int code_at = (gl >> 3) * group_bytes + (gl & 7) * (D / 2);  // of the head in a staged row
     const int scale_at = (gl >> 3) * group_bytes + min(HB, 8) * (D / 2) + (gl & 7) * NB;
+    uint4 qraw[NQ][NB];        // the coming unit's query rows as they lie in q
     uint32_t qb[NQ][NB][4];    // query rows: per block two k-steps of B fragments
+    float s[kMT][NQ][4];       // scores of the warp's stage (in units of the row's scale sl), 16 keys a tile
     float o[OT][NQ][4];
     float m[NQ][2], l[NQ][2], sl[NQ][2];
     int lim[NQ][2];
-    int stage = 0;
+    int stage = 0;             // the stage looked at; its phase
     uint32_t phase = 0, xphase = 0;
 
+    // B fragments of query row 8n + gq: block b, k-step t, columns (2cq, 2cq+1 | +8, +9) <- dims
+    // 32b + 8cq + 4t + (0, 1 | 2, 3), the order the K fragments come in
+    auto load_q = [&](int tok0, int ntok, int hb) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int r = 8 * n + gq;
+            const uint16_t* src = p.q + ((int64_t)(tok0 + r / G) * Hq + (hb * HB + gl) * G + r % G) * D + 8 * cq;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                qraw[n][b] = r < ntok * G ? *reinterpret_cast<const uint4*>(src + 32 * b) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    bool have_q = have_first;  // qraw holds the coming unit's rows
+    if (have_first) load_q(du_first.tok0, du_first.ntok, share > 0 ? 0 : (int)blockIdx.x % n_hb);
+
+    auto advance = [&] {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+    auto release = [&](int st) {
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&sh->empty[st]);
+    };
+    // S^T = K Q^T of a stage's part (kPart keys from key `at` on)
+    auto scores = [&](int st, int at) {
+        const uint8_t* Ks = ring + st * stage_bytes + at * stride;
+        // codes: [block][keys 0-7 | 8-15]; all loads first where there are registers for them
+        constexpr bool kAhead = NQ == 1 && !MW::kMany;
+        uint32_t kc[kAhead ? kMT : 1][NB][2];
+        auto load_k = [&](int mt, uint32_t (&c)[NB][2]) {
+            const uint32_t ka = dev::smem_u32(Ks) + (mt * 16 + (lane & 15)) * stride + code_at + (lane >> 4) * 16;
+#pragma unroll
+            for (int b = 0; b < NB; b += 2)
+                dev::ldsm_x4(ka + b * 16, c[b][0], c[b][1], c[b + 1][0], c[b + 1][1]);
+        };
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) load_k(mt, kc[mt]);
+        }
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+            if constexpr (!kAhead) load_k(mt, kc[0]);
+            const uint8_t* kr = Ks + (mt * 16 + gq) * stride + scale_at;
+            float f0[NB], f1[NB];  // scales of keys gq, gq + 8
+            mx::scales_f32<NB>(kr, f0);
+            mx::scales_f32<NB>(kr + 8 * stride, f1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t(&w)[2] = kc[kAhead ? mt : 0][b];
+                const uint32_t a0[4] = {mx::e2m1x2_to_f16x2<0>(w[0]), mx::e2m1x2_to_f16x2<0>(w[1]),
+                                        mx::e2m1x2_to_f16x2<1>(w[0]), mx::e2m1x2_to_f16x2<1>(w[1])};
+                const uint32_t a1[4] = {mx::e2m1x2_to_f16x2<2>(w[0]), mx::e2m1x2_to_f16x2<2>(w[1]),
+                                        mx::e2m1x2_to_f16x2<3>(w[0]), mx::e2m1x2_to_f16x2<3>(w[1])};
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    float c[4];
+                    mma_f16_zero(c, a0, qb[n][b][0], qb[n][b][1]);
+                    mma_f16(c, a1, qb[n][b][2], qb[n][b][3]);
+                    float(&x)[4] = s[mt][n];
+                    if (b == 0) {
+                        x[0] = c[0] * f0[b], x[1] = c[1] * f0[b], x[2] = c[2] * f1[b], x[3] = c[3] * f1[b];
+                    } else {
+                        x[0] += c[0] * f0[b], x[1] += c[1] * f0[b], x[2] += c[2] * f1[b], x[3] += c[3] * f1[b];
+                    }
+                }
+            }
+        }
+    };
+
     while (true) {
-        if (!warp_wait(&sh->full[stage], phase, wlim, sh, err)) return;
-        const StageInfo si = sh->info[stage];
+        // the unit's first stage
+        if (!wait_suspended(&sh->full[stage], phase, wlim, err)) return;
+        MxStage si = sh->info[stage];
         if (si.flags & kEnd) break;
         const int rows = si.ntok * G;
         const int g = si.hb * HB + gl;
-        if (si.index == kw) {  // the warp's first stage of the unit
+        bool last = (si.flags & kLast) != 0;  // no stage of the unit lies past `stage`
+        // the warp's first stage of the unit
+        for (int i = 0; i < kw && !last; ++i) {
+            release(stage);
+            advance();
+            if (!wait_suspended(&sh->full[stage], phase, wlim, err)) return;
+            si = sh->info[stage];
+            last = (si.flags & kLast) != 0;
+        }
+        int cur = stage;
+        const bool mine = si.index == kw;  // (else the unit has fewer stages than the head warps)
+        if (mine) {
+            if (!have_q) load_q(si.tok0, si.ntok, si.hb);
+            have_q = false;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                // B fragments of query row 8n + gq: block b, k-step t, columns (2cq, 2cq+1 | +8, +9) <-
-                // dims 32b + 8cq + 4t + (0, 1 | 2, 3), the order the K fragments come in
-                const int r = 8 * n + gq;
-                uint4 w[NB];
                 uint32_t amax = 0;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    w[b] = make_uint4(0, 0, 0, 0);
-                    if (r < rows)
-                        w[b] = *reinterpret_cast<const uint4*>(
-                            p.q + ((int64_t)(si.tok0 + r / G) * Hq + g * G + r % G) * D + 32 * b + 8 * cq);
-                    const uint32_t ww[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+                    const uint32_t ww[4] = {qraw[n][b].x, qraw[n][b].y, qraw[n][b].z, qraw[n][b].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         amax = max(amax, max((ww[i] << 16) & 0x7FFFFFFFu, ww[i] & 0x7FFF0000u));
@@ -386,7 +553,7 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                 const float qs = __uint_as_float((uint32_t)ex << 23);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    const uint32_t ww[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+                    const uint32_t ww[4] = {qraw[n][b].x, qraw[n][b].y, qraw[n][b].z, qraw[n][b].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         qb[n][b][i] = dev::pack_f16x2(__uint_as_float(ww[i] << 16) * f,
@@ -404,54 +571,20 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                 for (int t = 0; t < OT; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
             }
         }
-        if (si.index % KW == kw) {
-            const uint8_t* Ks = ring + stage * stage_bytes;
-            const uint8_t* Vs = Ks + kKeys * stride;
-            // ---- S^T = K Q^T, 16 keys a tile (in units of the row's scale sl)
-            float s[kMT][NQ][4];
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-                const uint32_t ka = dev::smem_u32(Ks) + (mt * 16 + (lane & 15)) * stride + code_at + (lane >> 4) * 16;
-                const uint8_t* kr = Ks + (mt * 16 + gq) * stride + scale_at;
-                float f0[NB], f1[NB];  // scales of keys gq, gq + 8
-                mx::scales_f32<NB>(kr, f0);
-                mx::scales_f32<NB>(kr + 8 * stride, f1);
-#pragma unroll
-                for (int b2 = 0; b2 < NB; b2 += 2) {
-                    uint32_t w[2][2];  // [block][keys 0-7 | 8-15]
-                    dev::ldsm_x4(ka + b2 * 16, w[0][0], w[0][1], w[1][0], w[1][1]);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int b = b2 + i;
-                        const uint32_t a0[4] = {mx::e2m1x2_to_f16x2<0>(w[i][0]), mx::e2m1x2_to_f16x2<0>(w[i][1]),
-                                                mx::e2m1x2_to_f16x2<1>(w[i][0]), mx::e2m1x2_to_f16x2<1>(w[i][1])};
-                        const uint32_t a1[4] = {mx::e2m1x2_to_f16x2<2>(w[i][0]), mx::e2m1x2_to_f16x2<2>(w[i][1]),
-                                                mx::e2m1x2_to_f16x2<3>(w[i][0]), mx::e2m1x2_to_f16x2<3>(w[i][1])};
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            float c[4];
-                            mma_f16_zero(c, a0, qb[n][b][0], qb[n][b][1]);
-                            dev::mma_f16_16816(c, a1, qb[n][b][2], qb[n][b][3]);
-                            float(&x)[4] = s[mt][n];
-                            if (b == 0) {
-                                x[0] = c[0] * f0[b], x[1] = c[1] * f0[b], x[2] = c[2] * f1[b], x[3] = c[3] * f1[b];
-                            } else {
-                                x[0] += c[0] * f0[b], x[1] += c[1] * f0[b], x[2] += c[2] * f1[b], x[3] += c[3] * f1[b];
-                            }
-                        }
-                    }
-                }
-            }
-            // a stage that crosses the range's end or the first token's diagonal
-            if (si.k + kKeys > si.k1 || si.k + kKeys - 1 > si.qpos0) {
+        int at = 0;  // the warp's part of the stage
+        while (mine) {
+            const int k = si.k + at, k1 = si.k1;
+            scores(cur, at);
+            // a part that crosses the range's end or the first token's diagonal
+            if (k + kPart > si.k1 || k + kPart - 1 > si.qpos0) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int last = min(lim[n][e & 1], si.k1 - 1) - si.k - gq - 8 * (e >> 1);
+                        const int end = min(lim[n][e & 1], si.k1 - 1) - k - gq - 8 * (e >> 1);
 #pragma unroll
                         for (int mt = 0; mt < kMT; ++mt)
-                            if (mt * 16 > last) s[mt][n][e] = -INFINITY;
+                            if (mt * 16 > end) s[mt][n][e] = -INFINITY;
                     }
                 }
             }
@@ -460,43 +593,68 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
             uint32_t pb[kMT][NQ][2];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                float al[2], mu[2];
+                // the reference m moves only when the row's maximum outgrows it by more than 2^kSlack (its
+                // first stage: always): the weights stay below 2^kSlack, and o and l are rescaled rarely
+                float mx[2];
+                bool grows = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float mx = fmaxf(s[0][n][i], s[0][n][2 + i]);
+                    mx[i] = fmaxf(s[0][n][i], s[0][n][2 + i]);
 #pragma unroll
-                    for (int mt = 1; mt < kMT; ++mt) mx = dev::fmax3(mx, s[mt][n][i], s[mt][n][2 + i]);
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float mn = fmaxf(m[n][i], mx * sl[n][i]);  // (sl > 0)
-                    const float mz = mn == -INFINITY ? 0.f : mn;
-                    al[i] = dev::fast_exp2(m[n][i] - mz);
-                    m[n][i] = mn;
-                    mu[i] = kPShift - mz;
+                    for (int mt = 1; mt < kMT; ++mt) mx[i] = dev::fmax3(mx[i], s[mt][n][i], s[mt][n][2 + i]);
                 }
-                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int d = 4; d <= 16; d *= 2) {
+                    mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], d));
+                    mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], d));
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mx[i] *= sl[n][i];  // (sl > 0)
+                    grows |= mx[i] > m[n][i] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, grows)) {
+                    float al[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float mn = mx[i] > m[n][i] + kSlack ? mx[i] : m[n][i];
+                        al[i] = mn == -INFINITY ? 1.f : dev::fast_exp2(m[n][i] - mn);
+                        m[n][i] = mn;
+                        l[n][i] *= al[i];
+                    }
+#pragma unroll
+                    for (int t = 0; t < OT; ++t) {
+                        o[t][n][0] *= al[0], o[t][n][1] *= al[1];
+                        o[t][n][2] *= al[0], o[t][n][3] *= al[1];
+                    }
+                }
+                float mu[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mu[i] = kPShift - (m[n][i] == -INFINITY ? 0.f : m[n][i]);
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[mt][n][e] = dev::fast_exp2(fmaf(s[mt][n][e], sl[n][e & 1], mu[e & 1]));
-                        sum[e & 1] += s[mt][n][e];
+                    for (int h = 0; h < 4; h += 2) {
+                        float e0, e1;
+                        dev::ffma2(e0, e1, s[mt][n][h], s[mt][n][h + 1], sl[n][0], sl[n][1], mu[0], mu[1]);
+                        e0 = dev::fast_exp2(e0);
+                        e1 = dev::fast_exp2(e1);
+                        dev::fadd2(sum[0], sum[1], e0, e1);
+                        // (key gq, rows 2cq, 2cq+1) -> (row gq, keys 2cq, 2cq+1)
+                        pb[mt][n][h / 2] = movmatrix_t(dev::pack_f16x2(e0, e1));
                     }
-                    // (key gq, rows 2cq, 2cq+1) -> (row gq, keys 2cq, 2cq+1)
-                    pb[mt][n][0] = movmatrix_t(dev::pack_f16x2(s[mt][n][0], s[mt][n][1]));
-                    pb[mt][n][1] = movmatrix_t(dev::pack_f16x2(s[mt][n][2], s[mt][n][3]));
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) l[n][i] = l[n][i] * al[i] + sum[i];
-#pragma unroll
-                for (int t = 0; t < OT; ++t) {
-                    o[t][n][0] *= al[0], o[t][n][1] *= al[1];
-                    o[t][n][2] *= al[0], o[t][n][3] *= al[1];
-                }
+                l[n][0] += sum[0];
+                l[n][1] += sum[1];
+            }
+
+            if (last) {  // request the next unit's query rows
+                have_q = si.next_ntok > 0;
+                if (have_q) load_q(si.next_tok0, si.next_ntok, si.next_hb);
             }
 
             // ---- O^T += V^T P^T: the lane's keys 2cq, 2cq+1 | 2cq+8, 2cq+9, dims gq*D/8 .. +D/8-1
+            const uint8_t* Vs = ring + cur * stage_bytes + (kKeys + at) * stride;
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt) {
                 uint32_t vw[4][VW], ve[4];
@@ -511,11 +669,11 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                     }
                     ve[i] = vr[scale_at + gq * (D / 8) / mx::kBlock];
                 }
-                if (si.k + kKeys > si.k1) {
+                if (k + kPart > k1) {
                     // a row past the range's end holds what an earlier stage left: scale 0 (its P is 0)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (si.k + mt * 16 + 2 * cq + (i & 1) + (i >> 1) * 8 >= si.k1) ve[i] = 0;
+                        if (k + mt * 16 + 2 * cq + (i & 1) + (i >> 1) * 8 >= k1) ve[i] = 0;
                 }
                 const uint32_t f01 = dev::pack_f16x2(mx::scale_f32(ve[0]), mx::scale_f32(ve[1]));
                 const uint32_t f89 = dev::pack_f16x2(mx::scale_f32(ve[2]), mx::scale_f32(ve[3]));
@@ -532,7 +690,7 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                             mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(x01), f01), mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(y01), f01),
                             mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(x89), f89), mx::mul_f16x2(mx::e2m1x2_to_f16x2<B>(y89), f89)};
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n) dev::mma_f16_16816(o[4 * w + B][n], a, pb[mt][n][0], pb[mt][n][1]);
+                        for (int n = 0; n < NQ; ++n) mma_f16(o[4 * w + B][n], a, pb[mt][n][0], pb[mt][n][1]);
                     };
                     tile(IntTag<0>{});
                     tile(IntTag<1>{});
@@ -540,26 +698,41 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                     tile(IntTag<3>{});
                 }
             }
+            // ---- the warp's next part: of this stage, or of its next stage of the unit
+            if (kPart < kKeys && at + kPart < kKeys && k + kPart < k1) {
+                at += kPart;
+                continue;
+            }
+            at = 0;
+            bool more = !last;
+            for (int i = 0; i < KW && more; ++i) {
+                release(stage);  // (the first is the warp's own, the others other warps')
+                advance();
+                if (!wait_suspended(&sh->full[stage], phase, wlim, err)) return;
+                si = sh->info[stage];
+                last = (si.flags & kLast) != 0;
+                if (i < KW - 1) more = !last;
+            }
+            if (!more) break;
+            cur = stage;
         }
-
-        __syncwarp();
-        if (lane == 0) dev::mbar_arrive(&sh->empty[stage]);
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1;
+        release(stage);  // the unit's last
+        advance();
+        const int parts = min(KW, si.index + 1);  // warps that had a stage of the unit
+        if (!have_q || !mine) {
+            have_q = si.next_ntok > 0;
+            if (have_q) load_q(si.next_tok0, si.next_ntok, si.next_hb);
         }
-        if (!(si.flags & kLast)) continue;
 
         // ================================================================ the head's warps' join
         if (KW > 1) {
-            const int parts = min(KW, si.index + 1);  // warps that had a stage of the unit
             constexpr int kVals = OT * 4 * NQ + 4 * NQ;
             auto area = [&](int w) {
                 return reinterpret_cast<float*>(smem + sp.exch) + ((int64_t)(w - 1) * HB + gl) * (kVals * 32) + lane;
             };
             if (kw > 0) {
                 // the area is free once the first warp has taken the unit before
-                if (!warp_wait(&xs->xempty[gl], xphase ^ 1, wlim, sh, err)) return;
+                if (!wait_suspended(&sh->xempty[gl], xphase ^ 1, wlim, err)) return;
                 if (kw < parts) {
                     float* x = area(kw);
 #pragma unroll
@@ -576,11 +749,11 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                     }
                 }
                 __syncwarp();
-                if (lane == 0) dev::mbar_arrive(&xs->xfull[gl]);
+                if (lane == 0) dev::mbar_arrive(&sh->xfull[gl]);
                 xphase ^= 1;
                 continue;
             }
-            if (!warp_wait(&xs->xfull[gl], xphase, wlim, sh, err)) return;
+            if (!wait_suspended(&sh->xfull[gl], xphase, wlim, err)) return;
             for (int w = 1; w < parts; ++w) {
                 const float* x = area(w);
 #pragma unroll
@@ -603,7 +776,7 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                 }
             }
             __syncwarp();
-            if (lane == 0) dev::mbar_arrive(&xs->xempty[gl]);
+            if (lane == 0) dev::mbar_arrive(&sh->xempty[gl]);
             xphase ^= 1;
         }
 
@@ -633,7 +806,7 @@ __global__ void __launch_bounds__(32 * (mx_consumers(D, NQ) + 2), 1) decode_mx_k
                     if (p.lse != nullptr && gq == 0) p.lse[orow] = lse * kLn2;
                 } else {
                     // split group: fp32 partial (normalised O, log2 LSE) for the merge kernel
-                    const int64_t slot = (int64_t)(si.pbase + si.split) * p.lay.rows_per_slot;
+                    const int64_t slot = (int64_t)si.slot * p.lay.rows_per_slot;
                     const int prow = (r / G) * Hq + g * G + r % G;
                     float4* d4 = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.ws + p.lay.partial_o) +
                                                            (slot + prow) * D + gq * (D / 8));
@@ -776,34 +949,58 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const ForwardPara
     }
 }
 
-template <int D, int NQ, bool CP>
-cudaError_t launch_q(const ForwardParams& p, int ctas, cudaStream_t s) {
+template <int D, int NQ, int HBT>
+cudaError_t launch_h(const ForwardParams& p, bool cp, int ctas, cudaStream_t s) {
     const int Hkv = p.num_kv_heads;
     MxShape sp{};
     sp.hb = decode_mx_heads(Hkv, D, 8 * NQ);
-    sp.kw = mx_consumers(D, NQ) / sp.hb;
-    sp.pw = CP ? 2 : 1;
-    // a head group of a row, or the row as the pool has it, padding included
-    sp.stride = sp.hb < Hkv ? mx::group_bytes(Hkv, D) * (sp.hb / 8) : p.mx_row_bytes;
+    sp.kw = MxWarps<D, NQ>::kConsumers / sp.hb;
+    sp.kw = sp.kw < 8 ? sp.kw : 8;
+    sp.stride = mx_stride(sp.hb, D);  // (of a block of heads, or of all: then the pool's row)
+    sp.cp = cp ? 1 : 0;
     const int head = (int)((sizeof(MxSmem) + 127) / 128 * 128);
-    const int exch = (sp.kw - 1) * sp.hb * (D / 4 + 4) * NQ * 128;
-    const int stage_bytes = 2 * kKeys * sp.stride;
-    sp.stages = (220 * 1024 - 1024 - head - exch) / stage_bytes;
-    sp.stages = sp.stages < 2 ? 2 : (sp.stages > 8 ? 8 : sp.stages);
+    const int stage_bytes = 2 * mx_stage_keys(NQ) * sp.stride;
+    int exch = 0;
+    for (;; --sp.kw) {
+        exch = (sp.kw - 1) * sp.hb * (D / 4 + 4) * NQ * 128;
+        sp.stages = (220 * 1024 - 1024 - head - exch) / stage_bytes;
+        sp.stages = sp.stages > kMaxStages ? kMaxStages : sp.stages;
+        // a warp holds a stage while it waits for its next one, kw stages on
+        if (sp.kw == 1 || sp.kw <= sp.stages - 2) break;
+    }
+    if (sp.stages < 2) return cudaErrorInvalidConfiguration;
     sp.exch = head + sp.stages * stage_bytes;
     const size_t smem = (size_t)sp.exch + exch;
+    // the register split inside the kernel assumes the launch allocates exactly kRegsLaunch a thread
+    static int launch_regs = -1;
+    if (launch_regs < 0) {
+        cudaFuncAttributes attr{};
+        const cudaError_t ea = cudaFuncGetAttributes(&attr, decode_mx_kernel<D, NQ, HBT>);
+        if (ea != cudaSuccess) return ea;
+        launch_regs = attr.numRegs;
+    }
+    if (launch_regs != MxWarps<D, NQ>::kRegsLaunch) return cudaErrorInvalidConfiguration;
     const cudaError_t e =
-        cudaFuncSetAttribute(decode_mx_kernel<D, NQ, CP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(decode_mx_kernel<D, NQ, HBT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_programmatic(decode_mx_kernel<D, NQ, CP>, (unsigned)ctas, 32u * (sp.hb * sp.kw + sp.pw), smem, s, p, sp);
+    return launch_programmatic(decode_mx_kernel<D, NQ, HBT>, (unsigned)ctas, (unsigned)MxWarps<D, NQ>::kThreads, smem, s, p, sp);
 }
 
 template <int D>
 cudaError_t launch_dec(const ForwardParams& p, int ctas, cudaStream_t s) {
-    const bool cp = decode_mx_small_pages(p.num_kv_heads, p.page_size, D) ||
-                    decode_mx_heads(p.num_kv_heads, D, p.dec_rows) < p.num_kv_heads;
-    if (p.dec_rows <= 8) return cp ? launch_q<D, 1, true>(p, ctas, s) : launch_q<D, 1, false>(p, ctas, s);
-    return cp ? launch_q<D, 2, true>(p, ctas, s) : launch_q<D, 2, false>(p, ctas, s);
+    const int hb = decode_mx_heads(p.num_kv_heads, D, p.dec_rows);
+    const bool cp = decode_mx_small_pages(p.num_kv_heads, p.page_size, D) || hb < p.num_kv_heads;
+    if (p.dec_rows > 8)
+        return hb == 8 ? launch_h<D, 2, 8>(p, cp, ctas, s) : launch_h<D, 2, 0>(p, cp, ctas, s);
+    switch (hb) {
+        case 1: return launch_h<D, 1, 1>(p, cp, ctas, s);
+        case 2: return launch_h<D, 1, 2>(p, cp, ctas, s);
+        case 4: return launch_h<D, 1, 4>(p, cp, ctas, s);
+        case 8: return launch_h<D, 1, 8>(p, cp, ctas, s);
+    }
+    if constexpr (D == 64)
+        if (hb == 16) return launch_h<D, 1, 16>(p, cp, ctas, s);
+    return launch_h<D, 1, 0>(p, cp, ctas, s);
 }
 
 }  // namespace
@@ -817,7 +1014,7 @@ bool decode_mx_small_pages(int num_kv_heads, int page_size, int head_dim) {
 // kv heads a decode CTA serves: all of them, or a block of them when its warps are fewer.
 int decode_mx_heads(int num_kv_heads, int head_dim, int rows) {
     if (num_kv_heads <= kDecHeadBlock) return num_kv_heads;
-    return mx_consumers(head_dim, rows <= 8 ? 1 : 2) == 16 && num_kv_heads % 16 == 0 ? 16 : kDecHeadBlock;
+    return rows <= 8 && head_dim == 64 && num_kv_heads % 16 == 0 ? 16 : kDecHeadBlock;
 }
 
 cudaError_t launch_join_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s) {
