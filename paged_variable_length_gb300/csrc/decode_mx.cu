@@ -127,7 +127,7 @@ struct MxSmem {
 struct MxShape {
     int hb, kw, stages, stride;
     int exch;  // byte offset of the exchange area
-    int cp;    // the producers copy rows with 16-byte async copies, not one bulk copy a page run
+    int producers;  // producer warps: 1, or 4 that share a stage's rows (small copies)
 };
 
 // Bytes of a staged row of hb heads.
@@ -154,8 +154,7 @@ struct MxWarps {
 template <int D, int NQ, int HBT>
 __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(const ForwardParams p, const MxShape sp) {
     using MW = MxWarps<D, NQ>;
-    const bool CP = sp.cp;
-    const int kCopyWarps = CP ? 4 : 1;  // producer warps at work
+    const bool shared_copies = sp.producers > 1;
     constexpr int kKeys = mx_stage_keys(NQ), kHalf = kKeys / 2;
     constexpr int kPart = mx_part_keys(D, NQ), kMT = kPart / 16;
     constexpr int NB = D / mx::kBlock;  // blocks of a head
@@ -205,9 +204,9 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
         du.pad1 = 0;
         return true;
     };
-    // CP: several producer warps walk the units alike, so a queue's units go round the CTAs in
+    // several producer warps walk the units alike, so a queue's units then go round the CTAs in
     // turn (they are listed longest first) instead of through the counter
-    const bool static_first = CP || !wait_late || share > 0;
+    const bool static_first = shared_copies || !wait_late || share > 0;
     DecUnit du_first{};
     bool have_first = false;
     int g_first = -1;
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            dev::mbar_init(&sh->full[s], CP ? 32 * kCopyWarps + 1 : 1);
+            dev::mbar_init(&sh->full[s], sp.producers);
             dev::mbar_init(&sh->empty[s], consumers);
         }
         for (int h = 0; h < kDecHeadBlock; ++h) {
@@ -252,8 +251,10 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
     if (warp >= MW::kConsumers) {
         // ================================================================ producers
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MW::kRegsProducer));
-        const int pwarp = warp - MW::kConsumers;  // CP: pool (bit 0) and half of the stage (bit 1)
-        if (pwarp >= kCopyWarps) return;
+        const int pwarp = warp - MW::kConsumers;
+        if (pwarp >= sp.producers) return;
+        // the warp's rows of a stage: all of both pools, or (of four warps) a half of one pool
+        const int row_lo = shared_copies ? (pwarp >> 1) * kHalf : 0, row_hi = shared_copies ? row_lo + kHalf : kKeys;
         const int r = lane;
         int stage = 0;
         uint32_t phase = 0;
@@ -271,11 +272,6 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
             dev::set_error(err, kErrPage);
             return 0;
         };
-        // CP: this thread's copies into the stage complete its arrival
-        auto arrive_copies = [&](int st) {
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(dev::smem_u32(&sh->full[st])) : "memory");
-        };
-        const int nch = stride / 16, ch_q = 32 / nch, ch_r = 32 % nch;  // CP: 16-byte chunks of a row
         int u;
         DecUnit du{};
         int32_t pg[kPL];  // page ids of the coming stage's keys
@@ -295,11 +291,10 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
         while (true) {
             if (!wait_suspended(&sh->empty[stage], phase ^ 1, wlim, err)) break;
             if (u >= n_units) {
-                if (lane == 0 && pwarp == 0) {
-                    sh->info[stage].flags = kEnd;
+                if (lane == 0) {
+                    if (pwarp == 0) sh->info[stage].flags = kEnd;
                     dev::mbar_arrive(&sh->full[stage]);
                 }
-                if (CP) arrive_copies(stage);
                 armed &= ~(1u << stage);
                 break;
             }
@@ -317,7 +312,7 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
             for (int si_ = 0; si_ < nst; ++si_) {
                 const int k = du.k0 + si_ * kKeys;
                 // the next unit: ticket, then its record, then its first page ids (see decode.cu)
-                if (!CP && share == 0 && si_ == max(nst - 4, 0) && lane == 0) ticket = sched_base + atomicAdd(sched, 1);
+                if (!shared_copies && share == 0 && si_ == max(nst - 4, 0) && lane == 0) ticket = sched_base + atomicAdd(sched, 1);
                 if (si_ == max(nst - 2, 0)) {
                     if (share > 0) {
                         const int gn = g_cur + 1;
@@ -326,7 +321,7 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
                             g_next = gn;
                         }
                     } else {
-                        u_next = CP ? u + (int)gridDim.x : __shfl_sync(0xffffffffu, ticket, 0);
+                        u_next = shared_copies ? u + (int)gridDim.x : __shfl_sync(0xffffffffu, ticket, 0);
                         if (u_next < n_units) du_next = units[u_next / n_hb];
                     }
                 }
@@ -352,52 +347,26 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
                     si.next_tok0 = du_next.tok0;
                     si.next_ntok = u_next < n_units ? du_next.ntok : 0;
                     si.next_hb = u_next % n_hb;
-                    if (CP) dev::mbar_arrive(&sh->full[stage]);
-                    else dev::mbar_arrive_expect_tx(&sh->full[stage], (uint32_t)(2 * nk * stride));
                 }
+                const int rows = max(min(nk, row_hi) - row_lo, 0);  // this warp's, in each of its pools
+                if (lane == 0) dev::mbar_arrive_expect_tx(&sh->full[stage], (uint32_t)((shared_copies ? 1 : 2) * rows * stride));
                 armed |= 1u << stage;
                 armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
                 __syncwarp();
-                uint32_t slot[kPL];  // (a pool has fewer than 2^32)
 #pragma unroll
-                for (int h = 0; h < kPL; ++h)
-                    slot[h] = r + 32 * h < nk ? (uint32_t)((checked(cur[h]) << p.page_shift) + ((k + r + 32 * h) & ps_mask)) : 0u;
-                if (CP) {
-                    // this warp's half of the stage's rows in one pool, their chunks dealt to the lanes in
-                    // order
-                    const int half = pwarp >> 1, nr = min(nk - half * kHalf, kHalf);
-                    const uint8_t* pool = reinterpret_cast<const uint8_t*>(pwarp & 1 ? p.v_pool : p.k_pool) + (int64_t)hb * stride;
-                    const uint32_t dst = dev::smem_u32(ring) + stage * stage_bytes + ((pwarp & 1) * kKeys + half * kHalf) * stride;
-                    // the half's first row is key lane 0 (64 keys: slot[half]) or lane kHalf * half
-                    const uint32_t mine = kPL == 2 && half ? slot[kPL - 1] : slot[0];
-                    const int lane0 = kPL == 2 ? 0 : half * kHalf;
-                    int row = lane / nch, ch = lane % nch;
-                    for (int e = 0; e < nr * nch; e += 32) {
-                        const uint32_t sl = __shfl_sync(0xffffffffu, mine, (lane0 + row) & 31);
-                        if (row < nr)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + row * stride + ch * 16),
-                                         "l"(pool + (int64_t)sl * p.mx_row_bytes + ch * 16));
-                        row += ch_q;
-                        ch += ch_r;
-                        if (ch >= nch) ch -= nch, ++row;
-                    }
-                    arrive_copies(stage);
-                } else {
-                    // every head in the CTA: the rows of one page are contiguous in the pool and in the
-                    // stage, and the lane of a page's first row copies them all
-#pragma unroll
-                    for (int h = 0; h < kPL; ++h) {
-                        const int row = r + 32 * h, in_page = (k + row) & ps_mask;
-                        if (row < nk && (row == 0 || in_page == 0)) {
-                            const int64_t src = (int64_t)slot[h] * p.mx_row_bytes;
-                            const uint32_t bytes = (uint32_t)(min(p.page_size - in_page, nk - row) * stride);
-                            uint8_t* dst = ring + stage * stage_bytes + row * stride;
-                            dev::bulk_g2s_hint(dst, reinterpret_cast<const uint8_t*>(p.k_pool) + src, bytes,
-                                               &sh->full[stage], policy);
-                            dev::bulk_g2s_hint(dst + kKeys * stride, reinterpret_cast<const uint8_t*>(p.v_pool) + src,
-                                               bytes, &sh->full[stage], policy);
-                        }
-                    }
+                for (int h = 0; h < kPL; ++h) {
+                    // with every head in the CTA the rows of one page are contiguous in the pool and in
+                    // the stage, and the lane of a page's first row copies them all
+                    const int row = r + 32 * h, in_page = (k + row) & ps_mask;
+                    if (row < row_lo || row >= row_lo + rows || (n_hb == 1 && row != row_lo && in_page != 0)) continue;
+                    const int64_t src = ((checked(cur[h]) << p.page_shift) + in_page) * p.mx_row_bytes + (int64_t)hb * stride;
+                    const uint32_t bytes = (uint32_t)((n_hb == 1 ? min(p.page_size - in_page, row_lo + rows - row) : 1) * stride);
+                    uint8_t* dst = ring + stage * stage_bytes + row * stride;
+                    if (!shared_copies || (pwarp & 1) == 0)
+                        dev::bulk_g2s_hint(dst, reinterpret_cast<const uint8_t*>(p.k_pool) + src, bytes, &sh->full[stage], policy);
+                    if (!shared_copies || (pwarp & 1) == 1)
+                        dev::bulk_g2s_hint(dst + kKeys * stride, reinterpret_cast<const uint8_t*>(p.v_pool) + src, bytes,
+                                           &sh->full[stage], policy);
                 }
                 if (++stage == stages) {
                     stage = 0;
@@ -410,12 +379,8 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
         }
     producer_done:
         // every copy issued must land before the CTA may exit
-        if (CP) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        } else {
-            for (int s = 0; s < stages; ++s)
-                if (armed & (1u << s)) (void)dev::mbar_wait(&sh->full[s], (armed_par >> s) & 1u);
-        }
+        for (int s = 0; s < stages; ++s)
+            if (armed & (1u << s)) (void)dev::mbar_wait(&sh->full[s], (armed_par >> s) & 1u);
         if (wait_late) dev::grid_dep_wait();
         return;
     }
@@ -950,14 +915,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const ForwardPara
 }
 
 template <int D, int NQ, int HBT>
-cudaError_t launch_h(const ForwardParams& p, bool cp, int ctas, cudaStream_t s) {
+cudaError_t launch_h(const ForwardParams& p, int producers, int ctas, cudaStream_t s) {
     const int Hkv = p.num_kv_heads;
     MxShape sp{};
     sp.hb = decode_mx_heads(Hkv, D, 8 * NQ);
     sp.kw = MxWarps<D, NQ>::kConsumers / sp.hb;
     sp.kw = sp.kw < 8 ? sp.kw : 8;
     sp.stride = mx_stride(sp.hb, D);  // (of a block of heads, or of all: then the pool's row)
-    sp.cp = cp ? 1 : 0;
+    sp.producers = producers;
     const int head = (int)((sizeof(MxSmem) + 127) / 128 * 128);
     const int stage_bytes = 2 * mx_stage_keys(NQ) * sp.stride;
     int exch = 0;
@@ -989,27 +954,26 @@ cudaError_t launch_h(const ForwardParams& p, bool cp, int ctas, cudaStream_t s) 
 template <int D>
 cudaError_t launch_dec(const ForwardParams& p, int ctas, cudaStream_t s) {
     const int hb = decode_mx_heads(p.num_kv_heads, D, p.dec_rows);
-    const bool cp = decode_mx_small_pages(p.num_kv_heads, p.page_size, D) || hb < p.num_kv_heads;
+    // One warp issues a bulk copy in about 70 cycles whatever its size, so copies of one or a few
+    // rows (small pages, or a block of the heads) are shared by four: 40 requests of up to 4000
+    // one-slot pages, 16 heads of D 64: 42 us a layer call, against 54 with 16-byte async copies by
+    // four warps.
+    const int run = hb < p.num_kv_heads ? mx_stride(hb, D) : p.page_size * p.mx_row_bytes;
+    const int producers = run < 2048 ? 4 : 1;
     if (p.dec_rows > 8)
-        return hb == 8 ? launch_h<D, 2, 8>(p, cp, ctas, s) : launch_h<D, 2, 0>(p, cp, ctas, s);
+        return hb == 8 ? launch_h<D, 2, 8>(p, producers, ctas, s) : launch_h<D, 2, 0>(p, producers, ctas, s);
     switch (hb) {
-        case 1: return launch_h<D, 1, 1>(p, cp, ctas, s);
-        case 2: return launch_h<D, 1, 2>(p, cp, ctas, s);
-        case 4: return launch_h<D, 1, 4>(p, cp, ctas, s);
-        case 8: return launch_h<D, 1, 8>(p, cp, ctas, s);
+        case 1: return launch_h<D, 1, 1>(p, producers, ctas, s);
+        case 2: return launch_h<D, 1, 2>(p, producers, ctas, s);
+        case 4: return launch_h<D, 1, 4>(p, producers, ctas, s);
+        case 8: return launch_h<D, 1, 8>(p, producers, ctas, s);
     }
     if constexpr (D == 64)
-        if (hb == 16) return launch_h<D, 1, 16>(p, cp, ctas, s);
-    return launch_h<D, 1, 0>(p, cp, ctas, s);
+        if (hb == 16) return launch_h<D, 1, 16>(p, producers, ctas, s);
+    return launch_h<D, 1, 0>(p, producers, ctas, s);
 }
 
 }  // namespace
-
-// Whether the producers copy rows in 16-byte pieces: the copy engine takes about 70 cycles a bulk
-// copy whatever its size, so a page's run has to be long to keep up with HBM.
-bool decode_mx_small_pages(int num_kv_heads, int page_size, int head_dim) {
-    return page_size * mx::row_bytes(num_kv_heads, head_dim) < 2048;
-}
 
 // kv heads a decode CTA serves: all of them, or a block of them when its warps are fewer.
 int decode_mx_heads(int num_kv_heads, int head_dim, int rows) {

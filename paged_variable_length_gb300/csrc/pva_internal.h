@@ -385,7 +385,6 @@ cudaError_t launch_prepare(const PrepareParams& p, cudaStream_t s);
 size_t prepare_smem_bytes(int smem_batch, bool cascade);
 cudaError_t launch_store(const ForwardParams& p, int head_dim, cudaStream_t s);
 cudaError_t launch_decode(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
-bool decode_mx_small_pages(int num_kv_heads, int page_size, int head_dim);
 int decode_mx_heads(int num_kv_heads, int head_dim, int rows);
 cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_join_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
