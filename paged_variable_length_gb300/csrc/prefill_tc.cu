@@ -32,10 +32,13 @@
 // shared-memory staging area (kStage8), and once its own copies have landed converts
 // exactly those bytes to f16 (exact: every E4M3 value is an f16 value) into the
 // swizzled operand tiles; Q lands as bf16 and each softmax thread converts its own row
-// in place at the start of a unit (exact inside f16's range); P is packed as f16.
+// in place, before it writes out the results of the unit before (exact inside f16's range); P is
+// packed as f16.
 // k_scale of the unit's kv head folds into the softmax scale, v_scale into 1/l.
-// MXFP4 pools take the same form with a ring of staged half tiles, the block's scale applied as the codes are converted, a power of two per Q row, and P held
-// 2^7 times the weight; see the producer.
+// MXFP4 pools take the same form with a ring of staged K and V tiles, the block's scale applied as
+// the codes are converted, a power of two taken out of each Q row, and P held 2^7 times the weight;
+// see the producer.  8 prefills of 256-4096 tokens, 32/8 heads of 128: 408 us a layer call (342 from
+// a bf16 pool, whose rows need no conversion).
 // Every wait is bounded; a timeout sets PVA_DEVERR_TIMEOUT and the CTA winds
 // down (outstanding copies and MMAs waited for, TMEM freed) without trapping.
 #include <cuda.h>  // CUtensorMap and the tensor-map encoder's types (resolved through the runtime)
@@ -59,7 +62,8 @@ namespace {
 // (8 x kRegsSoftmax + 4 x kRegsCtrl == 12 x kRegsLaunch, so the increase never waits
 // for registers that are not there).
 // MXFP4 pools take three more producer warps (a fourth warpgroup), since every element is
-// converted; the registers a thread are then fewer on both sides.
+// converted; the registers a thread are then fewer on both sides.  (The split is the one at which
+// neither side spills: 184 / 72 left the producers short, 448 us for the prefills above against 414.)
 constexpr int kMmaWarp = 8;
 constexpr int kProducerWarp0 = 9;
 template <int KV>
@@ -67,8 +71,8 @@ struct Roles {
     static constexpr bool kWide = KV == PVA_KV_MXFP4;
     static constexpr int kThreads = kWide ? 512 : 384;
     static constexpr int kRegsLaunch = kWide ? 128 : 168;
-    static constexpr int kRegsSoftmax = kWide ? 184 : 200;
-    static constexpr int kRegsCtrl = kWide ? 72 : 104;
+    static constexpr int kRegsSoftmax = kWide ? 160 : 200;
+    static constexpr int kRegsCtrl = kWide ? 96 : 104;
     static constexpr int kProducers = kWide ? 6 : 3;  // producer warps
     // Readers of every work-queue entry: the producer warps, the MMA warp, 8 softmax warps.
     static constexpr int kQueueReaders = kProducers + 1 + 8;
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kRegsCtrl));
     if (warp >= kProducerWarp0 && warp < kProducerWarp0 + R::kProducers) {
         // ============================================================== producer (cp.async gathers)
-        // The three producer warps move the rows of every Q / K / V tile: a row is one kv
+        // The three producer warps (MXFP4: six, see there) move the rows of every Q / K / V tile: a row is one kv
         // head of one slot (or one q head of one token), D*2 bytes, copied as 16-byte async
         // copies into the 128-byte-swizzled layout the MMA descriptors expect.  Q rows that
         // are gathered (shared-prefix members, or Q without a tensor map): the lanes of a
@@ -398,7 +402,9 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                 // MXFP4 rows: LPR lanes cover a row's head, a lane one block, a warp RPI rows at a time.  A
                 // K or V tile is a step, in the order K(0) V(0) K(1) ...: its codes (16 bytes a lane)
                 // and the rows' scale words come by async copy into a ring of three steps, two steps
-                // ahead of their conversion; its page ids were read a tile earlier.  Codes become f16
+                // ahead of their conversion; a lane looks up one of the warp's rows (its page id read a
+                // tile earlier), and the lanes that copy the row take its slot by shuffle (each looking
+                // up its own rows took twice the instructions: 110 against 100 us).  Codes become f16
                 // pairs (exact), times the scale (exact for every scale the store writes), in the
                 // swizzled operand tiles.  Three producer warps took 5 200 cycles a tile for this, twice
                 // the tensor core's time (one warp a scheduler, every instruction waiting for the one
@@ -417,35 +423,38 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                 const int my_byte = 8 * ((scales & 3) + lb);
                 const uint32_t ring = dev::smem_u32(smem + L::kStage8);
                 auto row_of4 = [&](int m) { return pwarp * RPI + sub + RPS * m; };
-                auto tile_pages = [&](int j, int32_t (&pg)[NS]) {
-#pragma unroll
-                    for (int m = 0; m < NS; ++m) {
-                        const int key = uv.key_base + j * kPreKeys + row_of4(m);
-                        pg[m] = (row_of4(m) < kPreRows && key < kv_end) ? prow[key >> p.page_shift] : 0;
-                    }
+                // lane i looks up the warp's row i (of RPI * NS <= 32): its page id, then its slot, kNoSlot for
+                // a row that is not copied (past the tile, or past the keys' end)
+                constexpr uint32_t kNoSlot = 0xFFFFFFFFu;
+                static_assert(RPI * NS <= 32, "a row a lane");
+                const int my_row = lane < RPI * NS ? pwarp * RPI + lane % RPI + RPS * (lane / RPI) : kPreRows;
+                auto tile_page = [&](int j) -> int32_t {
+                    const int key = uv.key_base + j * kPreKeys + my_row;
+                    return my_row < kPreRows && key < kv_end ? prow[key >> p.page_shift] : 0;
                 };
-                // the copies of tile j of a pool (page ids pg) into ring slot buf; rows past the keys' end
-                // are not copied
-                auto load_step = [&](const void* pool, int j, const int32_t (&pg)[NS], uint32_t buf) {
-                    bool bad = false;
+                auto tile_slot = [&](int j, int32_t page) -> uint32_t {
+                    const int key = uv.key_base + j * kPreKeys + my_row;
+                    if (my_row >= kPreRows || key >= kv_end) return kNoSlot;
+                    if (page < 0 || page >= p.num_pages) {
+                        dev::set_error(err, kErrPage);
+                        page = 0;
+                    }
+                    return ((uint32_t)page << p.page_shift) + (uint32_t)(key & ps_mask);
+                };
+                // the copies of a tile of a pool into ring slot buf
+                auto load_step = [&](const void* pool, uint32_t slot, uint32_t buf) {
+                    const uint8_t* src = static_cast<const uint8_t*>(pool);
+                    if (slot != kNoSlot)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(buf + kCodes + 4 * my_row),
+                                     "l"(src + (uint64_t)slot * (uint32_t)p.mx_row_bytes + (scales & ~3)));
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
-                        const int r = row_of4(m);
-                        const int key = uv.key_base + j * kPreKeys + r;
-                        if (r >= kPreRows || key >= kv_end) continue;
-                        int64_t page = pg[m];
-                        if (page < 0 || page >= p.num_pages) {
-                            bad = true;
-                            page = 0;
-                        }
-                        const uint8_t* src = static_cast<const uint8_t*>(pool) +
-                                             ((page << p.page_shift) + (key & ps_mask)) * p.mx_row_bytes;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(buf + r * (D / 2) + lb * 16), "l"(src + codes));
-                        if (lb == 0)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(buf + kCodes + 4 * r), "l"(src + (scales & ~3)));
+                        const uint32_t x = __shfl_sync(0xffffffffu, slot, RPI * m + sub);
+                        if (x != kNoSlot)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(buf + row_of4(m) * (D / 2) + lb * 16),
+                                         "l"(src + (uint64_t)x * (uint32_t)p.mx_row_bytes + codes));
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (bad) dev::set_error(err, kErrPage);
                 };
                 // a step's staged rows (tile j) -> f16 operand rows, then the tile's barrier.  A row past
                 // the keys' end becomes zeros, so that its weight 0 meets no infinity or NaN.
@@ -483,32 +492,35 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                     tc::fence_proxy_async_smem();
                     dev::mbar_arrive(full);
                 };
-                int32_t pg[NS], pg_next[NS];
-                uint32_t b0 = ring, b1 = ring + L::kMxStep, b2 = ring + 2 * L::kMxStep;  // this step's slot, the next two
-                tile_pages(0, pg);
-                load_step(p.k_pool, 0, pg, b0);
-                load_step(p.v_pool, 0, pg, b1);
-                tile_pages(1, pg);
-                for (int j = 0; j < nkt && ok; ++j, ++it) {
-                    const int st = it & 1;
-                    const uint32_t ph = (it >> 1) & 1;
-                    auto step = [&](const void* pool, uint64_t* empty, uint64_t* full, uint8_t* tile) {
-                        __syncwarp();  // every lane has read the step before, whose slot is filled again
-                        load_step(pool, j + 1, pg, b2);
-                        asm volatile("cp.async.wait_group 2;" ::: "memory");  // this lane's copies of this step
-                        __syncwarp();                                        // and the row's other lanes'
-                        if (!wait_or_abort(empty, ph ^ 1, wlim, b, err)) return false;
-                        convert(j, b0, tile, full);
-                        const uint32_t t = b0;
-                        b0 = b1, b1 = b2, b2 = t;
-                        return true;
-                    };
-                    tile_pages(j + 2, pg_next);
-                    if (!(ok = step(p.k_pool, &b->k_empty[st], &b->k_full[st], smem + L::kK + st * L::kTile))) break;
-                    if (!(ok = step(p.v_pool, &b->v_empty[st], &b->v_full[st], smem + L::kV + st * L::kTile))) break;
-#pragma unroll
-                    for (int m = 0; m < NS; ++m) pg[m] = pg_next[m];
+                // (K and V through one copy of the code: 103 us for a batch of chunks, 106 with both
+                // written out, as the roles' loops share the instruction cache)
+                int32_t page = tile_page(0);  // of the coming tile
+                uint32_t slot = kNoSlot;      // of this tile
+                uint32_t at = 0, fill = 0;    // ring slot converted next, filled next
+                auto after = [](uint32_t x) { return x == 2 ? 0u : x + 1; };
+                const uint32_t it0 = it;
+                // step x is requested at turn x and converted at turn x + 2
+#pragma unroll 1
+                for (int x = 0; x < 2 * nkt + 2 && ok; ++x) {
+                    __syncwarp();  // every lane has read the step before, whose slot is filled again
+                    if ((x & 1) == 0) {
+                        slot = tile_slot(x >> 1, page);
+                        page = tile_page((x >> 1) + 1);
+                    }
+                    load_step((x & 1) ? p.v_pool : p.k_pool, slot, ring + fill * L::kMxStep);
+                    fill = after(fill);
+                    if (x < 2) continue;
+                    asm volatile("cp.async.wait_group 2;" ::: "memory");  // this lane's copies of the step
+                    __syncwarp();                                        // and the row's other lanes'
+                    const int y = x - 2;
+                    const uint32_t i = it0 + (y >> 1), st = i & 1;
+                    if (!(ok = wait_or_abort((y & 1) ? &b->v_empty[st] : &b->k_empty[st], ((i >> 1) & 1) ^ 1, wlim, b, err)))
+                        break;
+                    convert(y >> 1, ring + at * L::kMxStep, smem + ((y & 1) ? L::kV : L::kK) + st * L::kTile,
+                            (y & 1) ? &b->v_full[st] : &b->k_full[st]);
+                    at = after(at);
                 }
+                it += nkt;
             } else if constexpr (F8) {
                 // E4M3 rows: each lane async-copies 16 bytes (16 elements) of its rows of a tile's
                 // K and V into a staging area, and once its own copies have landed converts
@@ -812,57 +824,55 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         constexpr float kPUp = MX ? 7.f : 0.f;
         uint32_t n_s = 0;   // S tiles seen by this warpgroup
         uint32_t n_u = 0;   // units with this Q tile
+        // F8: this thread's row of Q tile h of the CTA's unit k, bf16 -> f16 in place (both regions;
+        // every warp takes part in every unit: q_full counts the eight softmax warps).  MXFP4: times
+        // the power of two that brings the row's largest element to [1, 2), which the softmax scale
+        // takes back (q_scale): q keeps its bits whatever its magnitude.
+        float q_scale = 1.f;
+        auto convert_q = [&](int k) -> bool {
+            if (!wait_or_abort(&b->q_raw, k & 1, wlim, b, err)) return false;
+            // (each lane takes its row's chunks from another one on: in the same order, the lanes of an
+            // access would all meet in one 16-byte column of banks)
+            auto chunk = [&](int i) {
+                return reinterpret_cast<uint4*>(smem + L::kQ + h * L::kTile + (i >> 3) * kRegion + row * 128 +
+                                                ((i ^ row) & 7) * 16);
+            };
+            float f = 1.f;
+            if constexpr (MX) {
+                uint32_t amax = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = *chunk(i);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+                }
+                const int ex = min(max((int)(amax >> 23), 1), 253);
+                f = __uint_as_float((uint32_t)(254 - ex) << 23);
+                q_scale = __uint_as_float((uint32_t)ex << 23);
+            }
+            auto two = [&](uint32_t w) {
+                return MX ? dev::pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f)
+                          : dev::bf16x2_to_f16x2(w);
+            };
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 v = *chunk(i);
+                *chunk(i) = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(&b->q_full);
+            return true;
+        };
+        int u = queue_read(b, 0, lane, wlim, err);
+        if (F8 && u >= 0 && !convert_q(0)) u = -1;
         for (int k = 0;; ++k) {
-            const int u = queue_read(b, k, lane, wlim, err);
             if (u < 0 || b->abort_flag) break;
             const PreTile pt = units[u];
             const UnitView uv = unit_view(pt);
             const int ntok = h ? pt.ntok1 : pt.ntok0;
             const int nk = uv.nk[h];
-            float q_scale = 1.f;  // MXFP4: the power of two taken out of this thread's row of Q
-            if constexpr (F8) {
-                // this thread's row of Q tile h, bf16 -> f16 in place (both regions; every
-                // warp takes part in every unit: q_full counts the eight softmax warps)
-                if (!wait_or_abort(&b->q_raw, k & 1, wlim, b, err)) break;
-                auto chunk = [&](int i) {
-                    return reinterpret_cast<uint4*>(smem + L::kQ + h * L::kTile + (i >> 3) * kRegion + row * 128 +
-                                                    (i & 7) * 16);
-                };
-                if constexpr (MX) {
-                    // times the power of two that brings the row's largest element to [1, 2), which
-                    // the softmax scale takes back: q keeps its bits whatever its magnitude
-                    uint32_t amax = 0;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = *chunk(i);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
-                    }
-                    const int ex = min(max((int)(amax >> 23), 1), 253);
-                    const float f = __uint_as_float((uint32_t)(254 - ex) << 23);
-                    q_scale = __uint_as_float((uint32_t)ex << 23);
-                    auto two = [&](uint32_t w) {
-                        return dev::pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
-                    };
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = *chunk(i);
-                        *chunk(i) = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = *chunk(i);
-                        *chunk(i) = make_uint4(dev::bf16x2_to_f16x2(v.x), dev::bf16x2_to_f16x2(v.y),
-                                               dev::bf16x2_to_f16x2(v.z), dev::bf16x2_to_f16x2(v.w));
-                    }
-                }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) dev::mbar_arrive(&b->q_full);
-            }
-            if (nk == 0) continue;
             const float sl = MX ? sl_base * q_scale : F8 ? sl_base * p.k_scale[pt.kvh] : sl_base;
             const bool valid = row < ntok * G;
             // last visible key of this row, and the first key some row may not see
@@ -959,6 +969,13 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                 if (lane == 0) dev::mbar_arrive(&b->p_full[h]);
             }
             if (!ok) break;
+            // the next unit's Q before this one's results: its rows lie in the Q tile by the time the
+            // last weights are out, and the tensor core goes on with its products during the epilogue
+            if constexpr (F8) {
+                u = queue_read(b, k + 1, lane, wlim, err);
+                if (u >= 0 && !convert_q(k + 1)) break;
+            }
+            if (nk > 0) {
             // ---- epilogue: O / l -> bf16 rows of out, LSE
             if (!wait_or_abort(&b->o_ready[h], n_u & 1, wlim, b, err)) break;
             tc::fence_after_sync();
@@ -1011,6 +1028,8 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                 if (p.lse != nullptr)
                     p.lse[orow] = l > 0.f ? (m + (__log2f(l) - kPUp)) * kLn2 : (MX && l != 0.f ? l : -INFINITY);
             }
+            }
+            if constexpr (!F8) u = queue_read(b, k + 1, lane, wlim, err);
         }
     }
     tc::fence_before_sync();
