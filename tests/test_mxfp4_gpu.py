@@ -412,3 +412,67 @@ def test_many_chunks_share_the_queue_with_decodes():
     ql = [int(x) for x in rng.integers(1, 90, 40)]
     kl = [n + int(x) for n, x in zip(ql, rng.integers(0, 200, 40))]
     full_case(W.custom(ql + [1] * 20, kl + [1 + 13 * i for i in range(20)], 8, 2, 64, 16, seed=5))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps,n", [(48, 16, 128, 4, 4), (80, 16, 64, 1, 3), (48, 24, 64, 2, 1), (120, 24, 128, 16, 3),
+                                           (32, 32, 128, 2, 1), (64, 32, 64, 1, 1), (16, 1, 128, 1, 1), (15, 1, 64, 64, 1),
+                                           (12, 1, 128, 16, 1)])
+def test_head_blocks_row_tiles_and_page_sizes(Hq, Hkv, D, ps, n):
+    """Several CTAs a unit, one or two tiles of query rows, copies of a row or of a page."""
+    kl = [n, 31 + n, 32 + n, 64 + n, 65, 700, 1301, 2000]
+    eng, t = full_case(W.custom([n] * len(kl), kl, Hq, Hkv, D, ps, seed=Hq + ps))
+    assert pva.attn_debug_plan_counts(eng.meta)["dec_units"] > 0
+
+
+@pytest.mark.parametrize("ps", [1, 16])
+def test_layers_of_one_plan(ps):
+    """Several layer calls of one prepared batch (a queue of decode units beside prefill tiles)."""
+    wl = W.custom([150, 1, 1, 3, 1], [150, 900, 33, 40, 2500], 16, 8, 64, ps, seed=12)
+    eng = prepared(wl)
+    for layer in range(3):
+        t = make(wl, 20 + layer)
+        out, lse = run(wl, t, eng)
+        check(wl, t, out, lse)
+    again, _ = run(wl, t, eng)
+    assert torch.equal(again, out)
+
+
+def test_rows_past_the_batch_stay():
+    """Buffers longer than the batch: what lies behind the last token is neither read nor written."""
+    wl = W.custom([1, 40, 1], [700, 40, 33], 16, 4, 128, 16, seed=3)
+    t = make(wl, 3)
+    want, wl_lse = run(wl, t, prepared(wl))
+    T, pad = wl.total_tokens, 70
+    long = {n: torch.cat([t[n], torch.full((pad, *t[n].shape[1:]), float("nan"), dtype=torch.bfloat16, device=DEV)])
+            for n in ("q", "k", "v")}
+    out = torch.full_like(long["q"], 7.0)
+    lse = torch.full(long["q"].shape[:2], 7.0, device=DEV)
+    eng = prepared(wl)
+    eng.forward(long["q"], long["k"], long["v"], t["kp"], t["vp"], out=out, lse=lse)
+    k2, v2 = torch.full_like(long["k"], 7.0), torch.full_like(long["v"], 7.0)
+    eng.load(t["kp"], t["vp"], k=k2, v=v2)
+    torch.cuda.synchronize()
+    assert pva.attn_get_device_status(eng.meta) == 0
+    assert torch.equal(out[:T], want) and torch.equal(lse[:T], wl_lse)
+    for x in (out, lse, k2, v2):
+        assert bool((x[T:] == 7.0).all())
+
+
+def test_pools_past_4_gib():
+    """Slots whose byte offset needs more than 32 bits (decodes, a chunk, a prefill, the store)."""
+    Hq, Hkv, D, ps = 16, 8, 128, 16
+    wl = W.custom([1, 40, 1, 130], [700, 90, 33, 130], Hq, Hkv, D, ps, seed=3)
+    t = make(wl, 3)
+    near, far = {n: x.clone() for n, x in t.items()}, dict(t)
+    want, want_lse = run(wl, near, prepared(wl))
+    rb = pva.mxfp4_row_bytes(Hkv, D)
+    first = -(-(2 ** 32 + 2 ** 20) // (rb * ps))            # pages before the used ones
+    for n in ("kp", "vp"):
+        far[n] = torch.empty(first * ps + wl.num_slots, rb, dtype=torch.uint8, device=DEV)
+        far[n][first * ps:] = t[n]
+    w = W.Workload("far", list(wl.q_lens), list(wl.kv_lens), Hq, Hkv, D, ps, wl.num_pages + first,
+                   (wl.page_table + first).astype(np.int32))
+    out, lse = run(w, far, prepared(w))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    for n in ("kp", "vp"):
+        assert torch.equal(far[n][first * ps:], near[n])
