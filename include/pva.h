@@ -347,7 +347,7 @@ PVA_API pva_status attn_append_rope(const pva_meta* meta, const pva_rope* rope, 
 /*
  * attn_forward (of the meta's pool type) with attn_append_rope in place of its store: one
  * layer's call from projections to attention output.  q_rot receives the rotated q (as q_out
- * above) and is what the attention reads; out must not overlap it.
+ * above) and is what the attention reads; an out that overlaps it is refused.
  */
 PVA_API pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k,
                              const void* v, void* q_rot, void* k_pool, void* v_pool, const float* k_scale,

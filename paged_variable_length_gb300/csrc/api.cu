@@ -596,6 +596,10 @@ pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope, const v
     if (h->total_tokens > 0 && (q == nullptr || q_rot == nullptr)) return PVA_ERR_INVALID_ARG;
     const pva_status st = check_rope(h, rope, q, k, v, q_rot, k_scale, v_scale);
     if (st != PVA_OK) return st;
+    // (rows of q_rot are read while others' results are written)
+    const uintptr_t bytes = (uintptr_t)h->total_tokens * h->cfg.num_qo_heads * h->cfg.head_dim * 2;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), r = reinterpret_cast<uintptr_t>(q_rot);
+    if (o < r + bytes && r < o + bytes) return PVA_ERR_INVALID_ARG;
     return forward_impl(h, q, k, v, k_pool, v_pool, k_scale, v_scale, out, lse, stream, rope, q_rot);
 }
 

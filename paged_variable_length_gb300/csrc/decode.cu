@@ -53,7 +53,6 @@
 
 #include <cfloat>
 
-#include "decode_common.cuh"
 #include "device_utils.cuh"
 #include "pva_internal.h"
 
@@ -64,6 +63,37 @@ constexpr int kMaxKvHeads = kDecHeadBlock;
 constexpr int kStageKeys = kDecKeysPerStage;  // 16
 constexpr int kRowPad = 16;                    // bytes between consecutive staged rows beyond Hkv*D*2
 constexpr float kLn2 = 0.69314718055994530942f;
+
+struct StageInfo {
+    int32_t unit, group, k, k1;
+    int32_t tok0, ntok, qpos0, nsplit;
+    int32_t pbase, split, flags, hb;
+    int32_t nparts, pad0, pad1, pad2;
+};
+constexpr int kFirst = 1, kLast = 2, kEnd = 4;
+
+struct DecSmemHead {
+    uint64_t full[8];
+    uint64_t empty[8];
+    StageInfo info[8];
+    int32_t abort_flag;
+};
+
+__device__ __forceinline__ void abort_cta(DecSmemHead* sh, uint32_t* err) {
+    sh->abort_flag = 1;
+    dev::set_error(err, kErrTimeout);
+}
+
+// A work wait of one whole warp (every lane calls it, converged): the lanes' results are
+// voted, so the warp leaves together or not at all (its next steps -- warp MMAs, fragment
+// loads, warp syncs -- need every lane); lane 0 records the abort.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit, DecSmemHead* sh,
+                                          uint32_t* err) {
+    if (__all_sync(0xffffffffu, dev::mbar_wait(bar, parity, limit))) return true;
+    if ((threadIdx.x & 31) == 0) abort_cta(sh, err);
+    __syncwarp();
+    return false;
+}
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(32 * (kMaxKvHeads + 1), 1)

@@ -26,7 +26,6 @@
 // Every wait is bounded, as in decode.cu.
 #include <cuda_runtime.h>
 
-#include "decode_common.cuh"
 #include "device_utils.cuh"
 #include "mxfp4.cuh"
 #include "pva_internal.h"
@@ -74,7 +73,7 @@ __device__ __forceinline__ uint32_t bitsel(uint32_t a, uint32_t b, uint32_t m) {
 
 // Bounded wait on a barrier that lets the hardware suspend the warp (up to 100 us at a time) until
 // the phase completes: 16 warps polling without the hint issued a third of the kernel's
-// instructions.  As warp_wait otherwise.
+// instructions.  The lanes' results are voted, so that the warp leaves together or not at all.
 __device__ __forceinline__ bool wait_suspended(uint64_t* bar, uint32_t parity, uint64_t limit, uint32_t* err) {
     bool ok;
     if (limit == 0) {
@@ -105,13 +104,20 @@ __device__ __forceinline__ bool wait_suspended(uint64_t* bar, uint32_t parity, u
 }
 
 // What the producers say of a stage: the unit it belongs to (its keys k .. min(k + stage, k1) - 1
-// are staged), its number in it, and the query rows of the unit after it (0 tokens: not known yet,
-// or none).
+// are staged), its number in it (index), and the query rows of the unit after it (0 tokens: not
+// known yet, or none).
 struct MxStage {
     int32_t k, k1, tok0, ntok;
     int32_t qpos0, nparts, slot, hb;  // slot: the unit's partial slot
     int32_t index, flags, next_tok0, next_ntok;
     int32_t next_hb, pad0, pad1, pad2;
+};
+
+constexpr int kFirst = 1, kLast = 2, kEnd = 4;  // MxStage::flags
+
+template <int I>
+struct IntTag {
+    static constexpr int value = I;
 };
 
 // The ring's barriers, and those by which a head's warps hand their results to its first.

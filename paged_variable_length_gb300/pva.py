@@ -217,14 +217,27 @@ def attn_store_kvcache_fp8kv(meta: Meta, k, v, k_pool, v_pool, k_scale, v_scale,
     _check(st, "attn_store_kvcache_fp8kv")
 
 
+def _strided(where: str) -> PvaError:
+    """Only q, k and v of a rotation may be strided (by token)."""
+    return PvaError(1, f"{where} (a strided tensor)")
+
+
 def attn_forward_mxfp4kv(meta: Meta, q, k, v, k_pool, v_pool, out, lse=None, stream=None) -> None:
     """attn_forward over MXFP4 pools (uint8 [slots, mxfp4_row_bytes] tensors)."""
+    if not ((q is None or q.is_contiguous()) and (k is None or k.is_contiguous())
+            and (v is None or v.is_contiguous()) and (k_pool is None or k_pool.is_contiguous())
+            and (v_pool is None or v_pool.is_contiguous()) and (out is None or out.is_contiguous())
+            and (lse is None or lse.is_contiguous())):
+        raise _strided("attn_forward_mxfp4kv")
     st = load().attn_forward_mxfp4kv(ctypes.byref(meta), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
                                      _ptr(out), _ptr(lse), _stream(stream))
     _check(st, "attn_forward_mxfp4kv")
 
 
 def attn_store_kvcache_mxfp4kv(meta: Meta, k, v, k_pool, v_pool, stream=None) -> None:
+    if not ((k is None or k.is_contiguous()) and (v is None or v.is_contiguous())
+            and (k_pool is None or k_pool.is_contiguous()) and (v_pool is None or v_pool.is_contiguous())):
+        raise _strided("attn_store_kvcache_mxfp4kv")
     st = load().attn_store_kvcache_mxfp4kv(ctypes.byref(meta), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
                                            _stream(stream))
     _check(st, "attn_store_kvcache_mxfp4kv")
@@ -232,6 +245,9 @@ def attn_store_kvcache_mxfp4kv(meta: Meta, k, v, k_pool, v_pool, stream=None) ->
 
 def attn_load_kvcache_mxfp4kv(meta: Meta, k_pool, v_pool, k, v, stream=None) -> None:
     """The values the pools hold at the batch's new tokens' slots, into bf16 k / v [T, Hkv, D]."""
+    if not ((k_pool is None or k_pool.is_contiguous()) and (v_pool is None or v_pool.is_contiguous())
+            and (k is None or k.is_contiguous()) and (v is None or v.is_contiguous())):
+        raise _strided("attn_load_kvcache_mxfp4kv")
     st = load().attn_load_kvcache_mxfp4kv(ctypes.byref(meta), _ptr(k_pool), _ptr(v_pool), _ptr(k), _ptr(v),
                                           _stream(stream))
     _check(st, "attn_load_kvcache_mxfp4kv")
@@ -301,6 +317,9 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
 def attn_append_rope(meta: Meta, rope: Rope, q, k, v, q_out, k_pool, v_pool, k_scale=None, v_scale=None,
                      stream=None) -> None:
     """q rotated into q_out, k rotated and stored, v stored; q, k, v may be strided by token."""
+    if not ((q_out is None or q_out.is_contiguous()) and (k_pool is None or k_pool.is_contiguous())
+            and (v_pool is None or v_pool.is_contiguous())):
+        raise _strided("attn_append_rope")
     args = rope.args(q, k, v)
     st = load().attn_append_rope(ctypes.byref(meta), ctypes.byref(args), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out),
                                  _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _stream(stream))
@@ -310,6 +329,10 @@ def attn_append_rope(meta: Meta, rope: Rope, q, k, v, q_out, k_pool, v_pool, k_s
 def attn_forward_rope(meta: Meta, rope: Rope, q, k, v, q_rot, k_pool, v_pool, out, lse=None, k_scale=None,
                       v_scale=None, stream=None) -> None:
     """attn_append_rope, then the attention of the rotated q."""
+    if not ((q_rot is None or q_rot.is_contiguous()) and (k_pool is None or k_pool.is_contiguous())
+            and (v_pool is None or v_pool.is_contiguous()) and (out is None or out.is_contiguous())
+            and (lse is None or lse.is_contiguous())):
+        raise _strided("attn_forward_rope")
     args = rope.args(q, k, v)
     st = load().attn_forward_rope(ctypes.byref(meta), ctypes.byref(args), _ptr(q), _ptr(k), _ptr(v), _ptr(q_rot),
                                   _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse),
@@ -391,6 +414,9 @@ class PagedAttention:
         nbytes = attn_workspace_size(self.cfg)
         if nbytes == 0:
             raise PvaError(2, "attn_workspace_size")
+        self._mx_pool_bytes = 0
+        if kv_dtype == KV_MXFP4:
+            self._mx_pool_bytes = num_pages * page_size * mxfp4_row_bytes(num_kv_heads, head_dim)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.meta = None
         self._keep = None
@@ -405,6 +431,22 @@ class PagedAttention:
                                           total_tokens, max_q_len, self.workspace, stream)
         return self.meta
 
+    def _check_pools(self, k_pool, v_pool) -> None:
+        n = self._mx_pool_bytes
+        if k_pool.numel() < n or v_pool.numel() < n:  # (uint8)
+            raise PvaError(1, f"an MXFP4 pool of fewer than {n} bytes (mxfp4_row_bytes a slot)")
+
+    @staticmethod
+    def _empty(shape, like, stream):
+        """A bf16 tensor of the stream that writes it (so that its memory, once let go, is not given to
+        another stream's work while that one still runs)."""
+        import torch
+
+        if stream is None:
+            return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+            return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+
     def forward(self, q, k, v, k_pool, v_pool, out=None, lse=None, stream=None, k_scale=None, v_scale=None,
                 rope: Rope | None = None, q_rot=None):
         """One layer.  With an E4M3 config the pools are uint8 and k_scale / v_scale (fp32 [Hkv],
@@ -415,9 +457,11 @@ class PagedAttention:
 
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if self._mx_pool_bytes:
+            self._check_pools(k_pool, v_pool)
         if rope is not None:
             if q_rot is None:
-                q_rot = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_rot = self._empty(q.shape, q, stream)
             attn_forward_rope(self.meta, rope, q, k, v, q_rot, k_pool, v_pool, out, lse, k_scale, v_scale, stream)
         elif self.cfg.kv_dtype == KV_E4M3:
             attn_forward_fp8kv(self.meta, q, k, v, k_pool, v_pool, k_scale, v_scale, out, lse, stream)
@@ -430,15 +474,17 @@ class PagedAttention:
     def append(self, q, k, v, k_pool, v_pool, rope: Rope, q_out=None, k_scale=None, v_scale=None, stream=None):
         """attn_append_rope of one layer; returns the rotated q (q_out, a new tensor when None; None
         without q)."""
-        import torch
-
+        if self._mx_pool_bytes:
+            self._check_pools(k_pool, v_pool)
         if q_out is None and q is not None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = self._empty(q.shape, q, stream)
         attn_append_rope(self.meta, rope, q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, stream)
         return q_out
 
     def store(self, k, v, k_pool, v_pool, k_scale=None, v_scale=None, stream=None) -> None:
         """store_kvcache of one layer, into pools of the config's type."""
+        if self._mx_pool_bytes:
+            self._check_pools(k_pool, v_pool)
         if self.cfg.kv_dtype == KV_E4M3:
             attn_store_kvcache_fp8kv(self.meta, k, v, k_pool, v_pool, k_scale, v_scale, stream)
         elif self.cfg.kv_dtype == KV_MXFP4:
@@ -448,10 +494,10 @@ class PagedAttention:
 
     def load(self, k_pool, v_pool, k=None, v=None, stream=None):
         """What MXFP4 pools hold at the batch's new tokens' slots, as bf16 (k, v) [T, Hkv, D]."""
-        import torch
-
+        if self._mx_pool_bytes:
+            self._check_pools(k_pool, v_pool)
         shape = (self.total_tokens, self.cfg.num_kv_heads, self.cfg.head_dim)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if v is None else v
+        k = self._empty(shape, k_pool, stream) if k is None else k
+        v = self._empty(shape, k_pool, stream) if v is None else v
         attn_load_kvcache_mxfp4kv(self.meta, k_pool, v_pool, k, v, stream)
         return k, v

@@ -325,3 +325,57 @@ def test_append_captured_with_the_plan_and_replayed():
         torch.cuda.synchronize()
         for i in range(2):
             assert torch.equal(got[0][i], outs[i]) and torch.equal(got[1][i], layers[i][0])
+
+
+def test_forward_rope_refuses_an_output_over_the_rotated_q():
+    wl = W.custom([3, 1], [10, 1], 8, 2, 64, 4, seed=3)
+    eng, (q, k, v, q_out, kp, vp, _, _, rope) = check_append(wl, BF16, 64)
+    room = torch.zeros(2, *q_out.shape, dtype=torch.bfloat16, device=DEV).view(-1)
+    n, was = q_out.numel(), kp.clone()
+    q_rot = room[:n].view(q_out.shape)
+    for at in (0, 8, n - 8):
+        with pytest.raises(pva.PvaError) as e:
+            eng.forward(q, k, v, kp, vp, out=room[at:at + n].view(q_out.shape), rope=rope, q_rot=q_rot)
+        assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert torch.equal(kp.view(torch.int16), was.view(torch.int16)) and not bool(room.any())
+    eng.forward(q, k, v, kp, vp, out=room[n:].view(q_out.shape), rope=rope, q_rot=q_rot)   # side by side
+    torch.cuda.synchronize()
+    assert torch.equal(q_rot, q_out)
+
+
+def test_outputs_of_calls_on_another_stream():
+    """Tensors that the binding allocates belong to the stream that writes them."""
+    wl = W.custom([1, 300], [1, 300], 16, 4, 128, 16, seed=3)
+    eng, (q, k, v, q_out, kp, vp, _, _, rope) = check_append(wl, MX, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        got = eng.append(q, k, v, kp, vp, rope, stream=stream)
+        k2, v2 = eng.load(kp, vp, stream=stream)
+        out = torch.empty_like(q)
+        eng.forward(q, k, v, kp, vp, out=out, rope=rope, stream=stream)
+        noise = torch.empty_like(q).fill_(3.0)   # current stream: must not be given the rotated q's memory
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got, q_out) and bool(torch.isfinite(out.float()).all()) and bool((noise == 3.0).all())
+        assert torch.equal(eng.load(kp, vp)[0], k2) and torch.equal(eng.load(kp, vp)[1], v2)
+        torch.cuda.synchronize()
+
+
+def test_binding_refuses_strided_outputs_and_short_pools():
+    wl = W.custom([3, 1], [10, 1], 8, 2, 64, 4, seed=3)
+    eng, (q, k, v, q_out, kp, vp, _, _, rope) = check_append(wl, MX, 64)
+    wide = torch.empty(wl.total_tokens, 8, 128, dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: eng.append(q, k, v, kp, vp, rope, q_out=wide[..., :64]),
+                 lambda: eng.forward(q, k, v, kp, vp, out=wide[..., 64:], rope=rope),
+                 lambda: eng.forward(wide[..., :64], k, v, kp, vp),
+                 lambda: eng.load(kp, vp, k=wide[:, :2, :64], v=v.clone()),
+                 lambda: eng.store(wide[:, :2, :64], v, kp, vp),
+                 lambda: eng.store(k, v, kp[:-1], vp),
+                 lambda: eng.append(q, k, v, kp, vp[1:], rope),
+                 lambda: eng.load(kp[:0], vp),
+                 lambda: eng.forward(q, k, v, kp[:4], vp, rope=rope)):
+        with pytest.raises(pva.PvaError) as e:
+            call()
+        assert e.value.status == 1
