@@ -75,8 +75,10 @@ __device__ __forceinline__ int token_index(const ForwardParams& p, int batch, in
 //   kSplit  half-split pairs over the whole head: a lane has both elements of its 8 pairs;
 //   kInter  interleaved pairs: 4 in each chunk;
 //   kPart   half-split pairs over part of the head: a pair's other element lies rot/2 away, in
-//           another lane of the row, and comes by shuffle.
-constexpr int kNone = 0, kSplit = 1, kInter = 2, kPart = 3;
+//           another lane of the row, and comes by shuffle;
+//   kLow    the same where rot <= D/2: only the lane's first chunk turns, half the cosines, sines
+//           and shuffles (the 4-bit append and read-back of 9 k tokens, rot = D/2: 46.5 us, 54.5 as kPart).
+constexpr int kNone = 0, kSplit = 1, kInter = 2, kPart = 3, kLow = 4;
 
 // x c + z s, every product and the sum rounded by itself.  (As packed pairs the assembler contracts
 // a product and the sum into one rounding, explicit roundings or not.)
@@ -151,9 +153,11 @@ __device__ __forceinline__ void store_mx(uint8_t* row, const float (&y)[16], int
 }
 
 // KV: PVA_KV_BF16, PVA_KV_E4M3 or PVA_KV_MXFP4.  R: row steps a warp takes (each 512 elements);
-// a warp serves one token.
+// a warp serves one token.  (kPart alone needs its registers bounded: five blocks an SM, 52.8 us for
+// the append and read-back above with rot = 3/4 D, against 56.0 unbounded and 58.6 at six; 0 leaves
+// the others unbounded, a bound of 1 cost the bf16 append 5 us.)
 template <int D, int KV, int MODE, int R>
-__global__ void __launch_bounds__(kThreads) append_kernel(const ForwardParams p, const RopeParams rp) {
+__global__ void __launch_bounds__(kThreads, MODE == kPart ? 5 : 0) append_kernel(const ForwardParams p, const RopeParams rp) {
     constexpr int LR = D / 16;   // lanes of a head row
     constexpr int RW = 32 / LR;  // head rows of a step
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
@@ -192,9 +196,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const ForwardParams p,
     if (errors & kErrFatal) return;
     const int index = MODE != kNone || p.slots == nullptr ? token_index(p, rp.batch, t, req) : 0;
     const int64_t slot = row0 + R * RW > Hq ? token_slot(p, t, req, index, &hdr->error_bits, lane == 0) : -1;
-    // cosines and sines: of the lane's 8 pairs (kInter: 4 of each chunk), or of its 16 elements (kPart)
+    // cosines and sines: of the lane's 8 pairs (kInter: 4 of each chunk), or of its elements that may
+    // turn (kPart: 16, kLow: the first 8)
     constexpr int NC = MODE == kPart ? 16 : 8;
-    const int rot = rp.rot_dim, half = rot / 16;  // half: chunks between the elements of a kPart pair
+    const int rot = rp.rot_dim, half = rot / 16;  // half: chunks between the elements of a kPart or kLow pair
     float c[NC], s[NC];
     if constexpr (MODE != kNone) {
         const int pos = rp.positions != nullptr ? rp.positions[t] : index;
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const ForwardParams p,
                 take(4, 8 * j + 4);
             } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < (MODE == kLow ? 1 : 2); ++h) {
                     const int ch = j + h * LR;
                     if (8 * ch >= rot) continue;
                     if constexpr (MODE == kInter) {
@@ -257,9 +262,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const ForwardParams p,
                 x[2 * i] = turn(u, c[i], w, -s[i]);
                 x[2 * i + 1] = turn(w, c[i], u, s[i]);
             }
-        } else if constexpr (MODE == kPart) {
+        } else if constexpr (MODE == kPart || MODE == kLow) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < (MODE == kLow ? 1 : 2); ++h) {
                 const int ch = j + h * LR;
                 const int other = ch < half ? ch + half : ch < 2 * half ? ch - half : ch;  // the pair's chunk
                 const uint32_t wa[4] = {(uint32_t)a[r].x, (uint32_t)a[r].y, (uint32_t)a[r].z, (uint32_t)a[r].w};
@@ -267,8 +272,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const ForwardParams p,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t oa = __shfl_sync(0xffffffffu, wa[i], sub * LR + other % LR);
-                    const uint32_t ob = __shfl_sync(0xffffffffu, wb[i], sub * LR + other % LR);
-                    const uint32_t o = other < LR ? oa : ob;
+                    const uint32_t ob = MODE == kPart ? __shfl_sync(0xffffffffu, wb[i], sub * LR + other % LR) : 0;
+                    const uint32_t o = MODE == kLow || other < LR ? oa : ob;
                     const int e = 8 * h + 2 * i;
                     if (turned && 8 * ch < rot) {
                         x[e] = turn(x[e], c[e], __uint_as_float(o << 16), s[e]);
@@ -373,7 +378,7 @@ cudaError_t launch_kv(const ForwardParams& p, const RopeParams& rp, cudaStream_t
     if (rp.rot_dim == 0) return launch_mode<D, KV, kNone>(p, rp, s);
     if (rp.interleaved) return launch_mode<D, KV, kInter>(p, rp, s);
     if (rp.rot_dim == D) return launch_mode<D, KV, kSplit>(p, rp, s);
-    return launch_mode<D, KV, kPart>(p, rp, s);
+    return 2 * rp.rot_dim <= D ? launch_mode<D, KV, kLow>(p, rp, s) : launch_mode<D, KV, kPart>(p, rp, s);
 }
 
 template <int D>
