@@ -272,10 +272,10 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
     if (warp >= 8) {
         // control warpgroups: give registers to the softmax warpgroups
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kRegsCtrl));
-    if (warp >= kProducerWarp0 && warp < kProducerWarp0 + R::kProducers) {
+    if (warp >= kProducerWarp0 && (!R::kWide || warp < kProducerWarp0 + R::kProducers)) {
         // ============================================================== producer (cp.async gathers)
-        // The three producer warps (MXFP4: six, see there) move the rows of every Q / K / V tile: a row is one kv
-        // head of one slot (or one q head of one token), D*2 bytes, copied as 16-byte async
+        // The three producer warps (MXFP4: six, see there) move the rows of every Q / K / V tile: a
+        // row is one kv head of one slot (or one q head of one token), D*2 bytes, copied as 16-byte async
         // copies into the 128-byte-swizzled layout the MMA descriptors expect.  Q rows that
         // are gathered (shared-prefix members, or Q without a tensor map): the lanes of a
         // copy instruction take consecutive 16-byte chunks of kRowsPerCopy whole rows, so
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         // and lane + 32, -1 for a row that is not copied
         // table entry of row index k: the rows one lane copies (k = i * kRowsPerCopy + sub)
         // sit next to each other, so that the unrolled copy loop reads them as vectors
-        int64_t* offs = reinterpret_cast<int64_t*>(smem + L::kOff) + (pwarp % 3) * 64;
+        int64_t* offs = reinterpret_cast<int64_t*>(smem + L::kOff) + (R::kWide ? pwarp % 3 : pwarp) * 64;
         auto slot_of = [](int k) { return (k % kRowsPerCopy) * kCopyIters + k / kRowsPerCopy; };
         auto copy_tile = [&](uint8_t* tile, int64_t o0, int64_t o1, const uint16_t* base) {
             __syncwarp();  // the previous tile's copy loop has read the table
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                     }
                     tma_pending = uc & 1;
                 }
-            } else if (pwarp < 3)
+            } else if (!R::kWide || pwarp < 3)
             for (int h = 0; h < 2; ++h) {
                 const int ntok = h ? pt.ntok1 : pt.ntok0;
                 int64_t oq[2];
@@ -865,14 +865,19 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
             if (lane == 0) dev::mbar_arrive(&b->q_full);
             return true;
         };
-        int u = queue_read(b, 0, lane, wlim, err);
-        if (F8 && u >= 0 && !convert_q(0)) u = -1;
+        int u = -1;
+        if constexpr (F8) {
+            u = queue_read(b, 0, lane, wlim, err);
+            if (u >= 0 && !convert_q(0)) u = -1;
+        }
         for (int k = 0;; ++k) {
+            if constexpr (!F8) u = queue_read(b, k, lane, wlim, err);
             if (u < 0 || b->abort_flag) break;
             const PreTile pt = units[u];
             const UnitView uv = unit_view(pt);
             const int ntok = h ? pt.ntok1 : pt.ntok0;
             const int nk = uv.nk[h];
+            if (!F8 && nk == 0) continue;
             const float sl = MX ? sl_base * q_scale : F8 ? sl_base * p.k_scale[pt.kvh] : sl_base;
             const bool valid = row < ntok * G;
             // last visible key of this row, and the first key some row may not see
@@ -974,8 +979,8 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
             if constexpr (F8) {
                 u = queue_read(b, k + 1, lane, wlim, err);
                 if (u >= 0 && !convert_q(k + 1)) break;
+                if (nk == 0) continue;
             }
-            if (nk > 0) {
             // ---- epilogue: O / l -> bf16 rows of out, LSE
             if (!wait_or_abort(&b->o_ready[h], n_u & 1, wlim, b, err)) break;
             tc::fence_after_sync();
@@ -1028,8 +1033,6 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                 if (p.lse != nullptr)
                     p.lse[orow] = l > 0.f ? (m + (__log2f(l) - kPUp)) * kLn2 : (MX && l != 0.f ? l : -INFINITY);
             }
-            }
-            if constexpr (!F8) u = queue_read(b, k + 1, lane, wlim, err);
         }
     }
     tc::fence_before_sync();
