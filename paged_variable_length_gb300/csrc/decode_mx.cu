@@ -387,9 +387,10 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
             g_cur = g_next;
         }
     producer_done:
-        // every copy issued must land before the CTA may exit
+        // every copy issued must land before the CTA may exit.  (Where another producer gave up, a stage's
+        // phase cannot complete: one such wait is long enough for all copies.)
         for (int s = 0; s < stages; ++s)
-            if (armed & (1u << s)) (void)dev::mbar_wait(&sh->full[s], (armed_par >> s) & 1u);
+            if ((armed & (1u << s)) && !dev::mbar_wait(&sh->full[s], (armed_par >> s) & 1u)) break;
         if (wait_late) dev::grid_dep_wait();
         return;
     }

@@ -476,3 +476,35 @@ def test_pools_past_4_gib():
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     for n in ("kp", "vp"):
         assert torch.equal(far[n][first * ps:], near[n])
+
+
+def test_bad_pages_of_a_prefill_are_reported():
+    """Page ids outside the pool among the keys of a chunk and of a prefill: flagged, the others' results
+    as they were."""
+    for D, ps in ((64, 1), (128, 16)):
+        wl = W.custom([40, 150, 70], [300, 150, 200], 8, 2, D, ps, seed=3)
+        t = make(wl)
+        ref, _ = run(wl, {n: x.clone() for n, x in t.items()}, prepared(wl))
+        wl.page_table[0, 2] = wl.num_pages + 5
+        wl.page_table[0, 4] = -1
+        eng = prepared(wl)
+        out = torch.zeros_like(t["q"])
+        eng.forward(t["q"], t["k"], t["v"], t["kp"], t["vp"], out=out)
+        assert pva.attn_get_device_status(eng.meta) == 0x04
+        assert torch.equal(out[40:], ref[40:])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps,ql,kl", [(16, 16, 64, 1, [1] * 4, [3000, 2000, 40, 999]),
+                                               (48, 24, 128, 2, [1] * 3, [700, 33, 1000]),
+                                               (16, 1, 128, 1, [1] * 3, [700, 33, 1000])],
+                         ids=["slots", "head-blocks", "one-head"])
+def test_waits_of_several_producers_that_run_out(Hq, Hkv, D, ps, ql, kl):
+    wl = W.custom(ql, kl, Hq, Hkv, D, ps, seed=3)
+    t = make(wl, 3)
+    eng = prepared(wl)
+    pva.attn_debug_set_wait_limit(eng.meta, 0)
+    eng.forward(t["q"], t["k"], t["v"], t["kp"], t["vp"], out=torch.zeros_like(t["q"]))
+    assert pva.attn_get_device_status(eng.meta) & 0x20
+    eng = prepared(wl)
+    out, lse = run(wl, t, eng)
+    check(wl, t, out, lse)
