@@ -274,7 +274,6 @@ class Rope:
         if rot_dim is not None and rot_dim != cos_sin.shape[1]:
             raise ValueError(f"cos_sin has {cos_sin.shape[1]} columns, rot_dim is {rot_dim}")
         self.cos_sin = cos_sin
-        self._cos_sin_ptr = cos_sin.data_ptr()
         self.max_positions, self.rot_dim = (int(n) for n in cos_sin.shape)
         self.interleaved = bool(interleaved)
         self.set_positions(positions)
@@ -291,7 +290,7 @@ class Rope:
         pos = self.positions
         if pos is not None and pos.numel() != k.shape[0]:
             raise ValueError(f"{pos.numel()} positions for {k.shape[0]} tokens")
-        return RopeArgs(self._cos_sin_ptr, None if pos is None else pos.data_ptr(),
+        return RopeArgs(self.cos_sin.data_ptr(), None if pos is None else pos.data_ptr(),
                         0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
                         self.max_positions, self.rot_dim, self.interleaved, 0)
 
@@ -444,7 +443,9 @@ class PagedAttention:
 
         if stream is None:
             return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
 
     def forward(self, q, k, v, k_pool, v_pool, out=None, lse=None, stream=None, k_scale=None, v_scale=None,

@@ -350,7 +350,7 @@ def test_outputs_of_calls_on_another_stream():
     eng, (q, k, v, q_out, kp, vp, _, _, rope) = check_append(wl, MX, 128)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    for stream in (side, side.cuda_stream):
+    for stream in (side, side.cuda_stream, 0):
         got = eng.append(q, k, v, kp, vp, rope, stream=stream)
         k2, v2 = eng.load(kp, vp, stream=stream)
         out = torch.empty_like(q)
