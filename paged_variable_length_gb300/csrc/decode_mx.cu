@@ -694,7 +694,9 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
         release(stage);  // the unit's last
         advance();
         const int parts = min(KW, si.index + 1);  // warps that had a stage of the unit
-        if (kQAhead && (!have_q || !mine)) {
+        if (!kQAhead) {
+            have_q = false;  // (a warp without a stage of the unit still holds its rows)
+        } else if (!have_q || !mine) {
             have_q = si.next_ntok > 0;
             if (have_q) load_q(si.next_tok0, si.next_ntok, si.next_hb);
         }

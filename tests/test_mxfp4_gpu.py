@@ -508,3 +508,15 @@ def test_waits_of_several_producers_that_run_out(Hq, Hkv, D, ps, ql, kl):
     eng = prepared(wl)
     out, lse = run(wl, t, eng)
     check(wl, t, out, lse)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(16, 1, 128, 32), (16, 1, 64, 16), (64, 4, 128, 16), (24, 2, 64, 1), (4, 1, 128, 4),
+                                         (8, 2, 64, 8), (32, 8, 128, 16)])
+def test_many_units_a_cta_of_unlike_lengths(Hq, Hkv, D, ps):
+    """CTAs that take several units, some too short for all of a head's warps, before longer ones."""
+    rng = np.random.default_rng(Hq + D)
+    kl = [int(x) for x in rng.choice([1, 20, 33, 64, 65, 130, 300, 700, 1500], 330)]
+    eng, _ = full_case(W.custom([1] * len(kl), kl, Hq, Hkv, D, ps, seed=ps))
+    assert pva.attn_debug_plan_counts(eng.meta)["dec_units"] > 330
+    full_case(W.custom([1] * len(kl), kl, Hq, Hkv, D, ps, seed=ps), enable_split_kv=False)
+    full_case(W.custom([1] * len(kl), kl, Hq, Hkv, D, ps, seed=ps), max_q_len=1)   # (one tile of query rows)
