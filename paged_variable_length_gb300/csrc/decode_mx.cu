@@ -26,6 +26,8 @@
 // Every wait is bounded, as in decode.cu.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "device_utils.cuh"
 #include "mxfp4.cuh"
 #include "pva_internal.h"
@@ -157,7 +159,9 @@ struct MxWarps {
 // D: head dim.  NQ: n8 tiles of query rows (rows of the batch's decode groups <= 8 NQ).  HBT: heads
 // of the CTA, 0: not known at compile time.  (A known row size makes the fragment addresses of a
 // stage one register and constants; computed, they were a quarter of the loop's instructions.)
-template <int D, int NQ, int HBT>
+// MULTI: decode groups may hold several tokens, which see different keys (without: 47.8 us for 64 decodes,
+// 48.9 with).
+template <int D, int NQ, int HBT, bool MULTI>
 __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(const ForwardParams p, const MxShape sp) {
     using MW = MxWarps<D, NQ>;
     const bool shared_copies = sp.producers > 1;
@@ -490,6 +494,38 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
         }
     };
 
+    // Rows of several tokens see different keys, and a hidden key's weight 0 times a NaN block of V would
+    // reach them all.  So in a part with the diagonal (n keys from key k, of stage st from `at` on) the NaN
+    // blocks of the head become zeros in the stage, and the rows that see the first of a block's (every row
+    // from its token on) take their NaN now: a sum that is one stays one.
+    auto hide_nan = [&](int st, int at, int k, int n) {
+        using Word = std::conditional_t<NB == 4, uint32_t, uint16_t>;  // a key's scale bytes
+        uint8_t* e = ring + st * stage_bytes + (kKeys + at) * stride + scale_at;
+        bool any = false;
+        for (int x = lane; x < n; x += 32) any |= __vcmpeq4(*reinterpret_cast<Word*>(e + x * stride), 0xFFFFFFFFu) != 0;
+        if (!__any_sync(0xffffffffu, any)) return;
+        const uint8_t* mine = e + gq * (D / 8) / mx::kBlock;  // of the lane's dims
+        int first = 0;
+        while (first < n && mine[first * stride] != mx::kScaleNan) ++first;
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (first == n || k + first > lim[nq][i]) continue;
+#pragma unroll
+                for (int t = 0; t < OT; ++t) o[t][nq][i] = o[t][nq][2 + i] = __int_as_float(0x7FFFFFFF);
+            }
+        }
+        __syncwarp();  // every lane has looked
+        for (int x = lane; x < n; x += 32) {
+            Word* w = reinterpret_cast<Word*>(e + x * stride);
+            *w &= (Word)~__vcmpeq4(*w, 0xFFFFFFFFu);
+        }
+        // (these stores come before the copy that fills the stage again)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+    };
+
     while (true) {
         // the unit's first stage
         if (!wait_suspended(&sh->full[stage], phase, wlim, err)) return;
@@ -562,6 +598,7 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
                             if (mt * 16 > end) s[mt][n][e] = -INFINITY;
                     }
                 }
+                if (MULTI && si.ntok > 1) hide_nan(cur, at, k, min(kPart, k1 - k));
             }
 
             // ---- online softmax: P^T as f16, transposed to the next product's operand
@@ -926,7 +963,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const ForwardPara
     }
 }
 
-template <int D, int NQ, int HBT>
+template <int D, int NQ, int HBT, bool MULTI>
 cudaError_t launch_h(const ForwardParams& p, int producers, int ctas, cudaStream_t s) {
     const int Hkv = p.num_kv_heads;
     MxShape sp{};
@@ -952,18 +989,18 @@ cudaError_t launch_h(const ForwardParams& p, int producers, int ctas, cudaStream
     static int launch_regs = -1;
     if (launch_regs < 0) {
         cudaFuncAttributes attr{};
-        const cudaError_t ea = cudaFuncGetAttributes(&attr, decode_mx_kernel<D, NQ, HBT>);
+        const cudaError_t ea = cudaFuncGetAttributes(&attr, decode_mx_kernel<D, NQ, HBT, MULTI>);
         if (ea != cudaSuccess) return ea;
         launch_regs = attr.numRegs;
     }
     if (launch_regs != MxWarps<D, NQ>::kRegsLaunch) return cudaErrorInvalidConfiguration;
     const cudaError_t e =
-        cudaFuncSetAttribute(decode_mx_kernel<D, NQ, HBT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(decode_mx_kernel<D, NQ, HBT, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_programmatic(decode_mx_kernel<D, NQ, HBT>, (unsigned)ctas, (unsigned)MxWarps<D, NQ>::kThreads, smem, s, p, sp);
+    return launch_programmatic(decode_mx_kernel<D, NQ, HBT, MULTI>, (unsigned)ctas, (unsigned)MxWarps<D, NQ>::kThreads, smem, s, p, sp);
 }
 
-template <int D>
+template <int D, bool MULTI>
 cudaError_t launch_dec(const ForwardParams& p, int ctas, cudaStream_t s) {
     const int hb = decode_mx_heads(p.num_kv_heads, D, p.dec_rows);
     // One warp issues a bulk copy in about 70 cycles whatever its size, so copies of one or a few
@@ -973,16 +1010,16 @@ cudaError_t launch_dec(const ForwardParams& p, int ctas, cudaStream_t s) {
     const int run = hb < p.num_kv_heads ? mx_stride(hb, D) : p.page_size * p.mx_row_bytes;
     const int producers = run < 2048 ? 4 : 1;
     if (p.dec_rows > 8)
-        return hb == 8 ? launch_h<D, 2, 8>(p, producers, ctas, s) : launch_h<D, 2, 0>(p, producers, ctas, s);
+        return hb == 8 ? launch_h<D, 2, 8, MULTI>(p, producers, ctas, s) : launch_h<D, 2, 0, MULTI>(p, producers, ctas, s);
     switch (hb) {
-        case 1: return launch_h<D, 1, 1>(p, producers, ctas, s);
-        case 2: return launch_h<D, 1, 2>(p, producers, ctas, s);
-        case 4: return launch_h<D, 1, 4>(p, producers, ctas, s);
-        case 8: return launch_h<D, 1, 8>(p, producers, ctas, s);
+        case 1: return launch_h<D, 1, 1, MULTI>(p, producers, ctas, s);
+        case 2: return launch_h<D, 1, 2, MULTI>(p, producers, ctas, s);
+        case 4: return launch_h<D, 1, 4, MULTI>(p, producers, ctas, s);
+        case 8: return launch_h<D, 1, 8, MULTI>(p, producers, ctas, s);
     }
     if constexpr (D == 64)
-        if (hb == 16) return launch_h<D, 1, 16>(p, producers, ctas, s);
-    return launch_h<D, 1, 0>(p, producers, ctas, s);
+        if (hb == 16) return launch_h<D, 1, 16, MULTI>(p, producers, ctas, s);
+    return launch_h<D, 1, 0, MULTI>(p, producers, ctas, s);
 }
 
 }  // namespace
@@ -1000,8 +1037,9 @@ cudaError_t launch_join_mx(const ForwardParams& p, int head_dim, int ctas, cudaS
 }
 
 cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s) {
-    if (head_dim == 128) return launch_dec<128>(p, ctas, s);
-    if (head_dim == 64) return launch_dec<64>(p, ctas, s);
+    const bool multi = p.dec_rows > p.group;
+    if (head_dim == 128) return multi ? launch_dec<128, true>(p, ctas, s) : launch_dec<128, false>(p, ctas, s);
+    if (head_dim == 64) return multi ? launch_dec<64, true>(p, ctas, s) : launch_dec<64, false>(p, ctas, s);
     return cudaErrorInvalidValue;
 }
 
