@@ -293,6 +293,8 @@ PVA_API pva_status attn_store_kvcache_fp8kv(const pva_meta* meta, const void* k,
  *   q, k, v, out, lse as for attn_forward
  * Attention reads each element as code * scale, otherwise exactly as attn_forward.  The new
  * tokens' own keys and values are read back from the pool, quantised like all others.
+ * A key that a token does not see has no part in its output, whatever it holds: a NaN block of
+ * V makes the block's dims NaN in the tokens that see it, and changes no others.
  */
 PVA_API pva_status attn_forward_mxfp4kv(const pva_meta* meta, const void* q, const void* k, const void* v, void* k_pool,
                                 void* v_pool, void* out, float* lse, void* stream);

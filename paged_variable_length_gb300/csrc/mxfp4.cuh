@@ -96,6 +96,14 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float* x, float f) {
 // elements become 0 * inf = NaN).
 __device__ __forceinline__ float scale_f32(uint32_t e) { return __uint_as_float(e << 23); }
 
+// A block scale as an f16 pair (exact for every scale the store writes); a NaN block's becomes f16's
+// maximum, which leaves the block's codes zeros.
+__device__ __forceinline__ uint32_t scale_f16x2_finite(uint32_t e) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(scale_f32(e)));
+    return r;
+}
+
 // The NB scale bytes of a head (2 or 4, a row's address) -> fp32; 255 -> NaN.
 template <int NB>
 __device__ __forceinline__ void scales_f32(const uint8_t* at, float (&f)[NB]) {

@@ -44,6 +44,7 @@
 #include <cuda.h>  // CUtensorMap and the tensor-map encoder's types (resolved through the runtime)
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstring>
 #include <mutex>
 
@@ -111,6 +112,10 @@ struct Bars {
     uint32_t tmem_base;
     int32_t abort_flag;
     uint64_t wait_limit;  // of the work waits (the drains before the CTA leaves: the default)
+    // MXFP4: the units whose staged scales may say NaN (past kNanUnits only their number counts on), and
+    // uc + 1 in entry uc & 3 once unit uc is among them (producer warps are a unit or two apart at most)
+    static constexpr int kNanUnits = 32;
+    int32_t nan_units[kNanUnits], n_nan, nan_noted[4];
 };
 
 // A work wait of one whole warp (every lane calls it, converged): the lanes' results are
@@ -190,6 +195,51 @@ __device__ __forceinline__ UnitView unit_view(const PreTile& pt) {
     return v;
 }
 
+// MXFP4: the NaN of a unit's results, whose NaN blocks entered the products as zeros (a hidden key's weight 0
+// would meet a NaN in every row of the tile).  What a row sees ends at its diagonal, so the first key with
+// a NaN block of K, and of each block of V, says which of its results are NaN.  By the eight softmax
+// warps, a row a thread, each warp looking through its tile's keys; after the unit's results were written.
+template <int D>
+__device__ void fix_nan(const ForwardParams& p, const PreTile& pt, const CascGroup* cgroups, const int2* cmembers) {
+    constexpr int NB = D / mx::kBlock;
+    const UnitView uv = unit_view(pt);
+    const int h = threadIdx.x >> 7, lane = threadIdx.x & 31, G = p.group, TM = kPreRows / G;
+    const int32_t* prow = p.page_table + (int64_t)(uv.casc ? cgroups[-1 - pt.req].leader : pt.req) * p.ld;
+    const int scales = mx::scales_at(pt.kvh, p.num_kv_heads, D);
+    int first[1 + NB];
+#pragma unroll
+    for (int i = 0; i <= NB; ++i) first[i] = INT_MAX;
+    for (int key = uv.key_base + lane; key < uv.end[h] && uv.nk[h] > 0; key += 32) {
+        int64_t page = prow[key >> p.page_shift];
+        if (page < 0 || page >= p.num_pages) page = 0;  // (as the producers read it)
+        const int64_t at = ((page << p.page_shift) + (key & (p.page_size - 1))) * p.mx_row_bytes + scales;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            if (reinterpret_cast<const uint8_t*>(p.k_pool)[at + i] == mx::kScaleNan) first[0] = min(first[0], key);
+            if (reinterpret_cast<const uint8_t*>(p.v_pool)[at + i] == mx::kScaleNan) first[1 + i] = min(first[1 + i], key);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i <= NB; ++i) first[i] = __reduce_min_sync(0xffffffffu, first[i]);
+    const int row = threadIdx.x & 127, t = row / G, head = pt.kvh * G + row % G;
+    if (t >= (h ? pt.ntok1 : pt.ntok0)) return;
+    const int limit = uv.casc ? uv.end[h] - 1 : pt.qpos0 + h * TM + t;  // last key that the row sees
+    const float nan = __int_as_float(0x7FFFFFFF);
+    const int64_t orow = (int64_t)(pt.tok0 + h * TM + t) * p.num_qo_heads + head;
+    const int64_t part = uv.casc ? (int64_t)(cmembers[pt.tok0 + h * TM + t].y + pt.qpos0) * p.lay.rows_per_slot + head : 0;
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+        if (min(first[0], first[1 + c]) > limit) continue;
+        for (int i = 0; i < 32; ++i) {
+            if (uv.casc) reinterpret_cast<float*>(p.ws + p.lay.partial_o)[part * D + c * 32 + i] = nan;
+            else p.out[orow * D + c * 32 + i] = 0x7FFF;
+        }
+    }
+    if (first[0] > limit) return;
+    if (uv.casc) reinterpret_cast<float*>(p.ws + p.lay.partial_lse)[part] = nan;
+    else if (p.lse != nullptr) p.lse[orow] = nan;
+}
+
 // q_map: Q as a 3-D tensor (D, Hq, T) whose box is one 64-column half of a Q tile (64
 // columns x G heads x TM tokens, rows in tile order); used when q_tma is nonzero.
 // KV: the pool type (PVA_KV_BF16, PVA_KV_E4M3, PVA_KV_MXFP4).
@@ -253,6 +303,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
             dev::mbar_init(&b->uq_full[s], 1);
             dev::mbar_init(&b->uq_empty[s], R::kQueueReaders);
         }
+        b->n_nan = b->nan_noted[0] = b->nan_noted[1] = b->nan_noted[2] = b->nan_noted[3] = 0;
         b->abort_flag = 0;
         b->wait_limit = dev::wait_limit(hdr->wait_override);
         dev::fence_barrier_init();
@@ -457,10 +508,14 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                     asm volatile("cp.async.commit_group;" ::: "memory");
                 };
                 // a step's staged rows (tile j) -> f16 operand rows, then the tile's barrier.  A row past
-                // the keys' end becomes zeros, so that its weight 0 meets no infinity or NaN.
+                // the keys' end becomes zeros, so that its weight 0 meets no infinity or NaN.  So do NaN
+                // blocks, since a hidden key's weight would meet them in every row of the tile; that the
+                // unit may have some (the words of rows not copied and a neighbouring head's bytes
+                // count too) is noted, and fix_nan gives the rows that see them their NaN.
                 auto convert = [&](int j, uint32_t buf, uint8_t* tile, uint64_t* full) {
                     const uint32_t t0 = dev::smem_u32(tile) + region;
-                    uint32_t w[NS][4], e[NS];
+                    uint32_t w[NS][4], e[NS], mine;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(mine) : "r"(buf + kCodes + 4 * min(my_row, kPreRows - 1)));
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
                         const int r = row_of4(m);
@@ -476,8 +531,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                     for (int m = 0; m < NS; ++m) {
                         const int r = row_of4(m);
                         if (r >= kPreRows) continue;
-                        const float f = mx::scale_f32((e[m] >> my_byte) & 255u);
-                        const uint32_t f2 = dev::pack_f16x2(f, f);
+                        const uint32_t f2 = mx::scale_f16x2_finite((e[m] >> my_byte) & 255u);
                         const uint32_t x[4] = {flip ? w[m][2] : w[m][0], flip ? w[m][3] : w[m][1],
                                                flip ? w[m][0] : w[m][2], flip ? w[m][1] : w[m][3]};
 #pragma unroll
@@ -487,6 +541,10 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                                               mx::mul_f16x2(mx::e2m1x2_to_f16x2<1>(x[i]), f2),
                                               mx::mul_f16x2(mx::e2m1x2_to_f16x2<2>(x[i]), f2),
                                               mx::mul_f16x2(mx::e2m1x2_to_f16x2<3>(x[i]), f2));
+                    }
+                    if (__vcmpeq4(mine, 0xFFFFFFFFu) != 0 && atomicExch(&b->nan_noted[uc & 3], uc + 1) != uc + 1) {
+                        const int i = atomicAdd(&b->n_nan, 1);
+                        if (i < Bars::kNanUnits) b->nan_units[i] = u;
                     }
                     // these generic-proxy stores -> the tensor core's operand reads
                     tc::fence_proxy_async_smem();
@@ -1040,6 +1098,12 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
     if (warp == kMmaWarp) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
+    }
+    if (MX && warp < 8 && b->n_nan > 0) {
+        // (past the list: every unit; one of another CTA's gets from it nothing that it does not get there)
+        const bool all = b->n_nan > Bars::kNanUnits;
+        for (int i = 0; i < (all ? n_units : b->n_nan); ++i)
+            fix_nan<D>(p, units[all ? i : b->nan_units[i]], cgroups, cmembers);
     }
 }
 
