@@ -436,17 +436,18 @@ class PagedAttention:
             raise PvaError(1, f"an MXFP4 pool of fewer than {n} bytes (mxfp4_row_bytes a slot)")
 
     @staticmethod
-    def _empty(shape, like, stream):
-        """A bf16 tensor of the stream that writes it (so that its memory, once let go, is not given to
+    def _empty(shape, like, stream, dtype=None):
+        """A tensor (bf16 unless said) of the stream that writes it (so that its memory, once let go, is not given to
         another stream's work while that one still runs)."""
         import torch
 
+        dtype = dtype or torch.bfloat16
         if stream is None:
-            return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+            return torch.empty(shape, dtype=dtype, device=like.device)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+            return torch.empty(shape, dtype=dtype, device=like.device)
 
     def forward(self, q, k, v, k_pool, v_pool, out=None, lse=None, stream=None, k_scale=None, v_scale=None,
                 rope: Rope | None = None, q_rot=None):
@@ -454,10 +455,8 @@ class PagedAttention:
         on the device) are required; with an MXFP4 config they are uint8 [slots, mxfp4_row_bytes].
         With ``rope``, q and k are rotated by position first (q into q_rot, a new tensor when None)
         and q, k, v may be strided by token."""
-        import torch
-
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = self._empty(q.shape, q, stream, q.dtype)
         if self._mx_pool_bytes:
             self._check_pools(k_pool, v_pool)
         if rope is not None:
