@@ -140,17 +140,22 @@ def _ptr(t):
 _raw_stream = None
 
 
+def _current():
+    """(handle of a device's current stream, the current device): functions that make no stream
+    object (which costs more than the launch it is for)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        torch.cuda.current_stream()  # initialises CUDA
+        _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    return _raw_stream
+
+
 def _stream(stream):
     if stream is None:
-        # the current stream's handle without a stream object (which costs more than the launch it
-        # is for)
-        global _raw_stream
-        if _raw_stream is None:
-            import torch
-
-            torch.cuda.current_stream()  # initialises CUDA
-            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
-        return _raw_stream[0](_raw_stream[1]())
+        handle, device = _current()
+        return handle(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -437,17 +442,18 @@ class PagedAttention:
 
     @staticmethod
     def _empty(shape, like, stream, dtype=None):
-        """A tensor (bf16 unless said) of the stream that writes it (so that its memory, once let go, is not given to
-        another stream's work while that one still runs)."""
+        """A tensor (bf16 unless said) on like's device, of the stream that writes it (so that its memory,
+        once let go, is not given to another stream's work while that one still runs)."""
         import torch
 
-        dtype = dtype or torch.bfloat16
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=like.device)
+        dtype, dev = dtype or torch.bfloat16, like.device
+        handle = _stream(stream) if stream is not None else None
+        if handle is None or handle == _current()[0](like.get_device()):
+            return torch.empty(shape, dtype=dtype, device=dev)
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=like.device)
+            return torch.empty(shape, dtype=dtype, device=dev)
 
     def forward(self, q, k, v, k_pool, v_pool, out=None, lse=None, stream=None, k_scale=None, v_scale=None,
                 rope: Rope | None = None, q_rot=None):
