@@ -52,6 +52,44 @@ class Config(ctypes.Structure):
 class Meta(ctypes.Structure):
     """Mirror of pva_meta (opaque, caller-owned, host memory)."""
     _fields_ = [("opaque", ctypes.c_uint64 * 64)]
+    batch = None   # what the prepared batch asks of a call's tensors (Batch)
+
+
+class Batch:
+    """Sizes of a prepared batch, its device, and the element types of a call's tensors."""
+    __slots__ = ("tokens", "q_heads", "kv_heads", "head_dim", "nq", "nkv", "nlse", "pool_bytes", "scaled", "device", "bf16",
+                 "f32")
+
+    def __init__(self, cfg: Config, total_tokens: int, device: int):
+        import torch
+
+        self.tokens, self.device = int(total_tokens), device
+        self.q_heads, self.kv_heads, self.head_dim = cfg.num_qo_heads, cfg.num_kv_heads, cfg.head_dim
+        elems = self.kv_heads * self.head_dim
+        row = {KV_BF16: 2 * elems, KV_E4M3: elems}.get(cfg.kv_dtype)
+        if row is None:
+            row = int(load().attn_mxfp4_row_bytes(self.kv_heads, self.head_dim))
+        self.nq, self.nkv = self.tokens * self.q_heads * self.head_dim, self.tokens * elems
+        self.nlse = self.tokens * self.q_heads
+        self.pool_bytes = cfg.num_pages * cfg.page_size * row
+        self.scaled = cfg.kv_dtype == KV_E4M3
+        self.bf16, self.f32 = torch.bfloat16, torch.float32
+
+    def lacks(self, x, n: int, dtype) -> bool:
+        """Whether x (or None, which the library refuses itself) is not at least n contiguous elements of
+        the type on the batch's device."""
+        return x is not None and (x.numel() < n or x.dtype is not dtype or x.get_device() != self.device
+                                  or not x.is_contiguous())
+
+    def lacks_pools(self, k_pool, v_pool) -> bool:
+        n, dev = self.pool_bytes, self.device
+        return ((k_pool is not None and (k_pool.nbytes < n or k_pool.get_device() != dev or not k_pool.is_contiguous()))
+                or (v_pool is not None and (v_pool.nbytes < n or v_pool.get_device() != dev or not v_pool.is_contiguous())))
+
+    def refusal(self, where: str) -> PvaError:
+        return PvaError(1, f"{where} (for {self.tokens} tokens of {self.q_heads} / {self.kv_heads} heads of {self.head_dim}, "
+                           f"pools of {self.pool_bytes} bytes: a tensor that is shorter, strided, of another type "
+                           "or on another device)")
 
 
 class RopeArgs(ctypes.Structure):
@@ -154,7 +192,7 @@ def _current():
 
 def _stream(stream):
     if stream is None:
-        handle, device = _current()
+        handle, device = _raw_stream or _current()
         return handle(device())
     if isinstance(stream, int):
         return stream
@@ -183,6 +221,7 @@ def attn_prepare_metadata(cfg: Config, cu_seqlens_q, cache_seqlens, page_table, 
         _ptr(slot_mapping), int(batch), int(total_tokens), int(max_q_len), _ptr(workspace),
         int(workspace.numel() * workspace.element_size()), _stream(stream), ctypes.byref(meta))
     _check(st, "attn_prepare_metadata")
+    meta.batch = Batch(cfg, total_tokens, cu_seqlens_q.get_device())
     return meta
 
 
@@ -194,6 +233,7 @@ def attn_prepare_metadata_static(cfg: Config, cu_seqlens_q, cache_seqlens, page_
         ctypes.byref(cfg), _ptr(cu_seqlens_q), _ptr(cache_seqlens), _ptr(page_table), int(page_table.stride(0)),
         _ptr(slot_mapping), int(batch), int(total_tokens), int(max_q_len), _stream(stream), ctypes.byref(meta))
     _check(st, "attn_prepare_metadata_static")
+    meta.batch = Batch(cfg, total_tokens, cu_seqlens_q.get_device())
     return meta
 
 
@@ -222,40 +262,36 @@ def attn_store_kvcache_fp8kv(meta: Meta, k, v, k_pool, v_pool, k_scale, v_scale,
     _check(st, "attn_store_kvcache_fp8kv")
 
 
-def _strided(where: str) -> PvaError:
-    """Only q, k and v of a rotation may be strided (by token)."""
-    return PvaError(1, f"{where} (a strided tensor)")
-
-
 def attn_forward_mxfp4kv(meta: Meta, q, k, v, k_pool, v_pool, out, lse=None, stream=None) -> None:
     """attn_forward over MXFP4 pools (uint8 [slots, mxfp4_row_bytes] tensors)."""
-    if not ((q is None or q.is_contiguous()) and (k is None or k.is_contiguous())
-            and (v is None or v.is_contiguous()) and (k_pool is None or k_pool.is_contiguous())
-            and (v_pool is None or v_pool.is_contiguous()) and (out is None or out.is_contiguous())
-            and (lse is None or lse.is_contiguous())):
-        raise _strided("attn_forward_mxfp4kv")
-    st = load().attn_forward_mxfp4kv(ctypes.byref(meta), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
-                                     _ptr(out), _ptr(lse), _stream(stream))
-    _check(st, "attn_forward_mxfp4kv")
+    b = meta.batch
+    if b is not None and (b.lacks(q, b.nq, b.bf16) or b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16)
+                          or b.lacks(out, b.nq, b.bf16) or b.lacks(lse, b.nlse, b.f32)
+                          or b.lacks_pools(k_pool, v_pool)):
+        raise b.refusal("attn_forward_mxfp4kv")
+    st = (_lib or load()).attn_forward_mxfp4kv(meta, _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), _ptr(out),
+                                               _ptr(lse), _stream(stream))
+    if st:
+        _check(st, "attn_forward_mxfp4kv")
 
 
 def attn_store_kvcache_mxfp4kv(meta: Meta, k, v, k_pool, v_pool, stream=None) -> None:
-    if not ((k is None or k.is_contiguous()) and (v is None or v.is_contiguous())
-            and (k_pool is None or k_pool.is_contiguous()) and (v_pool is None or v_pool.is_contiguous())):
-        raise _strided("attn_store_kvcache_mxfp4kv")
-    st = load().attn_store_kvcache_mxfp4kv(ctypes.byref(meta), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
-                                           _stream(stream))
-    _check(st, "attn_store_kvcache_mxfp4kv")
+    b = meta.batch
+    if b is not None and (b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16) or b.lacks_pools(k_pool, v_pool)):
+        raise b.refusal("attn_store_kvcache_mxfp4kv")
+    st = (_lib or load()).attn_store_kvcache_mxfp4kv(meta, _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), _stream(stream))
+    if st:
+        _check(st, "attn_store_kvcache_mxfp4kv")
 
 
 def attn_load_kvcache_mxfp4kv(meta: Meta, k_pool, v_pool, k, v, stream=None) -> None:
     """The values the pools hold at the batch's new tokens' slots, into bf16 k / v [T, Hkv, D]."""
-    if not ((k_pool is None or k_pool.is_contiguous()) and (v_pool is None or v_pool.is_contiguous())
-            and (k is None or k.is_contiguous()) and (v is None or v.is_contiguous())):
-        raise _strided("attn_load_kvcache_mxfp4kv")
-    st = load().attn_load_kvcache_mxfp4kv(ctypes.byref(meta), _ptr(k_pool), _ptr(v_pool), _ptr(k), _ptr(v),
-                                          _stream(stream))
-    _check(st, "attn_load_kvcache_mxfp4kv")
+    b = meta.batch
+    if b is not None and (b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16) or b.lacks_pools(k_pool, v_pool)):
+        raise b.refusal("attn_load_kvcache_mxfp4kv")
+    st = (_lib or load()).attn_load_kvcache_mxfp4kv(meta, _ptr(k_pool), _ptr(v_pool), _ptr(k), _ptr(v), _stream(stream))
+    if st:
+        _check(st, "attn_load_kvcache_mxfp4kv")
 
 
 def mxfp4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
@@ -279,6 +315,7 @@ class Rope:
         if rot_dim is not None and rot_dim != cos_sin.shape[1]:
             raise ValueError(f"cos_sin has {cos_sin.shape[1]} columns, rot_dim is {rot_dim}")
         self.cos_sin = cos_sin
+        self.device, self._bf16 = cos_sin.get_device(), torch.bfloat16
         self.max_positions, self.rot_dim = (int(n) for n in cos_sin.shape)
         self.interleaved = bool(interleaved)
         self.set_positions(positions)
@@ -289,23 +326,32 @@ class Rope:
 
         if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
             raise ValueError("positions is a contiguous int32 tensor")
+        if positions is not None and positions.get_device() != self.device:
+            raise ValueError("positions lie on another device than cos_sin")
         self.positions = positions
 
-    def args(self, q, k, v) -> RopeArgs:
+    def args(self, q, k, v, batch: Batch | None = None) -> RopeArgs:
+        """The C structure for q (or None), k and v [T, heads, D], checked against the batch they are of."""
         pos = self.positions
         if pos is not None and pos.numel() != k.shape[0]:
             raise ValueError(f"{pos.numel()} positions for {k.shape[0]} tokens")
+        if batch is not None and self.device != batch.device:
+            raise ValueError("cos_sin is not on the batch's device")
         return RopeArgs(self.cos_sin.data_ptr(), None if pos is None else pos.data_ptr(),
-                        0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
-                        self.max_positions, self.rot_dim, self.interleaved, 0)
+                        0 if q is None else self._token_stride(q, "q", batch, True), self._token_stride(k, "k", batch, False),
+                        self._token_stride(v, "v", batch, False), self.max_positions, self.rot_dim, self.interleaved, 0)
 
-
-def _token_stride(x, name: str) -> int:
-    T, heads, dim = x.shape
-    st, sh, sd = x.stride()
-    if sd != 1 or (sh != dim and heads > 1):
-        raise ValueError(f"{name} [T, heads, D] has contiguous heads (only the token stride is free)")
-    return st if T > 1 else heads * dim
+    def _token_stride(self, x, name: str, batch, is_q: bool) -> int:
+        T, heads, dim = x.shape
+        st, sh, sd = x.stride()
+        if sd != 1 or (sh != dim and heads > 1):
+            raise ValueError(f"{name} [T, heads, D] has contiguous heads (only the token stride is free)")
+        if x.dtype is not self._bf16 or x.get_device() != self.device:
+            raise ValueError(f"{name} is a bf16 tensor on the device of cos_sin")
+        if batch is not None and (T < batch.tokens or dim != batch.head_dim
+                                  or heads != (batch.q_heads if is_q else batch.kv_heads)):
+            raise batch.refusal(f"{name} {tuple(x.shape)}")
+        return st if T > 1 else heads * dim
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -321,27 +367,30 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
 def attn_append_rope(meta: Meta, rope: Rope, q, k, v, q_out, k_pool, v_pool, k_scale=None, v_scale=None,
                      stream=None) -> None:
     """q rotated into q_out, k rotated and stored, v stored; q, k, v may be strided by token."""
-    if not ((q_out is None or q_out.is_contiguous()) and (k_pool is None or k_pool.is_contiguous())
-            and (v_pool is None or v_pool.is_contiguous())):
-        raise _strided("attn_append_rope")
-    args = rope.args(q, k, v)
-    st = load().attn_append_rope(ctypes.byref(meta), ctypes.byref(args), _ptr(q), _ptr(k), _ptr(v), _ptr(q_out),
-                                 _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _stream(stream))
-    _check(st, "attn_append_rope")
+    b = meta.batch
+    args = rope.args(q, k, v, b)
+    if b is not None and (b.lacks(q_out, b.nq, b.bf16) or b.lacks_pools(k_pool, v_pool) or b.scaled
+                          and (b.lacks(k_scale, b.kv_heads, b.f32) or b.lacks(v_scale, b.kv_heads, b.f32))):
+        raise b.refusal("attn_append_rope")
+    st = (_lib or load()).attn_append_rope(meta, args, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pool), _ptr(v_pool),
+                                           _ptr(k_scale), _ptr(v_scale), _stream(stream))
+    if st:
+        _check(st, "attn_append_rope")
 
 
 def attn_forward_rope(meta: Meta, rope: Rope, q, k, v, q_rot, k_pool, v_pool, out, lse=None, k_scale=None,
                       v_scale=None, stream=None) -> None:
     """attn_append_rope, then the attention of the rotated q."""
-    if not ((q_rot is None or q_rot.is_contiguous()) and (k_pool is None or k_pool.is_contiguous())
-            and (v_pool is None or v_pool.is_contiguous()) and (out is None or out.is_contiguous())
-            and (lse is None or lse.is_contiguous())):
-        raise _strided("attn_forward_rope")
-    args = rope.args(q, k, v)
-    st = load().attn_forward_rope(ctypes.byref(meta), ctypes.byref(args), _ptr(q), _ptr(k), _ptr(v), _ptr(q_rot),
-                                  _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse),
-                                  _stream(stream))
-    _check(st, "attn_forward_rope")
+    b = meta.batch
+    args = rope.args(q, k, v, b)
+    if b is not None and (b.lacks(q_rot, b.nq, b.bf16) or b.lacks(out, b.nq, b.bf16) or b.lacks(lse, b.nlse, b.f32)
+                          or b.lacks_pools(k_pool, v_pool) or b.scaled
+                          and (b.lacks(k_scale, b.kv_heads, b.f32) or b.lacks(v_scale, b.kv_heads, b.f32))):
+        raise b.refusal("attn_forward_rope")
+    st = (_lib or load()).attn_forward_rope(meta, args, _ptr(q), _ptr(k), _ptr(v), _ptr(q_rot), _ptr(k_pool), _ptr(v_pool),
+                                            _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), _stream(stream))
+    if st:
+        _check(st, "attn_forward_rope")
 
 
 def attn_get_device_status(meta: Meta) -> int:
@@ -418,9 +467,6 @@ class PagedAttention:
         nbytes = attn_workspace_size(self.cfg)
         if nbytes == 0:
             raise PvaError(2, "attn_workspace_size")
-        self._mx_pool_bytes = 0
-        if kv_dtype == KV_MXFP4:
-            self._mx_pool_bytes = num_pages * page_size * mxfp4_row_bytes(num_kv_heads, head_dim)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.meta = None
         self._keep = None
@@ -434,11 +480,6 @@ class PagedAttention:
         self.meta = attn_prepare_metadata(self.cfg, cu_seqlens_q, cache_seqlens, page_table, slot_mapping, batch,
                                           total_tokens, max_q_len, self.workspace, stream)
         return self.meta
-
-    def _check_pools(self, k_pool, v_pool) -> None:
-        n = self._mx_pool_bytes
-        if k_pool.numel() < n or v_pool.numel() < n:  # (uint8)
-            raise PvaError(1, f"an MXFP4 pool of fewer than {n} bytes (mxfp4_row_bytes a slot)")
 
     @staticmethod
     def _empty(shape, like, stream, dtype=None):
@@ -463,8 +504,6 @@ class PagedAttention:
         and q, k, v may be strided by token."""
         if out is None:
             out = self._empty(q.shape, q, stream, q.dtype)
-        if self._mx_pool_bytes:
-            self._check_pools(k_pool, v_pool)
         if rope is not None:
             if q_rot is None:
                 q_rot = self._empty(q.shape, q, stream)
@@ -480,8 +519,6 @@ class PagedAttention:
     def append(self, q, k, v, k_pool, v_pool, rope: Rope, q_out=None, k_scale=None, v_scale=None, stream=None):
         """attn_append_rope of one layer; returns the rotated q (q_out, a new tensor when None; None
         without q)."""
-        if self._mx_pool_bytes:
-            self._check_pools(k_pool, v_pool)
         if q_out is None and q is not None:
             q_out = self._empty(q.shape, q, stream)
         attn_append_rope(self.meta, rope, q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, stream)
@@ -489,8 +526,6 @@ class PagedAttention:
 
     def store(self, k, v, k_pool, v_pool, k_scale=None, v_scale=None, stream=None) -> None:
         """store_kvcache of one layer, into pools of the config's type."""
-        if self._mx_pool_bytes:
-            self._check_pools(k_pool, v_pool)
         if self.cfg.kv_dtype == KV_E4M3:
             attn_store_kvcache_fp8kv(self.meta, k, v, k_pool, v_pool, k_scale, v_scale, stream)
         elif self.cfg.kv_dtype == KV_MXFP4:
@@ -500,8 +535,6 @@ class PagedAttention:
 
     def load(self, k_pool, v_pool, k=None, v=None, stream=None):
         """What MXFP4 pools hold at the batch's new tokens' slots, as bf16 (k, v) [T, Hkv, D]."""
-        if self._mx_pool_bytes:
-            self._check_pools(k_pool, v_pool)
         shape = (self.total_tokens, self.cfg.num_kv_heads, self.cfg.head_dim)
         k = self._empty(shape, k_pool, stream) if k is None else k
         v = self._empty(shape, k_pool, stream) if v is None else v
