@@ -57,8 +57,8 @@ class Meta(ctypes.Structure):
 
 class Batch:
     """Sizes of a prepared batch, its device, and the element types of a call's tensors."""
-    __slots__ = ("tokens", "q_heads", "kv_heads", "head_dim", "nq", "nkv", "nlse", "pool_bytes", "scaled", "device", "bf16",
-                 "f32")
+    __slots__ = ("tokens", "q_heads", "kv_heads", "head_dim", "nq", "nkv", "nlse", "pool_bytes", "scaled", "device",
+                 "bf16", "f32")
 
     def __init__(self, cfg: Config, total_tokens: int, device: int):
         import torch
@@ -83,13 +83,13 @@ class Batch:
 
     def lacks_pools(self, k_pool, v_pool) -> bool:
         n, dev = self.pool_bytes, self.device
-        return ((k_pool is not None and (k_pool.nbytes < n or k_pool.get_device() != dev or not k_pool.is_contiguous()))
-                or (v_pool is not None and (v_pool.nbytes < n or v_pool.get_device() != dev or not v_pool.is_contiguous())))
+        return (k_pool is not None and (k_pool.nbytes < n or k_pool.get_device() != dev or not k_pool.is_contiguous())
+                or v_pool is not None and (v_pool.nbytes < n or v_pool.get_device() != dev or not v_pool.is_contiguous()))
 
     def refusal(self, where: str) -> PvaError:
-        return PvaError(1, f"{where} (for {self.tokens} tokens of {self.q_heads} / {self.kv_heads} heads of {self.head_dim}, "
-                           f"pools of {self.pool_bytes} bytes: a tensor that is shorter, strided, of another type "
-                           "or on another device)")
+        return PvaError(1, f"{where} (for {self.tokens} tokens of {self.q_heads} / {self.kv_heads} heads of "
+                           f"{self.head_dim}, pools of {self.pool_bytes} bytes: a tensor that is shorter, strided, "
+                           "of another type or on another device)")
 
 
 class RopeArgs(ctypes.Structure):
@@ -199,6 +199,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _stream_on(b, stream, where):
+    """The stream's handle for a call of batch b, whose device has to be the current one (the library
+    launches there, whatever the stream)."""
+    on_gpu = b is not None and b.device >= 0
+    if on_gpu or stream is None:
+        handle, device = _raw_stream or _current()
+        current = device()
+        if on_gpu and current != b.device:
+            raise PvaError(1, f"{where} (the batch is on GPU {b.device}, which is not the current device)")
+        if stream is None:
+            return handle(current)
+    return _stream(stream)
+
+
 KV_BF16, KV_E4M3, KV_MXFP4 = 0, 1, 2
 
 
@@ -269,8 +283,9 @@ def attn_forward_mxfp4kv(meta: Meta, q, k, v, k_pool, v_pool, out, lse=None, str
                           or b.lacks(out, b.nq, b.bf16) or b.lacks(lse, b.nlse, b.f32)
                           or b.lacks_pools(k_pool, v_pool)):
         raise b.refusal("attn_forward_mxfp4kv")
+    s = _stream_on(b, stream, "attn_forward_mxfp4kv")
     st = (_lib or load()).attn_forward_mxfp4kv(meta, _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), _ptr(out),
-                                               _ptr(lse), _stream(stream))
+                                               _ptr(lse), s)
     if st:
         _check(st, "attn_forward_mxfp4kv")
 
@@ -279,7 +294,8 @@ def attn_store_kvcache_mxfp4kv(meta: Meta, k, v, k_pool, v_pool, stream=None) ->
     b = meta.batch
     if b is not None and (b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16) or b.lacks_pools(k_pool, v_pool)):
         raise b.refusal("attn_store_kvcache_mxfp4kv")
-    st = (_lib or load()).attn_store_kvcache_mxfp4kv(meta, _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), _stream(stream))
+    s = _stream_on(b, stream, "attn_store_kvcache_mxfp4kv")
+    st = (_lib or load()).attn_store_kvcache_mxfp4kv(meta, _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), s)
     if st:
         _check(st, "attn_store_kvcache_mxfp4kv")
 
@@ -289,7 +305,8 @@ def attn_load_kvcache_mxfp4kv(meta: Meta, k_pool, v_pool, k, v, stream=None) -> 
     b = meta.batch
     if b is not None and (b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16) or b.lacks_pools(k_pool, v_pool)):
         raise b.refusal("attn_load_kvcache_mxfp4kv")
-    st = (_lib or load()).attn_load_kvcache_mxfp4kv(meta, _ptr(k_pool), _ptr(v_pool), _ptr(k), _ptr(v), _stream(stream))
+    s = _stream_on(b, stream, "attn_load_kvcache_mxfp4kv")
+    st = (_lib or load()).attn_load_kvcache_mxfp4kv(meta, _ptr(k_pool), _ptr(v_pool), _ptr(k), _ptr(v), s)
     if st:
         _check(st, "attn_load_kvcache_mxfp4kv")
 
@@ -338,8 +355,9 @@ class Rope:
         if batch is not None and self.device != batch.device:
             raise ValueError("cos_sin is not on the batch's device")
         return RopeArgs(self.cos_sin.data_ptr(), None if pos is None else pos.data_ptr(),
-                        0 if q is None else self._token_stride(q, "q", batch, True), self._token_stride(k, "k", batch, False),
-                        self._token_stride(v, "v", batch, False), self.max_positions, self.rot_dim, self.interleaved, 0)
+                        0 if q is None else self._token_stride(q, "q", batch, True),
+                        self._token_stride(k, "k", batch, False), self._token_stride(v, "v", batch, False),
+                        self.max_positions, self.rot_dim, self.interleaved, 0)
 
     def _token_stride(self, x, name: str, batch, is_q: bool) -> int:
         T, heads, dim = x.shape
@@ -372,8 +390,9 @@ def attn_append_rope(meta: Meta, rope: Rope, q, k, v, q_out, k_pool, v_pool, k_s
     if b is not None and (b.lacks(q_out, b.nq, b.bf16) or b.lacks_pools(k_pool, v_pool) or b.scaled
                           and (b.lacks(k_scale, b.kv_heads, b.f32) or b.lacks(v_scale, b.kv_heads, b.f32))):
         raise b.refusal("attn_append_rope")
-    st = (_lib or load()).attn_append_rope(meta, args, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pool), _ptr(v_pool),
-                                           _ptr(k_scale), _ptr(v_scale), _stream(stream))
+    s = _stream_on(b, stream, "attn_append_rope")
+    st = (_lib or load()).attn_append_rope(meta, args, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pool),
+                                           _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), s)
     if st:
         _check(st, "attn_append_rope")
 
@@ -387,8 +406,9 @@ def attn_forward_rope(meta: Meta, rope: Rope, q, k, v, q_rot, k_pool, v_pool, ou
                           or b.lacks_pools(k_pool, v_pool) or b.scaled
                           and (b.lacks(k_scale, b.kv_heads, b.f32) or b.lacks(v_scale, b.kv_heads, b.f32))):
         raise b.refusal("attn_forward_rope")
-    st = (_lib or load()).attn_forward_rope(meta, args, _ptr(q), _ptr(k), _ptr(v), _ptr(q_rot), _ptr(k_pool), _ptr(v_pool),
-                                            _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), _stream(stream))
+    s = _stream_on(b, stream, "attn_forward_rope")
+    st = (_lib or load()).attn_forward_rope(meta, args, _ptr(q), _ptr(k), _ptr(v), _ptr(q_rot), _ptr(k_pool),
+                                            _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), s)
     if st:
         _check(st, "attn_forward_rope")
 

@@ -129,6 +129,20 @@ def test_tensors_on_another_device(kv_dtype):
             assert status(call, batch_of(kv_dtype), a) == 1, (name, n)
 
 
+@pytest.mark.parametrize("kv_dtype", KINDS)
+def test_a_batch_on_another_device_than_the_current_one(kv_dtype, monkeypatch):
+    """Refused on any stream: the library launches on the current device."""
+    current = [0]
+    monkeypatch.setattr(pva, "_raw_stream", (lambda dev: 0, lambda: current[0]))
+    for name, (_, call) in calls(kv_dtype).items():
+        a = {n: SomewhereElse(x) if isinstance(x, torch.Tensor) else x for n, x in tensors(kv_dtype).items()}
+        a["rope"] = pva.Rope(SomewhereElse(torch.zeros(64, D)))
+        current[0] = 0
+        assert status(call, batch_of(kv_dtype, device=3), a) == 1, name
+        current[0] = 3
+        assert status(call, batch_of(kv_dtype, device=3), a) == NOT_PREPARED, name
+
+
 def test_a_table_or_positions_on_another_device():
     a = tensors(pva.KV_MXFP4)
     table = SomewhereElse(torch.zeros(64, D))
