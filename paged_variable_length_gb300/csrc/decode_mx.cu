@@ -26,6 +26,7 @@
 // Every wait is bounded, as in decode.cu.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "device_utils.cuh"
@@ -124,6 +125,7 @@ struct IntTag {
 
 // The ring's barriers, and those by which a head's warps hand their results to its first.
 constexpr int kMaxStages = 16;
+constexpr int kSmemLimit = 220 * 1024;
 struct MxSmem {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t xfull[kDecHeadBlock], xempty[kDecHeadBlock];
@@ -977,7 +979,7 @@ cudaError_t launch_h(const ForwardParams& p, int producers, int ctas, cudaStream
     int exch = 0;
     for (;; --sp.kw) {
         exch = (sp.kw - 1) * sp.hb * (D / 4 + 4) * NQ * 128;
-        sp.stages = (220 * 1024 - 1024 - head - exch) / stage_bytes;
+        sp.stages = (kSmemLimit - 1024 - head - exch) / stage_bytes;
         sp.stages = sp.stages > kMaxStages ? kMaxStages : sp.stages;
         // a warp holds a stage while it waits for its next one, kw stages on
         if (sp.kw == 1 || sp.kw <= sp.stages - 2) break;
@@ -986,16 +988,17 @@ cudaError_t launch_h(const ForwardParams& p, int producers, int ctas, cudaStream
     sp.exch = head + sp.stages * stage_bytes;
     const size_t smem = (size_t)sp.exch + exch;
     // the register split inside the kernel assumes the launch allocates exactly kRegsLaunch a thread
-    static int launch_regs = -1;
-    if (launch_regs < 0) {
+    static std::atomic<int> launch_regs{-1};
+    if (launch_regs.load(std::memory_order_relaxed) < 0) {
         cudaFuncAttributes attr{};
         const cudaError_t ea = cudaFuncGetAttributes(&attr, decode_mx_kernel<D, NQ, HBT, MULTI>);
         if (ea != cudaSuccess) return ea;
-        launch_regs = attr.numRegs;
+        launch_regs.store(attr.numRegs, std::memory_order_relaxed);
     }
-    if (launch_regs != MxWarps<D, NQ>::kRegsLaunch) return cudaErrorInvalidConfiguration;
-    const cudaError_t e =
-        cudaFuncSetAttribute(decode_mx_kernel<D, NQ, HBT, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (launch_regs.load(std::memory_order_relaxed) != MxWarps<D, NQ>::kRegsLaunch) return cudaErrorInvalidConfiguration;
+    // (the bound, not this call's size: another thread may be launching another head layout of the kernel)
+    const cudaError_t e = cudaFuncSetAttribute(decode_mx_kernel<D, NQ, HBT, MULTI>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     return launch_programmatic(decode_mx_kernel<D, NQ, HBT, MULTI>, (unsigned)ctas, (unsigned)MxWarps<D, NQ>::kThreads, smem, s, p, sp);
 }
