@@ -768,12 +768,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(ForwardParams p) {
     }
 }
 
+constexpr int kSmemLimit = 220 * 1024;  // dynamic shared memory of the decode CTAs of an SM
+static_assert(sizeof(DecSmemHead) <= 1024, "what stage_count leaves for it");
+
 template <int D>
 int stage_count(int num_kv_heads, int ctas_per_sm, int es, int pad) {
     const int hb = num_kv_heads < kMaxKvHeads ? num_kv_heads : kMaxKvHeads;
     const int row_stride = hb * D * es + pad;
     const int stage_bytes = 2 * kStageKeys * row_stride;
-    const int budget = 220 * 1024 / ctas_per_sm - 1024;
+    const int budget = kSmemLimit / ctas_per_sm - 1024;
     int st = budget / stage_bytes;
     return st < 2 ? 2 : (st > 8 ? 8 : st);
 }
@@ -799,8 +802,8 @@ cudaError_t launch_d(const ForwardParams& p, int ctas, cudaStream_t s) {
     const bool runs = F8 && p.page_size >= kStageKeys && p.num_kv_heads <= kMaxKvHeads;
     const int stages = stage_count<D>(p.num_kv_heads, cps, es, runs ? 0 : kRowPad);
     const size_t smem = smem_bytes<D>(p.num_kv_heads, stages, es, runs ? 0 : kRowPad);
-    cudaError_t e =
-        cudaFuncSetAttribute(decode_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the bound, not this call's size: another thread may be launching another head layout of the kernel)
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     const int hb = p.num_kv_heads < kMaxKvHeads ? p.num_kv_heads : kMaxKvHeads;
     const int row_stride = hb * D * es + (runs ? 0 : kRowPad);

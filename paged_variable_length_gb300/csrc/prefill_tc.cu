@@ -44,6 +44,7 @@
 #include <cuda.h>  // CUtensorMap and the tensor-map encoder's types (resolved through the runtime)
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstring>
 #include <mutex>
@@ -1150,14 +1151,14 @@ cudaError_t launch_p(const ForwardParams& p, int ctas, cudaStream_t s) {
     // The register split inside the kernel assumes the launch allocates exactly
     // kRegsLaunch registers per thread; with fewer, the softmax warps' increase
     // could not be satisfied.  Refuse to launch rather than risk that.
-    static int launch_regs = -1;
-    if (launch_regs < 0) {
+    static std::atomic<int> launch_regs{-1};
+    if (launch_regs.load(std::memory_order_relaxed) < 0) {
         cudaFuncAttributes attr{};
         e = cudaFuncGetAttributes(&attr, prefill_kernel<D, KV>);
         if (e != cudaSuccess) return e;
-        launch_regs = attr.numRegs;
+        launch_regs.store(attr.numRegs, std::memory_order_relaxed);
     }
-    if (launch_regs != Roles<KV>::kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (launch_regs.load(std::memory_order_relaxed) != Roles<KV>::kRegsLaunch) return cudaErrorInvalidConfiguration;
     CUtensorMap q_map;
     memset(&q_map, 0, sizeof(q_map));
     const int q_tma = encode_q_map(p, D, &q_map) ? 1 : 0;

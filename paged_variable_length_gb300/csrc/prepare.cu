@@ -36,6 +36,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBuckets = 256;  // cost classes for the longest-first ordering of work items
 constexpr int kCmpPages = 8;         // page ids a lane compares per step of the shared-prefix search
+constexpr int kSmemLimit = 216 * 1024;  // dynamic shared memory (the largest batch kept there takes 208 KiB)
 constexpr int kLineLimit = 1 << 29;  // the balanced decode split is used below this many keys
 
 // Per-request shared-memory arrays (dynamic shared memory, batch <= smem_batch), followed
@@ -1217,7 +1218,8 @@ size_t prepare_smem_bytes(int smem_batch, bool cascade) {
 cudaError_t launch_prepare(const PrepareParams& p, cudaStream_t s) {
     const size_t smem = prepare_smem_bytes(p.smem_batch, p.use_cascade != 0);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // (the bound, not this call's size: another thread may be launching another batch's)
+        cudaError_t e = cudaFuncSetAttribute(prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
     }
     prepare_kernel<<<1, kThreads, smem, s>>>(p);

@@ -62,3 +62,21 @@ def test_mxfp4_layouts_of_one_kernel():
     seven heads of one tile."""
     at_once([layer(16, 1, 128, 16, pva.KV_MXFP4, 1), layer(32, 2, 128, 16, pva.KV_MXFP4, 2)])
     at_once([layer(12, 3, 128, 16, pva.KV_MXFP4, 3), layer(28, 7, 128, 16, pva.KV_MXFP4, 4)])
+
+
+def test_bf16_layouts_of_one_kernel():
+    """One and eight kv heads (several CTAs of an SM against one)."""
+    at_once([layer(4, 1, 128, 16, pva.KV_BF16, 1), layer(32, 8, 128, 16, pva.KV_BF16, 2)], times=6000)
+
+
+def test_plans_of_unlike_batches():
+    """Batches of 1100 and of 1500 requests, whose plans take unlike amounts of shared memory."""
+    def plan(B, seed):
+        wl = W.custom([1] * B, [1 + i % 7 for i in range(B)], 4, 1, 64, 1, seed=seed)
+        cu, sl, pt = (torch.as_tensor(x, dtype=torch.int32, device=DEV) for x in (wl.cu_seqlens_q, wl.cache_seqlens,
+                                                                                 wl.page_table))
+        eng, stream = make_engine(wl), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        return lambda: eng.prepare(cu, sl, pt, wl.total_tokens, max_q_len=1, stream=stream), torch.zeros(1, device=DEV)
+
+    at_once([plan(1100, 1), plan(1500, 2)], times=3000)
