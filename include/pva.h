@@ -336,7 +336,8 @@ typedef struct pva_rope {
 
 /*
  * store_kvcache with the rotation: q rotated into q_out (bf16 [T, Hq, D], contiguous; q itself
- * when that is contiguous, else no byte in common with q, k or v), k rotated and stored, v
+ * when that is contiguous, as one token's always is, else outside the memory from the first to
+ * the last element of q, of k and of v), k rotated and stored, v
  * stored, for every new token, into a pool of the meta's type.  q and q_out may both be NULL
  * (k and v alone).  k_scale and v_scale as in attn_forward_fp8kv, ignored for the other types.
  * A token whose position lies outside the table sets PVA_DEVERR_POSITION and nothing of it is

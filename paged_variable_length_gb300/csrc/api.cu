@@ -381,13 +381,13 @@ pva_status check_rope(const MetaHost* h, const pva_rope* rope, const void* q, co
         return PVA_ERR_INVALID_ARG;
     if (h->cfg.kv_dtype == PVA_KV_E4M3 && (k_scale == nullptr || v_scale == nullptr)) return PVA_ERR_INVALID_ARG;
     if (T == 0 || q == nullptr) return PVA_OK;
-    // q_out is q itself (then contiguous), or shares no byte with q, k or v
+    // q_out is q itself (then contiguous, as one token always is), or lies outside the spans of q, k and v
     const uintptr_t o0 = reinterpret_cast<uintptr_t>(q_out), o1 = o0 + (uintptr_t)(T * Hq * D * 2);
     auto overlaps = [&](const void* x, int64_t ld, int64_t heads) {
         const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), x1 = x0 + (uintptr_t)(((T - 1) * ld + heads * D) * 2);
         return x0 < o1 && o0 < x1;
     };
-    const bool in_place = q == q_out && rope->ld_q == Hq * D;
+    const bool in_place = q == q_out && (T == 1 || rope->ld_q == Hq * D);
     if ((!in_place && overlaps(q, rope->ld_q, Hq)) || overlaps(k, rope->ld_k, Hkv) || overlaps(v, rope->ld_v, Hkv))
         return PVA_ERR_INVALID_ARG;
     return PVA_OK;
