@@ -349,6 +349,7 @@ cudaError_t launch_store_any(const MetaHost* h, const ForwardParams& fp, cudaStr
     rp.ld_k = rp.ld_v = (int64_t)h->cfg.num_kv_heads * h->cfg.head_dim;
     rp.row_bytes = fp.mx_row_bytes;
     rp.batch = h->batch;
+    rp.sm_count = h->sm_count;
     return launch_append(fp, rp, h->cfg.head_dim, PVA_KV_MXFP4, s);
 }
 
@@ -407,6 +408,7 @@ RopeParams rope_params(const MetaHost* h, const pva_rope* rope, const void* q, v
     rp.interleaved = rope->interleaved ? 1 : 0;
     rp.row_bytes = mx::row_bytes(h->cfg.num_kv_heads, h->cfg.head_dim);
     rp.batch = h->batch;
+    rp.sm_count = h->sm_count;
     return rp;
 }
 

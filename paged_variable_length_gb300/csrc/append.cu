@@ -366,11 +366,11 @@ cudaError_t launch_r(const ForwardParams& p, const RopeParams& rp, cudaStream_t 
 
 template <int D, int KV, int MODE>
 cudaError_t launch_mode(const ForwardParams& p, const RopeParams& rp, cudaStream_t s) {
-    // four steps a warp (2 KiB of loads in flight each) carry HBM's rate (12 k tokens, bf16: 65.7 us,
-    // against 68.5 at two and 68.6 at six); one step a warp has the shortest chain of instructions
-    // for batches that do not fill the SMs with warps at four
+    // four steps a warp (2 KiB of loads in flight each) carry HBM's rate (16.6 k tokens, bf16: 65.3 us in a
+    // graph, against 74.2 at one, 68.9 at two and 67.8 at six); one step a warp has the shortest chain of
+    // instructions for batches that do not fill the SMs with warps at four (one token: 4.8 us, 6.2 at four)
     const int64_t warps = (int64_t)p.total_tokens * cdiv(rp_rows(p, rp), 4 * 32 / (D / 16));
-    return warps < 152 * 8 ? launch_r<D, KV, MODE, 1>(p, rp, s) : launch_r<D, KV, MODE, 4>(p, rp, s);
+    return warps < rp.sm_count * 8 ? launch_r<D, KV, MODE, 1>(p, rp, s) : launch_r<D, KV, MODE, 4>(p, rp, s);
 }
 
 template <int D, int KV>

@@ -260,6 +260,7 @@ struct RopeParams {
     int32_t interleaved;
     int32_t row_bytes;           // MXFP4: bytes of a pool row
     int32_t batch;
+    int32_t sm_count;
 };
 
 // Host view of a prepared batch, stored inside pva_meta::opaque.
