@@ -117,7 +117,8 @@ typedef enum pva_status {
  * even code; magnitudes above 6 * scale saturate (so those above 49152 do in any case, and
  * those below 2^-24 become 0).  A block with an infinity or a NaN is stored as e = 255 with
  * codes 0, and all its elements read as NaN.  Rows written by others may be read as long as
- * they keep to these scales.
+ * they keep to these scales, and to codes 0 under e = 255: nothing looks for others, and
+ * decodes and prefills read them differently.
  */
 #define PVA_KV_MXFP4 2
 
@@ -190,7 +191,9 @@ PVA_API size_t attn_workspace_size(const pva_config* cfg);
  *                  NULL (ld_page_table is then ignored)
  *   max_q_len      host upper bound on any request's q_len (<= 0: unknown,
  *                  taken as total_tokens); lets the forward skip the prefill
- *                  kernel for decode-only batches.  A request above it sets
+ *                  kernel for decode-only batches, and picks the decode kernel's
+ *                  row tile for MXFP4 pools (without it 64 single-token decodes
+ *                  take a third longer there).  A request above it sets
  *                  PVA_DEVERR_LIMITS and is skipped.
  *   workspace      device buffer of at least attn_workspace_size(cfg) bytes,
  *                  256-byte aligned, owned by the caller, not used
@@ -341,7 +344,9 @@ typedef struct pva_rope {
  * stored, for every new token, into a pool of the meta's type.  q and q_out may both be NULL
  * (k and v alone).  k_scale and v_scale as in attn_forward_fp8kv, ignored for the other types.
  * A token whose position lies outside the table sets PVA_DEVERR_POSITION and nothing of it is
- * written; a token with slot -1 has its q rotated and nothing stored.
+ * written: its slot and its row of q_out hold what they held, which attn_forward_rope's
+ * attention then reads, for that token and for later ones of its request.  A token with slot
+ * -1 has its q rotated and nothing stored.
  */
 PVA_API pva_status attn_append_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k,
                             const void* v, void* q_out, void* k_pool, void* v_pool, const float* k_scale,

@@ -21,7 +21,8 @@
 //     a bit select, so that one conversion gives the pair of keys the MMA wants;
 //   * P^T comes from S^T's accumulators by an 8x8 transpose in registers (movmatrix).
 // Each query row enters as f16 after a multiplication by the power of two that brings its
-// largest element to [1, 2) (undone in the softmax scale), so that its range is bf16's; P is
+// largest element to [1, 2) (undone in the softmax scale), so that its range is bf16's (elements
+// below 2^-14 of the row's largest lose their lowest bits); P is
 // rounded to f16 (2^-11 of a weight, below the output's bf16 rounding; kPShift), sums are fp32.
 // Every wait is bounded, as in decode.cu.
 #include <cuda_runtime.h>
@@ -843,7 +844,10 @@ __global__ void __launch_bounds__(MxWarps<D, NQ>::kThreads, 1) decode_mx_kernel(
 // another (128 parts of 32 rows: 28 us; here 5).  kW warps share a row, each joins every kW-th
 // part with loads of several parts in flight, and the row's warps are joined through shared
 // memory, in a fixed order.  kW follows the plan's parts per group: 1 up to 4 (the rows of many
-// groups fill the SMs by themselves), 4 up to 16, else 16.
+// groups fill the SMs by themselves), 4 up to 16, else 16.  Layer calls in a graph with 1 / 4 / 16:
+// 64 decodes (3 parts) 50.5 / 56.2 / 73.4 us, 61 decodes of 16 / 1 heads 39.1 / 41.0 / 51.0, 5 long
+// requests (30 parts) 56.9 / 53.1 / 53.3, 1 x 16 k keys (147 parts) 36.0 / 22.4 / 18.8; near the second
+// limit four would do (8 decodes, 19 parts: 23.6 / 21.2 / 24.1).
 constexpr int kJoinWarps = 16;
 
 template <int D>

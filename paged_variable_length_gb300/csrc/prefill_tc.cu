@@ -38,7 +38,8 @@
 // MXFP4 pools take the same form with a ring of staged K and V tiles, the block's scale applied as
 // the codes are converted, a power of two taken out of each Q row, and P held 2^7 times the weight;
 // see the producer.  8 prefills of 256-4096 tokens, 32/8 heads of 128: 408 us a layer call (342 from
-// a bf16 pool, whose rows need no conversion).
+// a bf16 pool, whose rows need no conversion; 405 before NaN blocks were kept from rows that do not
+// see them).
 // Every wait is bounded; a timeout sets PVA_DEVERR_TIMEOUT and the CTA winds
 // down (outstanding copies and MMAs waited for, TMEM freed) without trapping.
 #include <cuda.h>  // CUtensorMap and the tensor-map encoder's types (resolved through the runtime)
@@ -886,7 +887,8 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         // F8: this thread's row of Q tile h of the CTA's unit k, bf16 -> f16 in place (both regions;
         // every warp takes part in every unit: q_full counts the eight softmax warps).  MXFP4: times
         // the power of two that brings the row's largest element to [1, 2), which the softmax scale
-        // takes back (q_scale): q keeps its bits whatever its magnitude.
+        // takes back (q_scale): a row keeps its bits whatever its magnitude (elements below 2^-14 of its
+        // largest lose their lowest).
         float q_scale = 1.f;
         auto convert_q = [&](int k) -> bool {
             if (!wait_or_abort(&b->q_raw, k & 1, wlim, b, err)) return false;
