@@ -58,15 +58,15 @@ def parse():
 # what they were at capture time; after any change the roofline reports null.
 NCU_TRAFFIC = {
     ("decode", "decode"): {
-        "bytes": 617.276416e6,
+        "bytes": 617.166080e6,
         "sources": ['paged_variable_length_gb300/csrc/decode.cu', 'paged_variable_length_gb300/csrc/device_utils.cuh', 'paged_variable_length_gb300/csrc/pva_internal.h'],
-        "sha256_16": "3e0161db4653e5fc",
+        "sha256_16": "e510114b7bb51472",
         "summary": "profiles/decode_kernel_decode_workload.md",
     },
     ("tensor_core", "prefill"): {
-        "bytes": 219.98976e6,
+        "bytes": 219.460096e6,
         "sources": ['paged_variable_length_gb300/csrc/prefill_tc.cu', 'paged_variable_length_gb300/csrc/device_utils.cuh', 'paged_variable_length_gb300/csrc/tc_utils.cuh', 'paged_variable_length_gb300/csrc/pva_internal.h'],
-        "sha256_16": "0a933ec391a44559",
+        "sha256_16": "f9511adefc5966a9",
         "summary": "profiles/prefill_kernel_prefill_workload.md",
     },
 }
