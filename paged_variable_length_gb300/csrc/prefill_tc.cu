@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                 // the scale word holds the row's scale bytes (D 64: two heads' bytes, aligned down)
                 const int scales = mx::scales_at(pt.kvh, p.num_kv_heads, D);
                 const int my_byte = 8 * ((scales & 3) + lb);
+                const uint32_t head_bytes = D == 128 ? 0xFFFFFFFFu : 0xFFFFu << (8 * (scales & 3));
                 const uint32_t ring = dev::smem_u32(smem + L::kStage8);
                 auto row_of4 = [&](int m) { return pwarp * RPI + sub + RPS * m; };
                 // lane i looks up the warp's row i (of RPI * NS <= 32): its page id, then its slot, kNoSlot for
@@ -512,8 +513,8 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                 // a step's staged rows (tile j) -> f16 operand rows, then the tile's barrier.  A row past
                 // the keys' end becomes zeros, so that its weight 0 meets no infinity or NaN.  So do NaN
                 // blocks, since a hidden key's weight would meet them in every row of the tile; that the
-                // unit may have some (the words of rows not copied and a neighbouring head's bytes
-                // count too) is noted, and fix_nan gives the rows that see them their NaN.
+                // unit may have some (words that an earlier tile left count too) is noted, and fix_nan gives the
+                // rows that see them their NaN.
                 auto convert = [&](int j, uint32_t buf, uint8_t* tile, uint64_t* full) {
                     const uint32_t t0 = dev::smem_u32(tile) + region;
                     uint32_t w[NS][4], e[NS], mine;
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                                               mx::mul_f16x2(mx::e2m1x2_to_f16x2<2>(x[i]), f2),
                                               mx::mul_f16x2(mx::e2m1x2_to_f16x2<3>(x[i]), f2));
                     }
-                    if (__vcmpeq4(mine, 0xFFFFFFFFu) != 0 && atomicExch(&b->nan_noted[uc & 3], uc + 1) != uc + 1) {
+                    if ((__vcmpeq4(mine, 0xFFFFFFFFu) & head_bytes) != 0 && atomicExch(&b->nan_noted[uc & 3], uc + 1) != uc + 1) {
                         const int i = atomicAdd(&b->n_nan, 1);
                         if (i < Bars::kNanUnits) b->nan_units[i] = u;
                     }
