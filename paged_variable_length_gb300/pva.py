@@ -52,7 +52,14 @@ class Config(ctypes.Structure):
 class Meta(ctypes.Structure):
     """Mirror of pva_meta (opaque, caller-owned, host memory)."""
     _fields_ = [("opaque", ctypes.c_uint64 * 64)]
-    batch = None   # what the prepared batch asks of a call's tensors (Batch)
+    batch = None   # what the prepared batch asks of a call's tensors (Batch), made when a call first asks
+    _sizes = None
+
+    def of_batch(self):
+        """The Batch, or None of a meta that was never prepared."""
+        if self.batch is None and self._sizes is not None:
+            self.batch = Batch(*self._sizes)
+        return self.batch
 
 
 class Batch:
@@ -60,19 +67,19 @@ class Batch:
     __slots__ = ("tokens", "q_heads", "kv_heads", "head_dim", "nq", "nkv", "nlse", "pool_bytes", "scaled", "device",
                  "bf16", "f32")
 
-    def __init__(self, cfg: Config, total_tokens: int, device: int):
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, slots: int, kv_dtype: int, tokens: int, device: int):
         import torch
 
-        self.tokens, self.device = int(total_tokens), device
-        self.q_heads, self.kv_heads, self.head_dim = cfg.num_qo_heads, cfg.num_kv_heads, cfg.head_dim
-        elems = self.kv_heads * self.head_dim
-        row = {KV_BF16: 2 * elems, KV_E4M3: elems}.get(cfg.kv_dtype)
+        self.tokens, self.device = int(tokens), device
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        elems = kv_heads * head_dim
+        row = {KV_BF16: 2 * elems, KV_E4M3: elems}.get(kv_dtype)
         if row is None:
             row = int(load().attn_mxfp4_row_bytes(self.kv_heads, self.head_dim))
         self.nq, self.nkv = self.tokens * self.q_heads * self.head_dim, self.tokens * elems
         self.nlse = self.tokens * self.q_heads
-        self.pool_bytes = cfg.num_pages * cfg.page_size * row
-        self.scaled = cfg.kv_dtype == KV_E4M3
+        self.pool_bytes = slots * row
+        self.scaled = kv_dtype == KV_E4M3
         self.bf16, self.f32 = torch.bfloat16, torch.float32
 
     def lacks(self, x, n: int, dtype) -> bool:
@@ -90,6 +97,11 @@ class Batch:
         return PvaError(1, f"{where} (for {self.tokens} tokens of {self.q_heads} / {self.kv_heads} heads of "
                            f"{self.head_dim}, pools of {self.pool_bytes} bytes: a tensor that is shorter, strided, "
                            "of another type or on another device)")
+
+
+def _batch_sizes(cfg: Config, total_tokens, device: int):
+    return (cfg.num_qo_heads, cfg.num_kv_heads, cfg.head_dim, cfg.num_pages * cfg.page_size, cfg.kv_dtype, total_tokens,
+            device)
 
 
 class RopeArgs(ctypes.Structure):
@@ -235,7 +247,7 @@ def attn_prepare_metadata(cfg: Config, cu_seqlens_q, cache_seqlens, page_table, 
         _ptr(slot_mapping), int(batch), int(total_tokens), int(max_q_len), _ptr(workspace),
         int(workspace.numel() * workspace.element_size()), _stream(stream), ctypes.byref(meta))
     _check(st, "attn_prepare_metadata")
-    meta.batch = Batch(cfg, total_tokens, cu_seqlens_q.get_device())
+    meta._sizes = _batch_sizes(cfg, total_tokens, cu_seqlens_q.get_device())
     return meta
 
 
@@ -247,7 +259,7 @@ def attn_prepare_metadata_static(cfg: Config, cu_seqlens_q, cache_seqlens, page_
         ctypes.byref(cfg), _ptr(cu_seqlens_q), _ptr(cache_seqlens), _ptr(page_table), int(page_table.stride(0)),
         _ptr(slot_mapping), int(batch), int(total_tokens), int(max_q_len), _stream(stream), ctypes.byref(meta))
     _check(st, "attn_prepare_metadata_static")
-    meta.batch = Batch(cfg, total_tokens, cu_seqlens_q.get_device())
+    meta._sizes = _batch_sizes(cfg, total_tokens, cu_seqlens_q.get_device())
     return meta
 
 
@@ -278,7 +290,7 @@ def attn_store_kvcache_fp8kv(meta: Meta, k, v, k_pool, v_pool, k_scale, v_scale,
 
 def attn_forward_mxfp4kv(meta: Meta, q, k, v, k_pool, v_pool, out, lse=None, stream=None) -> None:
     """attn_forward over MXFP4 pools (uint8 [slots, mxfp4_row_bytes] tensors)."""
-    b = meta.batch
+    b = meta.batch or meta.of_batch()
     if b is not None and (b.lacks(q, b.nq, b.bf16) or b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16)
                           or b.lacks(out, b.nq, b.bf16) or b.lacks(lse, b.nlse, b.f32)
                           or b.lacks_pools(k_pool, v_pool)):
@@ -291,7 +303,7 @@ def attn_forward_mxfp4kv(meta: Meta, q, k, v, k_pool, v_pool, out, lse=None, str
 
 
 def attn_store_kvcache_mxfp4kv(meta: Meta, k, v, k_pool, v_pool, stream=None) -> None:
-    b = meta.batch
+    b = meta.batch or meta.of_batch()
     if b is not None and (b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16) or b.lacks_pools(k_pool, v_pool)):
         raise b.refusal("attn_store_kvcache_mxfp4kv")
     s = _stream_on(b, stream, "attn_store_kvcache_mxfp4kv")
@@ -302,7 +314,7 @@ def attn_store_kvcache_mxfp4kv(meta: Meta, k, v, k_pool, v_pool, stream=None) ->
 
 def attn_load_kvcache_mxfp4kv(meta: Meta, k_pool, v_pool, k, v, stream=None) -> None:
     """The values the pools hold at the batch's new tokens' slots, into bf16 k / v [T, Hkv, D]."""
-    b = meta.batch
+    b = meta.batch or meta.of_batch()
     if b is not None and (b.lacks(k, b.nkv, b.bf16) or b.lacks(v, b.nkv, b.bf16) or b.lacks_pools(k_pool, v_pool)):
         raise b.refusal("attn_load_kvcache_mxfp4kv")
     s = _stream_on(b, stream, "attn_load_kvcache_mxfp4kv")
@@ -385,7 +397,7 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device="
 def attn_append_rope(meta: Meta, rope: Rope, q, k, v, q_out, k_pool, v_pool, k_scale=None, v_scale=None,
                      stream=None) -> None:
     """q rotated into q_out, k rotated and stored, v stored; q, k, v may be strided by token."""
-    b = meta.batch
+    b = meta.batch or meta.of_batch()
     args = rope.args(q, k, v, b)
     if b is not None and (b.lacks(q_out, b.nq, b.bf16) or b.lacks_pools(k_pool, v_pool) or b.scaled
                           and (b.lacks(k_scale, b.kv_heads, b.f32) or b.lacks(v_scale, b.kv_heads, b.f32))):
@@ -400,7 +412,7 @@ def attn_append_rope(meta: Meta, rope: Rope, q, k, v, q_out, k_pool, v_pool, k_s
 def attn_forward_rope(meta: Meta, rope: Rope, q, k, v, q_rot, k_pool, v_pool, out, lse=None, k_scale=None,
                       v_scale=None, stream=None) -> None:
     """attn_append_rope, then the attention of the rotated q."""
-    b = meta.batch
+    b = meta.batch or meta.of_batch()
     args = rope.args(q, k, v, b)
     if b is not None and (b.lacks(q_rot, b.nq, b.bf16) or b.lacks(out, b.nq, b.bf16) or b.lacks(lse, b.nlse, b.f32)
                           or b.lacks_pools(k_pool, v_pool) or b.scaled

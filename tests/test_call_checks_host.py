@@ -19,7 +19,7 @@ def lib():
 
 def batch_of(kv_dtype, device=-1):
     meta = pva.Meta()
-    meta.batch = pva.Batch(pva.make_config(HQ, HKV, D, PS, PAGES, 2, T, 64, kv_dtype=kv_dtype), T, device)
+    meta.batch = pva.Batch(HQ, HKV, D, PS * PAGES, kv_dtype, T, device)
     return meta
 
 
@@ -153,6 +153,18 @@ def test_a_table_or_positions_on_another_device():
         rope.args(a["q"], a["k"], a["v"])
     with pytest.raises(ValueError):
         pva.Rope(torch.zeros(64, D), positions=SomewhereElse(torch.zeros(T, dtype=torch.int32)))
+
+
+def test_a_prepared_meta_makes_its_batch_when_first_asked():
+    """From what the config said at prepare, whatever it is changed to later."""
+    cfg = pva.make_config(HQ, HKV, D, PS, PAGES, 2, T, 64, kv_dtype=pva.KV_MXFP4)
+    meta = pva.Meta()
+    assert meta.of_batch() is None
+    meta._sizes = pva._batch_sizes(cfg, T, -1)
+    cfg.num_qo_heads, cfg.kv_dtype = 99, pva.KV_BF16
+    b = meta.of_batch()
+    assert b is meta.batch and (b.tokens, b.q_heads, b.kv_heads, b.head_dim, b.device) == (T, HQ, HKV, D, -1)
+    assert b.pool_bytes == PS * PAGES * pva.mxfp4_row_bytes(HKV, D) and not b.scaled
 
 
 class SomewhereElse(torch.Tensor):
