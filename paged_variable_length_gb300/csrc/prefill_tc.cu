@@ -96,10 +96,11 @@ struct SmemMap {
     static constexpr int kV = kK + 2 * kTile;    // two V stages
     static constexpr int kOff = kV + 2 * kTile;  // per producer warp: source offsets of its rows (64 x int64)
     // FP8: the raw E4M3 rows of one K tile and one V tile (row r at r * D); MXFP4: a ring of
-    // three tiles (K, V, K, ...) of codes and scale words
+    // three tiles (K, V, K, ...) of codes and scale words, then the units to look through for NaN blocks
     static constexpr int kStage8 = kOff + 3 * 64 * 8;
     static constexpr int kMxStep = kPreRows * (D / 2 + 4);  // codes and scale words of a K or V tile
-    static constexpr int kBytes = kStage8 + (KV == PVA_KV_E4M3 ? 2 * kPreRows * D : KV == PVA_KV_MXFP4 ? 3 * kMxStep : 0);
+    static constexpr int kNan = kStage8 + 3 * kMxStep, kNanUnits = 1024;  // int32 each
+    static constexpr int kBytes = KV == PVA_KV_MXFP4 ? kNan + 4 * kNanUnits : kStage8 + (KV == PVA_KV_E4M3 ? 2 * kPreRows * D : 0);
 };
 
 struct Bars {
@@ -114,10 +115,10 @@ struct Bars {
     uint32_t tmem_base;
     int32_t abort_flag;
     uint64_t wait_limit;  // of the work waits (the drains before the CTA leaves: the default)
-    // MXFP4: the units whose staged scales may say NaN (past kNanUnits only their number counts on), and
-    // uc + 1 in entry uc & 3 once unit uc is among them (producer warps are a unit or two apart at most)
-    static constexpr int kNanUnits = 32;
-    int32_t nan_units[kNanUnits], n_nan, nan_noted[4];
+    // MXFP4: how many units' staged scales may say NaN (SmemMap::kNan holds the first kNanUnits of them), and
+    // uc + 1 in entry uc & 3 once unit uc is among them (producer warps are a unit or two apart at most);
+    // the first keys of the unit that fix_nan is at
+    int32_t n_nan, nan_noted[4], nan_first[5];
 };
 
 // A work wait of one whole warp (every lane calls it, converged): the lanes' results are
@@ -199,47 +200,56 @@ __device__ __forceinline__ UnitView unit_view(const PreTile& pt) {
 
 // MXFP4: the NaN of a unit's results, whose NaN blocks entered the products as zeros (a hidden key's weight 0
 // would meet a NaN in every row of the tile).  What a row sees ends at its diagonal, so the first key with
-// a NaN block of K, and of each block of V, says which of its results are NaN.  By the eight softmax
-// warps, a row a thread, each warp looking through its tile's keys; after the unit's results were written.
+// a NaN block of K, and of each block of V, says which of its results are NaN.  By the 256 softmax threads
+// together, a row each, after the unit's results were written; first: shared memory.
 template <int D>
-__device__ void fix_nan(const ForwardParams& p, const PreTile& pt, const CascGroup* cgroups, const int2* cmembers) {
-    constexpr int NB = D / mx::kBlock;
+__device__ void fix_nan(const ForwardParams& p, const PreTile& pt, const CascGroup* cgroups, const int2* cmembers,
+                        int32_t* first) {
+    constexpr int NB = D / mx::kBlock, kWhole = 256;
     const UnitView uv = unit_view(pt);
-    const int h = threadIdx.x >> 7, lane = threadIdx.x & 31, G = p.group, TM = kPreRows / G;
+    const int h = threadIdx.x >> 7, G = p.group, TM = kPreRows / G;
     const int32_t* prow = p.page_table + (int64_t)(uv.casc ? cgroups[-1 - pt.req].leader : pt.req) * p.ld;
     const int scales = mx::scales_at(pt.kvh, p.num_kv_heads, D);
-    int first[1 + NB];
+    if (threadIdx.x <= NB) first[threadIdx.x] = INT_MAX;
+    dev::named_bar_sync(1, kWhole);
+    int mine[1 + NB];
 #pragma unroll
-    for (int i = 0; i <= NB; ++i) first[i] = INT_MAX;
-    for (int key = uv.key_base + lane; key < uv.end[h] && uv.nk[h] > 0; key += 32) {
+    for (int i = 0; i <= NB; ++i) mine[i] = INT_MAX;
+    for (int key = uv.key_base + threadIdx.x; key < uv.key_end; key += kWhole) {
         int64_t page = prow[key >> p.page_shift];
         if (page < 0 || page >= p.num_pages) page = 0;  // (as the producers read it)
         const int64_t at = ((page << p.page_shift) + (key & (p.page_size - 1))) * p.mx_row_bytes + scales;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            if (reinterpret_cast<const uint8_t*>(p.k_pool)[at + i] == mx::kScaleNan) first[0] = min(first[0], key);
-            if (reinterpret_cast<const uint8_t*>(p.v_pool)[at + i] == mx::kScaleNan) first[1 + i] = min(first[1 + i], key);
+            if (reinterpret_cast<const uint8_t*>(p.k_pool)[at + i] == mx::kScaleNan) mine[0] = min(mine[0], key);
+            if (reinterpret_cast<const uint8_t*>(p.v_pool)[at + i] == mx::kScaleNan) mine[1 + i] = min(mine[1 + i], key);
         }
     }
 #pragma unroll
-    for (int i = 0; i <= NB; ++i) first[i] = __reduce_min_sync(0xffffffffu, first[i]);
+    for (int i = 0; i <= NB; ++i) {
+        const int least = __reduce_min_sync(0xffffffffu, mine[i]);
+        if ((threadIdx.x & 31) == 0 && least < INT_MAX) atomicMin(&first[i], least);
+    }
+    dev::named_bar_sync(1, kWhole);
     const int row = threadIdx.x & 127, t = row / G, head = pt.kvh * G + row % G;
-    if (t >= (h ? pt.ntok1 : pt.ntok0)) return;
-    const int limit = uv.casc ? uv.end[h] - 1 : pt.qpos0 + h * TM + t;  // last key that the row sees
-    const float nan = __int_as_float(0x7FFFFFFF);
-    const int64_t orow = (int64_t)(pt.tok0 + h * TM + t) * p.num_qo_heads + head;
-    const int64_t part = uv.casc ? (int64_t)(cmembers[pt.tok0 + h * TM + t].y + pt.qpos0) * p.lay.rows_per_slot + head : 0;
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        if (min(first[0], first[1 + c]) > limit) continue;
-        for (int i = 0; i < 32; ++i) {
-            if (uv.casc) reinterpret_cast<float*>(p.ws + p.lay.partial_o)[part * D + c * 32 + i] = nan;
-            else p.out[orow * D + c * 32 + i] = 0x7FFF;
+    if (t < (h ? pt.ntok1 : pt.ntok0)) {
+        const int limit = uv.casc ? uv.end[h] - 1 : pt.qpos0 + h * TM + t;  // last key that the row sees
+        const float nan = __int_as_float(0x7FFFFFFF);
+        const int64_t orow = (int64_t)(pt.tok0 + h * TM + t) * p.num_qo_heads + head;
+        const int64_t part = uv.casc ? (int64_t)(cmembers[pt.tok0 + h * TM + t].y + pt.qpos0) * p.lay.rows_per_slot + head : 0;
+        for (int c = 0; c < NB; ++c) {
+            if (min(first[0], first[1 + c]) > limit) continue;
+            for (int i = 0; i < 32; ++i) {
+                if (uv.casc) reinterpret_cast<float*>(p.ws + p.lay.partial_o)[part * D + c * 32 + i] = nan;
+                else p.out[orow * D + c * 32 + i] = 0x7FFF;
+            }
+        }
+        if (first[0] <= limit) {
+            if (uv.casc) reinterpret_cast<float*>(p.ws + p.lay.partial_lse)[part] = nan;
+            else if (p.lse != nullptr) p.lse[orow] = nan;
         }
     }
-    if (first[0] > limit) return;
-    if (uv.casc) reinterpret_cast<float*>(p.ws + p.lay.partial_lse)[part] = nan;
-    else if (p.lse != nullptr) p.lse[orow] = nan;
+    dev::named_bar_sync(1, kWhole);
 }
 
 // q_map: Q as a 3-D tensor (D, Hq, T) whose box is one 64-column half of a Q tile (64
@@ -547,7 +557,7 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
                     }
                     if ((__vcmpeq4(mine, 0xFFFFFFFFu) & head_bytes) != 0 && atomicExch(&b->nan_noted[uc & 3], uc + 1) != uc + 1) {
                         const int i = atomicAdd(&b->n_nan, 1);
-                        if (i < Bars::kNanUnits) b->nan_units[i] = u;
+                        if (i < L::kNanUnits) reinterpret_cast<int32_t*>(smem + L::kNan)[i] = u;
                     }
                     // these generic-proxy stores -> the tensor core's operand reads
                     tc::fence_proxy_async_smem();
@@ -1103,11 +1113,12 @@ __global__ void __launch_bounds__(Roles<KV>::kThreads, 1)
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
     }
-    if (MX && warp < 8 && b->n_nan > 0) {
+    if (MX && warp < 8 && !b->abort_flag) {
         // (past the list: every unit; one of another CTA's gets from it nothing that it does not get there)
-        const bool all = b->n_nan > Bars::kNanUnits;
-        for (int i = 0; i < (all ? n_units : b->n_nan); ++i)
-            fix_nan<D>(p, units[all ? i : b->nan_units[i]], cgroups, cmembers);
+        const int n = b->n_nan;
+        const bool all = n > L::kNanUnits;
+        for (int i = 0; i < (all ? n_units : n); ++i)
+            fix_nan<D>(p, units[all ? i : reinterpret_cast<const int32_t*>(smem + L::kNan)[i]], cgroups, cmembers, b->nan_first);
     }
 }
 
@@ -1147,7 +1158,7 @@ bool encode_q_map(const ForwardParams& p, int D, CUtensorMap* m) {
 template <int D, int KV>
 cudaError_t launch_p(const ForwardParams& p, int ctas, cudaStream_t s) {
     const size_t smem = SmemMap<D, KV>::kBytes + 1024;
-    static_assert(SmemMap<D, KV>::kBytes + 1024 + 512 <= 227 * 1024, "shared memory per block");
+    static_assert(SmemMap<D, KV>::kBytes + 1024 + sizeof(Bars) <= 227 * 1024, "shared memory per block");
     cudaError_t e =
         cudaFuncSetAttribute(prefill_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -4,8 +4,10 @@ import numpy as np
 import pytest
 import torch
 
-from test_mxfp4_gpu import DEV, make, prepared, run
+import mx_reference as R
+from paged_variable_length_gb300 import pva
 from paged_variable_length_gb300 import workloads as W
+from test_mxfp4_gpu import DEV, make, prepared, run
 
 pytestmark = pytest.mark.gpu
 
@@ -72,8 +74,8 @@ def test_hidden_values_of_many_units():
     masked_case(wl, [(i, 10 + i % 30, i % 8, (37 * i) % 128, True, NAN) for i in range(0, B, 3)])
 
 
-def test_hidden_values_of_more_units_than_a_cta_notes():
-    """Every unit of a long queue holds a NaN (more of them on a CTA than it lists)."""
+def test_hidden_values_of_every_unit():
+    """Every unit of a long queue holds a NaN."""
     B = 700
     wl = W.custom([17] * B, [17 + i % 5 for i in range(B)], 8, 8, 64, 4, seed=4)
     masked_case(wl, [(i, i % 17, h, (37 * i) % 64, True, NAN) for i in range(B) for h in range(8)], max_q_len=17)
@@ -82,7 +84,6 @@ def test_hidden_values_of_more_units_than_a_cta_notes():
 def test_values_of_a_shared_prefix():
     """A NaN in a prefix that several decodes share reaches each of them, in its block and nowhere else."""
     from test_parity_gpu import _cascade_batch
-    import mx_reference as R
 
     wl = _cascade_batch(seed=4)
     t = make(wl, wl.seed)
@@ -111,3 +112,22 @@ def test_values_of_a_shared_prefix():
         if cascade:
             ok = torch.as_tensor(~want).to(DEV)
             assert torch.equal(out[ok], clean[ok])
+
+
+def test_hidden_values_of_more_units_than_a_cta_lists():
+    """160 000 units, each with a NaN: more than a thousand on a CTA."""
+    B, Hq, Hkv, D = 20_000, 128, 8, 64
+    wl = W.Workload("many", [2] * B, [2] * B, Hq, Hkv, D, 2, B, np.arange(B, dtype=np.int32)[:, None])
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q, k, v = (torch.randn(2 * B, h, D, generator=g, device=DEV).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    t = {"q": q, "k": k, "v": v}
+    for n in ("kp", "vp"):
+        t[n] = torch.zeros(2 * B, R.row_layout(Hkv, D)[2], dtype=torch.uint8, device=DEV)
+    eng = prepared(wl, max_q_len=2, enable_cascade=False)
+    clean, clean_lse = run(wl, t, eng)
+    v[1::2, :, 40] = NAN                    # the second token's, in every head's second block
+    out, lse = run(wl, t, eng)
+    nan = torch.isnan(out)
+    assert bool(nan[1::2, :, 32:].all()) and not bool(nan[1::2, :, :32].any()) and not bool(nan[::2].any())
+    assert torch.equal(out[~nan], clean[~nan]) and torch.equal(lse, clean_lse)
+    assert pva.attn_debug_plan_counts(eng.meta)["pre_tiles"] > 1024 * torch.cuda.get_device_properties(0).multi_processor_count
