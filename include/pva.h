@@ -93,6 +93,7 @@ typedef enum pva_status {
 #define PVA_DEVERR_LIMITS     0x10u  /* batch exceeds cfg.max_batch / max_tokens / max_kv_len or the max_q_len hint */
 #define PVA_DEVERR_TIMEOUT    0x20u  /* a bounded wait inside a kernel gave up (internal error) */
 #define PVA_DEVERR_POSITION   0x40u  /* a token's rotary position lies outside [0, max_positions) */
+#define PVA_DEVERR_STATE      0x80u  /* a state slot outside [-1, num_states), or two requests at one (linear attention) */
 
 /*
  * Element type of the paged KV pool (pva_config.kv_dtype).  The pages name the
@@ -362,7 +363,116 @@ PVA_API pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope,
                              const float* v_scale, void* out, float* lse, void* stream);
 
 /*
- * Debug/test helper: synchronises the stream of the last prepare/forward on
+ * Norm of each head of q and k, before the rotation: a head row x becomes x / sqrt(mean(x^2) + eps) *
+ * gain, in fp32 (so are the squares and their sum: a row with elements beyond about 2^60 overflows them
+ * and becomes 0, as one whose squares vanish beside eps does).
+ */
+typedef struct pva_qk_norm {
+    const float* q_gain;        /* DEVICE fp32 [head_dim], 16-byte aligned, for every q head; NULL: ones */
+    const float* k_gain;        /* the same for k */
+    float eps;                  /* >= 0 and finite */
+    int32_t reserved;           /* 0 */
+} pva_qk_norm;
+
+/*
+ * attn_append_rope and attn_forward_rope with q and k normed first: norm, rotation and store in one
+ * pass, every step in fp32 and one rounding into what holds the result.  rope gives the strides and
+ * the rotation as there, and may say rot_dim 0 here (cos_sin NULL, max_positions ignored): a norm
+ * without a rotation.  norm NULL is refused (those calls are the ones without it).
+ */
+PVA_API pva_status attn_append_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const pva_rope* rope,
+                                 const void* q, const void* k, const void* v, void* q_out, void* k_pool,
+                                 void* v_pool, const float* k_scale, const float* v_scale, void* stream);
+PVA_API pva_status attn_forward_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const pva_rope* rope,
+                                  const void* q, const void* k, const void* v, void* q_rot, void* k_pool,
+                                  void* v_pool, const float* k_scale, const float* v_scale, void* out,
+                                  float* lse, void* stream);
+
+/*
+ * Norm and rotation without a pool, as a linear attention layer takes its q and k: q into q_out (bf16
+ * [T, Hq, D], contiguous) and k into k_out ([T, Hkv, D]).  meta: of either kind (attn_prepare_metadata,
+ * attn_linear_prepare).  norm NULL: the rotation alone; rope as above (ld_v is ignored).  q and q_out may
+ * both be NULL, or k and k_out.  An output is its own input (when that is contiguous, as one token's
+ * always is) or lies outside the memory from the first to the last element of q and of k, and outside
+ * the other output.  A token whose position lies outside the table sets PVA_DEVERR_POSITION and nothing
+ * of it is written.
+ */
+PVA_API pva_status attn_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const pva_rope* rope, const void* q,
+                          const void* k, void* q_out, void* k_out, void* stream);
+
+/*
+ * Linear attention with a decay for each head: instead of a pool of keys and values a request keeps one
+ * D x D state a kv head.  For each of its new tokens t in turn, with g the log decay of token t and head h,
+ *   S <- e^g S + k_t v_t^T      (S[i][j]: element i of k, j of v; fp32)
+ *   o_t = scale * q_t^T S       (for every q head of kv head h)
+ * A flat, mixed batch as above; the states lie in a pool of slots, fp32 [num_states, Hkv, D, D].
+ */
+typedef struct pva_linear_config {
+    int32_t num_qo_heads;       /* Hq */
+    int32_t num_kv_heads;       /* Hkv; Hq % Hkv == 0; q head h reads the state of kv head h / (Hq / Hkv) */
+    int32_t head_dim;           /* D: 64 or 128 */
+    float scale;                /* <= 0 selects 1/sqrt(head_dim) */
+    int64_t num_states;         /* slots of the state pool, below 2^31 */
+    int32_t max_batch;          /* upper bound on requests per batch, at most 65535 */
+    int32_t max_tokens;         /* upper bound on new tokens per batch */
+} pva_linear_config;
+
+/* Device bytes of the workspace of attn_linear_prepare; 0 when cfg is invalid or unsupported. */
+PVA_API size_t attn_linear_workspace_size(const pva_linear_config* cfg);
+
+/*
+ * Once per batch, like attn_prepare_metadata (validation on the device, one launch, no sync): the plan of
+ * the linear layers' calls.
+ *   cu_seqlens_q   int32 [batch+1], as there
+ *   cache_seqlens  int32 [batch]: a request's tokens including its new ones
+ *   state_in       int32 [batch]: slot of the state that a request goes on from, -1: from zero.  A request
+ *                  without earlier tokens (cache_seqlens = its new tokens) starts from zero whatever this says,
+ *                  and its slot is not read.  NULL: every request starts from zero.
+ *   state_out      int32 [batch]: slot that receives a request's state after its new tokens, -1: none.  The same
+ *                  array as state_in updates states in place; other slots keep the old ones (checkpoints, drafts
+ *                  that may be dropped), and several requests may go on from one.  NULL: no state is kept.
+ *   max_q_len      as there; a batch with max_q_len <= 16 launches no tensor-core kernel
+ *   workspace      device, at least attn_linear_workspace_size(cfg) bytes, 256-byte aligned
+ * A slot outside [-1, num_states), a state_out slot of two requests, and a state_out slot that another request
+ * goes on from set PVA_DEVERR_STATE: of the requests at fault (those that would write, in the last case the
+ * writer) nothing is written.  Requests without new tokens neither read nor write a state.
+ * The arrays must stay unchanged until the last call using `meta`.
+ */
+PVA_API pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_seqlens_q,
+                               const int32_t* cache_seqlens, const int32_t* state_in, const int32_t* state_out,
+                               int32_t batch, int32_t total_tokens, int32_t max_q_len, void* workspace,
+                               size_t workspace_bytes, void* stream, pva_meta* meta);
+
+typedef struct pva_linear_args {
+    const float* log_decay;     /* DEVICE fp32 [Hkv], or [total_tokens, Hkv] with ld_decay: natural logs, -inf (the
+                                   state is dropped) to 0; larger ones grow the state, as far as fp32 holds it */
+    int64_t ld_decay;           /* 0: one value a head; else elements between tokens, at least Hkv */
+    int64_t ld_q, ld_k, ld_v;   /* elements between consecutive tokens (multiples of 8); heads are contiguous */
+    float* states;              /* DEVICE fp32 [num_states, Hkv, D, D], 16-byte aligned, updated in place */
+} pva_linear_args;
+
+/*
+ * Once per layer.  q, k, v: bf16 [T, heads, D], 16-byte aligned; out: bf16 [T, Hq, D], contiguous, outside the
+ * memory of q, k, v, the decays and the states.  Requests of up to 16 new tokens run the recurrence as it stands,
+ * in fp32; longer ones in chunks of 128 tokens on the tensor cores, where the weights within a chunk and a copy
+ * of the state enter the products as bf16 (out moves by about half a bf16 step of its terms; the states keep
+ * fp32's accuracy).  Tokens hidden by causality have no part in a token's output, whatever they hold.
+ */
+PVA_API pva_status attn_linear_forward(const pva_meta* meta, const pva_linear_args* args, const void* q, const void* k,
+                               const void* v, void* out, void* stream);
+
+/*
+ * attn_norm_rope of q and k into q_rot and k_rot, then attn_linear_forward of those: a linear layer's call
+ * from projections to output.  norm may be NULL.  q, k and v have rope's strides (args' are ignored); q_rot and
+ * k_rot lie outside the memory of v, the decays, the states and out as well.
+ */
+PVA_API pva_status attn_linear_forward_norm_rope(const pva_meta* meta, const pva_linear_args* args,
+                                         const pva_qk_norm* norm, const pva_rope* rope, const void* q,
+                                         const void* k, const void* v, void* q_rot, void* k_rot, void* out,
+                                         void* stream);
+
+/*
+ * Debug/test helper (metas of either kind): synchronises the stream of the last prepare/forward on
  * meta's workspace, then reads the device error word into *error_bits
  * (PVA_DEVERR_*).  Returns PVA_ERR_DEVICE_CHECK when any bit is set.
  */
@@ -383,7 +493,7 @@ PVA_API pva_status attn_get_device_status(const pva_meta* meta, uint32_t* error_
 PVA_API pva_status attn_set_timing_events(pva_meta* meta, void* const* events, int32_t n);
 
 /*
- * Test helper for the kernels' bounded waits: every wait inside the forward kernels
+ * Test helper for the kernels' bounded waits (metas of either kind): every wait inside the forward kernels
  * (on a pipeline stage, the tensor core, the work queue) gives up after 2 s, sets
  * PVA_DEVERR_TIMEOUT, waits (with the 2 s limit) for its CTA's own copies and MMAs,
  * frees what it holds and returns, so a wedged kernel ends with a status instead of

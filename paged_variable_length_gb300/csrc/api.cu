@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "linear.h"
 #include "mxfp4.cuh"
 #include "pva_internal.h"
 
@@ -367,21 +368,17 @@ pva_status store_impl(const MetaHost* h, const void* k, const void* v, void* k_p
     return PVA_OK;
 }
 
-// Host checks of a pva_rope and the activations it goes with.
-pva_status check_rope(const MetaHost* h, const pva_rope* rope, const void* q, const void* k, const void* v,
-                      const void* q_out, const void* k_scale, const void* v_scale) {
-    if (rope == nullptr || rope->cos_sin == nullptr) return PVA_ERR_INVALID_ARG;
+// Host checks of a pva_rope (and a norm, or null) and the activations it goes with.
+pva_status check_rope(const MetaHost* h, const pva_rope* rope, const pva_qk_norm* norm, const void* q, const void* k,
+                      const void* v, const void* q_out, const void* k_scale, const void* v_scale) {
+    const pva_status st = check_rotation(rope, norm, h->cfg.head_dim);
+    if (st != PVA_OK) return st;
     const int64_t T = h->total_tokens, Hq = h->cfg.num_qo_heads, Hkv = h->cfg.num_kv_heads, D = h->cfg.head_dim;
     if (T > 0 && (k == nullptr || v == nullptr || (q != nullptr && q_out == nullptr))) return PVA_ERR_INVALID_ARG;
-    if (rope->max_positions <= 0 || rope->rot_dim <= 0 || rope->rot_dim > D || rope->reserved != 0)
-        return PVA_ERR_INVALID_ARG;
-    if (rope->rot_dim % 16 != 0) return PVA_ERR_UNSUPPORTED;
     if ((q != nullptr && rope->ld_q < Hq * D) || rope->ld_k < Hkv * D || rope->ld_v < Hkv * D)
         return PVA_ERR_INVALID_ARG;
     if ((q != nullptr && rope->ld_q % 8 != 0) || rope->ld_k % 8 != 0 || rope->ld_v % 8 != 0) return PVA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope->cos_sin) ||
-        (reinterpret_cast<uintptr_t>(rope->positions) & 3u) != 0)
-        return PVA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return PVA_ERR_INVALID_ARG;
     if (h->cfg.kv_dtype == PVA_KV_E4M3 && (k_scale == nullptr || v_scale == nullptr)) return PVA_ERR_INVALID_ARG;
     if (T == 0 || q == nullptr) return PVA_OK;
     // q_out is q itself (then contiguous, as one token always is), or lies outside the spans of q, k and v
@@ -396,18 +393,14 @@ pva_status check_rope(const MetaHost* h, const pva_rope* rope, const void* q, co
     return PVA_OK;
 }
 
-RopeParams rope_params(const MetaHost* h, const pva_rope* rope, const void* q, void* q_out) {
+RopeParams rope_params(const MetaHost* h, const pva_rope* rope, const pva_qk_norm* norm, const void* q, void* q_out) {
     RopeParams rp{};
     rp.q = static_cast<const uint16_t*>(q);
     rp.q_out = static_cast<uint16_t*>(q_out);
     rp.ld_q = rope->ld_q;
     rp.ld_k = rope->ld_k;
     rp.ld_v = rope->ld_v;
-    rp.cos_sin = rope->cos_sin;
-    rp.positions = rope->positions;
-    rp.max_positions = rope->max_positions;
-    rp.rot_dim = rope->rot_dim;
-    rp.interleaved = rope->interleaved ? 1 : 0;
+    set_rotation(rope, norm, &rp);
     rp.row_bytes = mx::row_bytes(h->cfg.num_kv_heads, h->cfg.head_dim);
     rp.batch = h->batch;
     rp.sm_count = h->sm_count;
@@ -455,21 +448,42 @@ pva_status attn_load_kvcache_mxfp4kv(const pva_meta* meta, const void* k_pool, c
     return PVA_OK;
 }
 
-pva_status attn_append_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k, const void* v,
-                            void* q_out, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
-                            void* stream) {
-    const MetaHost* h = meta_of(meta);
-    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
-    const pva_status st = check_rope(h, rope, q, k, v, q_out, k_scale, v_scale);
+namespace pva {
+namespace {
+
+pva_status append_impl(const MetaHost* h, const pva_rope* rope, const pva_qk_norm* norm, const void* q, const void* k,
+                       const void* v, void* q_out, void* k_pool, void* v_pool, const float* k_scale,
+                       const float* v_scale, void* stream) {
+    const pva_status st = check_rope(h, rope, norm, q, k, v, q_out, k_scale, v_scale);
     if (st != PVA_OK) return st;
     if (k_pool == nullptr || v_pool == nullptr || !aligned16(k_pool) || !aligned16(v_pool)) return PVA_ERR_INVALID_ARG;
     ForwardParams fp = forward_params(h, nullptr, k, v, k_pool, v_pool, nullptr, nullptr);
     fp.k_scale = k_scale;
     fp.v_scale = v_scale;
-    if (launch_append(fp, rope_params(h, rope, q, q_out), h->cfg.head_dim, h->cfg.kv_dtype,
+    if (launch_append(fp, rope_params(h, rope, norm, q, q_out), h->cfg.head_dim, h->cfg.kv_dtype,
                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return PVA_ERR_CUDA;
     return PVA_OK;
+}
+
+}  // namespace
+}  // namespace pva
+
+pva_status attn_append_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k, const void* v,
+                            void* q_out, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                            void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    return append_impl(h, rope, nullptr, q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, stream);
+}
+
+pva_status attn_append_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const pva_rope* rope, const void* q,
+                                 const void* k, const void* v, void* q_out, void* k_pool, void* v_pool,
+                                 const float* k_scale, const float* v_scale, void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    if (norm == nullptr) return PVA_ERR_INVALID_ARG;
+    return append_impl(h, rope, norm, q, k, v, q_out, k_pool, v_pool, k_scale, v_scale, stream);
 }
 
 int64_t attn_mxfp4_row_bytes(int32_t num_kv_heads, int32_t head_dim) {
@@ -523,7 +537,7 @@ namespace {
 // With `rope`, q is rotated into q_rot (which the attention reads) and k on its way to the pool.
 pva_status forward_impl(const MetaHost* h, const void* q, const void* k, const void* v, void* k_pool, void* v_pool,
                         const float* k_scale, const float* v_scale, void* out, float* lse, void* stream,
-                        const pva_rope* rope = nullptr, void* q_rot = nullptr) {
+                        const pva_rope* rope = nullptr, void* q_rot = nullptr, const pva_qk_norm* norm = nullptr) {
     if (h->total_tokens > 0 && (q == nullptr || k == nullptr || v == nullptr || out == nullptr))
         return PVA_ERR_INVALID_ARG;
     if (k_pool == nullptr || v_pool == nullptr) return PVA_ERR_INVALID_ARG;
@@ -546,7 +560,7 @@ pva_status forward_impl(const MetaHost* h, const void* q, const void* k, const v
                                                         : cudaEventRecord(ev, s);
     };
     if (mark(0) != cudaSuccess) return PVA_ERR_CUDA;
-    if ((rope != nullptr ? launch_append(fp, rope_params(h, rope, q, q_rot), h->cfg.head_dim, h->cfg.kv_dtype, s)
+    if ((rope != nullptr ? launch_append(fp, rope_params(h, rope, norm, q, q_rot), h->cfg.head_dim, h->cfg.kv_dtype, s)
                          : launch_store_any(h, fp, s)) != cudaSuccess)
         return PVA_ERR_CUDA;
     if (mark(1) != cudaSuccess) return PVA_ERR_CUDA;
@@ -592,27 +606,69 @@ pva_status attn_forward_mxfp4kv(const pva_meta* meta, const void* q, const void*
     return forward_impl(h, q, k, v, k_pool, v_pool, nullptr, nullptr, out, lse, stream);
 }
 
-pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k, const void* v,
-                             void* q_rot, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
-                             void* out, float* lse, void* stream) {
-    const MetaHost* h = meta_of(meta);
-    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+namespace pva {
+namespace {
+
+pva_status forward_rope_impl(const MetaHost* h, const pva_rope* rope, const pva_qk_norm* norm, const void* q,
+                             const void* k, const void* v, void* q_rot, void* k_pool, void* v_pool,
+                             const float* k_scale, const float* v_scale, void* out, float* lse, void* stream) {
     if (h->total_tokens > 0 && (q == nullptr || q_rot == nullptr)) return PVA_ERR_INVALID_ARG;
-    const pva_status st = check_rope(h, rope, q, k, v, q_rot, k_scale, v_scale);
+    const pva_status st = check_rope(h, rope, norm, q, k, v, q_rot, k_scale, v_scale);
     if (st != PVA_OK) return st;
     // (rows of q_rot are read while others' results are written)
     const uintptr_t bytes = (uintptr_t)h->total_tokens * h->cfg.num_qo_heads * h->cfg.head_dim * 2;
     const uintptr_t o = reinterpret_cast<uintptr_t>(out), r = reinterpret_cast<uintptr_t>(q_rot);
     if (o < r + bytes && r < o + bytes) return PVA_ERR_INVALID_ARG;
-    return forward_impl(h, q, k, v, k_pool, v_pool, k_scale, v_scale, out, lse, stream, rope, q_rot);
+    return forward_impl(h, q, k, v, k_pool, v_pool, k_scale, v_scale, out, lse, stream, rope, q_rot, norm);
 }
 
-pva_status attn_get_device_status(const pva_meta* meta, uint32_t* error_bits) {
+}  // namespace
+}  // namespace pva
+
+pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope, const void* q, const void* k, const void* v,
+                             void* q_rot, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                             void* out, float* lse, void* stream) {
     const MetaHost* h = meta_of(meta);
     if (h == nullptr) return PVA_ERR_NOT_PREPARED;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(h->stream)) != cudaSuccess) return PVA_ERR_CUDA;
+    return forward_rope_impl(h, rope, nullptr, q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale, out, lse, stream);
+}
+
+pva_status attn_forward_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const pva_rope* rope, const void* q,
+                                  const void* k, const void* v, void* q_rot, void* k_pool, void* v_pool,
+                                  const float* k_scale, const float* v_scale, void* out, float* lse, void* stream) {
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    if (norm == nullptr) return PVA_ERR_INVALID_ARG;
+    return forward_rope_impl(h, rope, norm, q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale, out, lse, stream);
+}
+
+namespace pva {
+namespace {
+
+// The plan header and the stream of a meta of either kind.
+bool header_of(const pva_meta* meta, uint8_t** header, cudaStream_t* stream) {
+    if (const LinHost* l = lin_of(meta)) {
+        *header = l->ws + l->lay.header;
+        *stream = static_cast<cudaStream_t>(l->stream);
+        return true;
+    }
+    const MetaHost* h = meta_of(meta);
+    if (h == nullptr) return false;
+    *header = h->ws + h->lay.header;
+    *stream = static_cast<cudaStream_t>(h->stream);
+    return true;
+}
+
+}  // namespace
+}  // namespace pva
+
+pva_status attn_get_device_status(const pva_meta* meta, uint32_t* error_bits) {
+    uint8_t* header;
+    cudaStream_t s;
+    if (!header_of(meta, &header, &s)) return PVA_ERR_NOT_PREPARED;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return PVA_ERR_CUDA;
     PlanHeader hdr{};
-    if (cudaMemcpy(&hdr, h->ws + h->lay.header, sizeof(hdr), cudaMemcpyDeviceToHost) != cudaSuccess)
+    if (cudaMemcpy(&hdr, header, sizeof(hdr), cudaMemcpyDeviceToHost) != cudaSuccess)
         return PVA_ERR_CUDA;
     if (error_bits) *error_bits = hdr.error_bits;
     return hdr.error_bits ? PVA_ERR_DEVICE_CHECK : PVA_OK;
@@ -633,13 +689,14 @@ pva_status attn_set_timing_events(pva_meta* meta, void* const* events, int32_t n
 }
 
 pva_status attn_debug_set_wait_limit(const pva_meta* meta, int64_t limit_ns) {
-    const MetaHost* h = meta_of(meta);
-    if (h == nullptr) return PVA_ERR_NOT_PREPARED;
+    uint8_t* header;
+    cudaStream_t s;
+    if (!header_of(meta, &header, &s)) return PVA_ERR_NOT_PREPARED;
     // the header holds limit + 1 (0: the default); limits above ~4.29 s are capped
     uint32_t v = 0;
     if (limit_ns >= 0) v = (uint32_t)((limit_ns < 0xFFFFFFFEll ? limit_ns : 0xFFFFFFFEll) + 1);
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(h->stream)) != cudaSuccess) return PVA_ERR_CUDA;
-    if (cudaMemcpy(h->ws + h->lay.header + offsetof(PlanHeader, wait_override), &v, sizeof(v),
+    if (cudaStreamSynchronize(s) != cudaSuccess) return PVA_ERR_CUDA;
+    if (cudaMemcpy(header + offsetof(PlanHeader, wait_override), &v, sizeof(v),
                    cudaMemcpyHostToDevice) != cudaSuccess)
         return PVA_ERR_CUDA;
     return PVA_OK;

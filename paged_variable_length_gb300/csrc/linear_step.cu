@@ -1,0 +1,323 @@
+// K9, K10: linear attention's plan, and its recurrence for requests of few new tokens.
+//
+// K10, for one (request, kv head): S <- e^{g_t} S + k_t v_t^T, o_t = scale q_t^T S_t, token by token, all
+// in fp32.  The state is read once and written once for all of the request's new tokens, and the G q
+// heads of the kv head share it.  Bound: HBM, 2 x 4 D^2 bytes a request and kv head (D = 128: 128 KiB
+// against 2 KiB of activations).  A thread keeps four columns of some rows in registers, so that a warp's
+// accesses are whole rows and every load of the state is in flight before the first is used; the columns
+// of a state may be dealt to 2 or 4 CTAs.
+#include <cuda_runtime.h>
+
+#include "device_utils.cuh"
+#include "linear.h"
+
+namespace pva {
+namespace {
+
+// ---------------------------------------------------------------- K9: the plan
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 256;  // segments sorted by chunks (more: the first bucket)
+
+// One CTA.  Validates the batch, resolves each request's state slots, lists the long requests'
+// segments, most tokens first, and notes each token's request.  A state slot is claimed by writing the
+// request's index to it and looking who is there afterwards: what an earlier batch left in a slot that
+// no one claimed is told by that request's own out slot being another.
+__global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlanParams p) {
+    __shared__ int32_t hist[kBuckets], first[kBuckets];
+    __shared__ int32_t n_items, n_pre, n_segs;
+    __shared__ uint32_t all_err;
+    PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
+    int2* req_state = reinterpret_cast<int2*>(p.ws + p.lay.req_state);
+    int32_t* claim = reinterpret_cast<int32_t*>(p.ws + p.lay.claim);
+    int32_t* tok_req = reinterpret_cast<int32_t*>(p.ws + p.lay.tok_req);
+    LinItem* items = reinterpret_cast<LinItem*>(p.ws + p.lay.items);
+    LinItem* pre = reinterpret_cast<LinItem*>(p.ws + p.lay.pre_items);
+    const int tid = threadIdx.x, B = p.batch;
+    for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+    if (tid == 0) n_items = n_pre = n_segs = 0, all_err = 0;
+
+    uint32_t err = 0;
+    for (int i = tid; i < B; i += kPlanThreads) {
+        const int c0 = p.cu[i], c1 = p.cu[i + 1];
+        if (c0 < 0 || c1 < c0 || c1 > p.total_tokens || (i == 0 && c0 != 0) || (i == B - 1 && c1 != p.total_tokens)) {
+            err |= kErrCu;
+            continue;
+        }
+        if (c1 - c0 > p.seqlens[i]) err |= kErrQgtKv;
+        if (c1 - c0 > p.max_q_len) err |= kErrLimits;
+    }
+    if (B == 0 && tid == 0 && p.cu[0] != 0) err |= kErrCu;
+    const bool fatal = __syncthreads_or(err != 0);
+    if (err) atomicOr(&all_err, err);
+
+    // slots: -1 nothing, -2 outside the pool
+    auto slot_in = [&](int i) -> int {
+        const int n = p.cu[i + 1] - p.cu[i];
+        if (n <= 0 || p.state_in == nullptr || p.seqlens[i] <= n) return -1;  // starts from zero
+        const int s = p.state_in[i];
+        return s < -1 || s >= p.num_states ? -2 : s;
+    };
+    auto slot_out = [&](int i) -> int {
+        if (p.cu[i + 1] - p.cu[i] <= 0 || p.state_out == nullptr) return -1;
+        const int s = p.state_out[i];
+        return s < -1 || s >= p.num_states ? -2 : s;
+    };
+    if (!fatal) {
+        for (int i = tid; i < B; i += kPlanThreads) {
+            const int in = slot_in(i), out = slot_out(i);
+            const bool bad = in == -2 || out == -2;
+            req_state[i] = bad ? make_int2(-2, -2) : make_int2(in, out);
+            if (bad) atomicOr(&all_err, kErrState);
+            if (!bad && out >= 0) claim[out] = i;
+        }
+        __syncthreads();
+        // two requests of one out slot are both skipped, and one that writes where another reads; every
+        // look is at the slots as given, so what is skipped depends on no order
+        auto clash = [&](int j) {
+            req_state[j].x = -2;
+            atomicOr(&all_err, kErrState);
+        };
+        for (int i = tid; i < B; i += kPlanThreads) {
+            const int in = slot_in(i), out = slot_out(i);
+            if (in == -2 || out == -2) continue;
+            if (out >= 0 && claim[out] != i) {
+                clash(i);
+                clash(claim[out]);
+            }
+            if (in >= 0) {
+                const int j = claim[in];
+                if (j >= 0 && j < B && j != i && slot_in(j) != -2 && slot_out(j) == in) clash(j);
+            }
+        }
+        __syncthreads();
+    }
+    // how a request is cut: chunks of a segment, and segments
+    auto cut = [&](int n, int* per) -> int {
+        const int chunks = (n + kChunk - 1) / kChunk;
+        const int want = (n + p.seg_tokens - 1) / p.seg_tokens;
+        *per = (chunks + want - 1) / want;
+        return (chunks + *per - 1) / *per;
+    };
+    auto is_long = [&](int i, int* n) {
+        *n = p.cu[i + 1] - p.cu[i];
+        return *n > kStepTokens && req_state[i].x != -2;
+    };
+    if (!fatal) {
+        for (int i = tid; i < B; i += kPlanThreads) {
+            int n, per;
+            if (!is_long(i, &n)) continue;
+            const int nseg = cut(n, &per);
+            for (int s = 0; s < nseg; ++s) {
+                const int chunks = (min(per * kChunk, n - s * per * kChunk) + kChunk - 1) / kChunk;
+                atomicAdd(&hist[kBuckets - min(chunks, kBuckets)], 1);
+            }
+        }
+        __syncthreads();
+        if (tid < 32) {  // where each bucket starts
+            int sum = 0;
+            for (int b0 = 0; b0 < kBuckets; b0 += 32) {
+                const int v = hist[b0 + tid];
+                int x = v;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (tid >= d) x += y;
+                }
+                first[b0 + tid] = sum + x - v;
+                sum += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (tid == 0) n_items = sum;
+        }
+        __syncthreads();
+        for (int i = tid; i < B; i += kPlanThreads) {
+            int n, per;
+            if (!is_long(i, &n)) continue;
+            const int nseg = cut(n, &per);
+            const int at = nseg > 1 ? atomicAdd(&n_pre, nseg - 1) : 0;
+            LinItem it;
+            it.req = i;
+            it.nseg = nseg;
+            it.base = nseg > 1 ? atomicAdd(&n_segs, nseg) : 0;
+            it.in = req_state[i].x;
+            it.out = req_state[i].y;
+            for (int s = 0; s < nseg; ++s) {
+                it.seg = s;
+                it.tok0 = p.cu[i] + s * per * kChunk;
+                it.ntok = min(per * kChunk, n - s * per * kChunk);
+                items[atomicAdd(&first[kBuckets - min((it.ntok + kChunk - 1) / kChunk, kBuckets)], 1)] = it;
+                if (s < nseg - 1) pre[at + s] = it;
+            }
+        }
+        // requests of the tokens: a few tokens by one thread, many by the block
+        for (int i = tid; i < B; i += kPlanThreads) {
+            const int c0 = p.cu[i], n = p.cu[i + 1] - c0;
+            if (n <= kStepTokens)
+                for (int t = 0; t < n; ++t) tok_req[c0 + t] = i;
+        }
+        for (int i = 0; i < B; ++i) {
+            const int c0 = p.cu[i], n = p.cu[i + 1] - c0;
+            if (n > kStepTokens)
+                for (int t = tid; t < n; t += kPlanThreads) tok_req[c0 + t] = i;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        hdr->n_pre_tiles = fatal ? 0 : n_items;
+        hdr->n_casc_tiles = fatal ? 0 : n_pre;
+        hdr->wait_override = 0;
+        hdr->error_bits = all_err;
+    }
+}
+
+// ---------------------------------------------------------------- K10: token by token
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// N consecutive bf16 as fp32 (N = 2, 4 or a multiple of 8).
+template <int N>
+__device__ __forceinline__ void load_bf16(const uint16_t* src, float (&x)[N]) {
+    if constexpr (N == 2) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src));
+        x[0] = bf_lo(w), x[1] = bf_hi(w);
+    } else if constexpr (N == 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+        x[0] = bf_lo(w.x), x[1] = bf_hi(w.x), x[2] = bf_lo(w.y), x[3] = bf_hi(w.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + i));
+            x[i] = bf_lo(w.x), x[i + 1] = bf_hi(w.x), x[i + 2] = bf_lo(w.y), x[i + 3] = bf_hi(w.y);
+            x[i + 4] = bf_lo(w.z), x[i + 5] = bf_hi(w.z), x[i + 6] = bf_lo(w.w), x[i + 7] = bf_hi(w.w);
+        }
+    }
+}
+
+constexpr int kHeadsAtOnce = 4;  // q heads whose results meet in shared memory together
+
+// P: CTAs that share a state's columns.
+template <int D, int P>
+struct StepShape {
+    static constexpr int kThreads = 2 * D;
+    static constexpr int kCols = D / P;              // columns of a CTA
+    static constexpr int kLanes = kCols / 4;         // lanes of a row
+    static constexpr int kGroups = kThreads / kLanes;
+    static constexpr int kRows = D / kGroups;        // rows of a thread
+    static constexpr int kWarps = kThreads / 32;
+};
+
+template <int D, int P>
+__global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(const LinParams p) {
+    using L = StepShape<D, P>;
+    constexpr int R = L::kRows, H = kHeadsAtOnce;
+    __shared__ alignas(16) float red[2][L::kWarps][H][L::kCols];
+    dev::grid_dep_wait();
+    dev::grid_dep_launch();
+    const int req = blockIdx.y, kvh = blockIdx.x / P, col0 = (blockIdx.x % P) * L::kCols;
+    const uint32_t errors = reinterpret_cast<const PlanHeader*>(p.ws + p.lay.header)->error_bits;
+    const int2 slots = reinterpret_cast<const int2*>(p.ws + p.lay.req_state)[req];
+    const int c0 = p.cu[req], n = p.cu[req + 1] - c0;
+    if ((errors & kErrFatal) || n <= 0 || n > kStepTokens || slots.x == -2) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int col = 4 * (tid % L::kLanes), row0 = (tid / L::kLanes) * R;
+
+    const int64_t per_head = (int64_t)D * D;
+    float4 S[R];
+    if (slots.x >= 0) {
+        const float* src = p.states + ((int64_t)slots.x * p.num_kv_heads + kvh) * per_head + row0 * D + col0 + col;
+#pragma unroll
+        for (int i = 0; i < R; ++i) S[i] = *reinterpret_cast<const float4*>(src + i * D);
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    int buf = 0;
+    for (int t = 0; t < n; ++t) {
+        const int64_t tok = c0 + t;
+        const float g = p.log_decay[(p.ld_decay ? tok * p.ld_decay : 0) + kvh];
+        float k[R], v[4];
+        load_bf16<R>(p.k + tok * p.ld_k + kvh * D + row0, k);
+        load_bf16<4>(p.v + tok * p.ld_v + kvh * D + col0 + col, v);
+        const float lam = expf(g < kLeastLogDecay ? kLeastLogDecay : g);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            S[i].x = fmaf(k[i], v[0], lam * S[i].x);
+            S[i].y = fmaf(k[i], v[1], lam * S[i].y);
+            S[i].z = fmaf(k[i], v[2], lam * S[i].z);
+            S[i].w = fmaf(k[i], v[3], lam * S[i].w);
+        }
+        for (int h0 = 0; h0 < p.group; h0 += H, buf ^= 1) {
+            const int heads = min(H, p.group - h0);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                if (h >= heads) break;
+                float q[R];
+                load_bf16<R>(p.q + tok * p.ld_q + (kvh * p.group + h0 + h) * D + row0, q);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    o.x = fmaf(q[i], S[i].x, o.x);
+                    o.y = fmaf(q[i], S[i].y, o.y);
+                    o.z = fmaf(q[i], S[i].z, o.z);
+                    o.w = fmaf(q[i], S[i].w, o.w);
+                }
+#pragma unroll
+                for (int m = L::kLanes; m < 32; m *= 2) {
+                    o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+                    o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+                    o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+                    o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+                }
+                if (lane < L::kLanes) *reinterpret_cast<float4*>(&red[buf][warp][h][col]) = o;
+            }
+            __syncthreads();
+            // (the other buffer is written before the next barrier: nobody is more than one ahead)
+            for (int x = tid; x < heads * L::kCols / 2; x += L::kThreads) {
+                const int h = x / (L::kCols / 2), c = 2 * (x % (L::kCols / 2));
+                float a = 0.f, b = 0.f;
+#pragma unroll
+                for (int w = 0; w < L::kWarps; ++w) {
+                    const float2 y = *reinterpret_cast<const float2*>(&red[buf][w][h][c]);
+                    a += y.x, b += y.y;
+                }
+                *reinterpret_cast<uint32_t*>(p.out + (tok * p.num_qo_heads + kvh * p.group + h0 + h) * D + col0 + c) =
+                    dev::pack_bf16x2(a * p.scale, b * p.scale);
+            }
+        }
+    }
+    if (slots.y >= 0) {
+        float* dst = p.states + ((int64_t)slots.y * p.num_kv_heads + kvh) * per_head + row0 * D + col0 + col;
+#pragma unroll
+        for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(dst + i * D) = S[i];
+    }
+}
+
+template <int D, int P>
+cudaError_t launch_step(const LinParams& p, cudaStream_t s) {
+    return launch_programmatic(linear_step_kernel<D, P>, dim3((unsigned)(p.num_kv_heads * P), (unsigned)p.batch),
+                               (unsigned)StepShape<D, P>::kThreads, 0, s, p);
+}
+
+template <int D>
+cudaError_t launch_step_d(const LinParams& p, cudaStream_t s) {
+    const int64_t heads = (int64_t)p.batch * p.num_kv_heads;
+    if (heads >= 2 * p.sm_count) return launch_step<D, 1>(p, s);
+    return heads >= p.sm_count ? launch_step<D, 2>(p, s) : launch_step<D, 4>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_plan(const LinPlanParams& p, cudaStream_t s) {
+    linear_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_step(const LinParams& p, int head_dim, cudaStream_t s) {
+    if (p.batch <= 0) return cudaSuccess;
+    if (head_dim == 128) return launch_step_d<128>(p, s);
+    if (head_dim == 64) return launch_step_d<64>(p, s);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pva

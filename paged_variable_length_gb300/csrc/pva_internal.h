@@ -264,6 +264,11 @@ struct RopeParams {
     int32_t row_bytes;           // MXFP4: bytes of a pool row
     int32_t batch;
     int32_t sm_count;
+    int32_t norm;                // nonzero: each head of q and k over its root mean square first
+    const float* q_gain;         // [D] or null: ones
+    const float* k_gain;
+    float eps;
+    uint16_t* k_out;             // without a pool: [T, Hkv, D] contiguous, or null: q alone
 };
 
 // Host view of a prepared batch, stored inside pva_meta::opaque.
@@ -393,6 +398,8 @@ int decode_mx_heads(int num_kv_heads, int head_dim, int rows);
 cudaError_t launch_decode_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_join_mx(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_append(const ForwardParams& p, const RopeParams& rp, int head_dim, int kv_dtype, cudaStream_t s);
+cudaError_t launch_append_norm(const ForwardParams& p, const RopeParams& rp, int head_dim, int kv_dtype, cudaStream_t s);
+cudaError_t launch_norm_rope(const ForwardParams& p, const RopeParams& rp, int head_dim, cudaStream_t s);
 cudaError_t launch_load_mx(const ForwardParams& p, void* k, void* v, int head_dim, cudaStream_t s);
 cudaError_t launch_merge(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
 cudaError_t launch_prefill(const ForwardParams& p, int head_dim, int ctas, cudaStream_t s);
