@@ -28,7 +28,7 @@ struct LinItem {
     int32_t ntok;
     int32_t seg;     // index among the request's segments
     int32_t nseg;
-    int32_t base;    // nseg > 1: first of the request's nseg segment states in the workspace
+    int32_t base;    // first of the request's nseg segment states in the workspace, -1: it has none (one CTA a kv head)
     int32_t in;      // state slot that the request starts from (-1: zero)
     int32_t out;     // state slot that receives its last state (-1: none)
 };
@@ -40,10 +40,11 @@ struct LinLayout {
     size_t header;
     size_t tok_req;     // int32 [max_tokens]: request of each new token
     size_t req_state;   // int2 [max_batch]: state slots (in, out) of each request, in = -2: skipped
+    size_t req_base;    // int32 [max_batch]: of a long request whose start is copied, its LinItem::base; else -1
     size_t claim;       // int32 [num_states]: the last request that claimed a slot as its out
     size_t items;       // LinItem [max_items], most tokens first
     size_t pre_items;   // LinItem [max_segs]: the segments of the first pass
-    size_t seg_state;   // fp32 [max_segs][Hkv][D][D]: a request's entry 0: its start; s: segment s - 1's end
+    size_t seg_state;   // fp32 [max_segs][Hkv][D][D]: a request's entry 0: a copy of its start; s: segment s - 1's end
     size_t seg_decay;   // fp32 [max_segs][Hkv]: entry s: the decay over segment s - 1
     size_t total;
     int32_t max_items;
@@ -59,6 +60,7 @@ struct LinPlanParams {
     int32_t total_tokens;
     int32_t max_q_len;
     int32_t seg_tokens;        // most tokens of a segment
+    int32_t head_parts;        // CTAs that share the q heads of a kv head
     int64_t num_states;
     uint8_t* ws;
     LinLayout lay;
@@ -80,6 +82,7 @@ struct LinParams {
     int32_t num_kv_heads;
     int32_t group;
     int32_t sm_count;
+    int32_t head_parts;
     float scale;
     uint8_t* ws;
     LinLayout lay;
@@ -94,6 +97,7 @@ struct LinHost {
     int32_t max_q_len;
     int32_t sm_count;
     int32_t seg_tokens;
+    int32_t head_parts;
     const int32_t* cu;
     const int32_t* seqlens;
     uint8_t* ws;

@@ -34,8 +34,9 @@ LinLayout make_layout(const pva_linear_config* c, int sms) {
     LinLayout L{};
     L.max_items = (int32_t)(c->max_tokens / kChunk + c->max_batch + 1);
     // a segment has at least T Hkv / sms of a batch's T tokens and only requests longer than one are cut
-    // (into at most twice what their length would fill): at most 2 sms / Hkv segments in all
-    L.max_segs = 2 * sms / c->num_kv_heads + 2;
+    // (into at most twice what their length would fill): at most 2 sms / Hkv segments of those, and q heads are
+    // dealt out where all long requests' kv heads are fewer than the SMs
+    L.max_segs = 3 * sms / c->num_kv_heads + 3;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -45,6 +46,7 @@ LinLayout make_layout(const pva_linear_config* c, int sms) {
     L.header = take(sizeof(PlanHeader));
     L.tok_req = take(sizeof(int32_t) * ((size_t)c->max_tokens + 1));
     L.req_state = take(sizeof(int2) * (size_t)c->max_batch);
+    L.req_base = take(sizeof(int32_t) * (size_t)c->max_batch);
     L.claim = take(sizeof(int32_t) * (size_t)c->num_states);
     L.items = take(sizeof(LinItem) * (size_t)L.max_items);
     L.pre_items = take(sizeof(LinItem) * (size_t)L.max_segs);
@@ -186,6 +188,7 @@ pva_status launch_linear(const LinHost* h, const pva_linear_args* a, const void*
     p.num_kv_heads = h->cfg.num_kv_heads;
     p.group = h->cfg.num_qo_heads / h->cfg.num_kv_heads;
     p.sm_count = h->sm_count;
+    p.head_parts = h->head_parts;
     p.scale = h->cfg.scale > 0.f ? h->cfg.scale : 1.0f / std::sqrt((float)h->cfg.head_dim);
     p.ws = h->ws;
     p.lay = h->lay;
@@ -199,7 +202,7 @@ pva_status launch_linear(const LinHost* h, const pva_linear_args* a, const void*
         if (launch_linear_chunks(p, D, true, (int)(most < h->sm_count ? most : h->sm_count), s) != cudaSuccess) return PVA_ERR_CUDA;
     }
     const int64_t longs = h->total_tokens / (kStepTokens + 1) < h->batch ? h->total_tokens / (kStepTokens + 1) : h->batch;
-    const int64_t most = (longs + (h->max_q_len > h->seg_tokens ? h->lay.max_segs : 0)) * Hkv;
+    const int64_t most = (longs + (h->max_q_len > h->seg_tokens ? h->lay.max_segs : 0)) * Hkv * h->head_parts;
     return launch_linear_chunks(p, D, false, (int)(most < h->sm_count ? most : h->sm_count), s) == cudaSuccess ? PVA_OK
                                                                                                              : PVA_ERR_CUDA;
 }
@@ -266,6 +269,7 @@ pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_s
     h.max_q_len = max_q_len > 0 && max_q_len < total_tokens ? max_q_len : (total_tokens > 0 ? total_tokens : 1);
     h.sm_count = sms;
     h.seg_tokens = segment_tokens(total_tokens, cfg->num_kv_heads, h.max_q_len, sms);
+    h.head_parts = 1;
     h.cu = cu_seqlens_q;
     h.seqlens = cache_seqlens;
     h.ws = static_cast<uint8_t*>(workspace);
@@ -279,6 +283,7 @@ pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_s
     pp.total_tokens = total_tokens;
     pp.max_q_len = h.max_q_len;
     pp.seg_tokens = h.seg_tokens;
+    pp.head_parts = h.head_parts;
     pp.num_states = cfg->num_states;
     pp.ws = h.ws;
     pp.lay = h.lay;

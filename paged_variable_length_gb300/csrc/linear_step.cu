@@ -5,7 +5,8 @@
 // heads of the kv head share it.  Bound: HBM, 2 x 4 D^2 bytes a request and kv head (D = 128: 128 KiB
 // against 2 KiB of activations).  A thread keeps four columns of some rows in registers, so that a warp's
 // accesses are whole rows and every load of the state is in flight before the first is used; the columns
-// of a state may be dealt to 2 or 4 CTAs.
+// of a state may be dealt to 2 or 4 CTAs.  It also copies the starts of long requests that several CTAs of
+// the tensor-core kernel behind it work on.
 #include <cuda_runtime.h>
 
 #include "device_utils.cuh"
@@ -29,6 +30,7 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
     __shared__ uint32_t all_err;
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
     int2* req_state = reinterpret_cast<int2*>(p.ws + p.lay.req_state);
+    int32_t* req_base = reinterpret_cast<int32_t*>(p.ws + p.lay.req_base);
     int32_t* claim = reinterpret_cast<int32_t*>(p.ws + p.lay.claim);
     int32_t* tok_req = reinterpret_cast<int32_t*>(p.ws + p.lay.tok_req);
     LinItem* items = reinterpret_cast<LinItem*>(p.ws + p.lay.items);
@@ -132,14 +134,17 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
         __syncthreads();
         for (int i = tid; i < B; i += kPlanThreads) {
             int n, per;
+            req_base[i] = -1;
             if (!is_long(i, &n)) continue;
             const int nseg = cut(n, &per);
             const int at = nseg > 1 ? atomicAdd(&n_pre, nseg - 1) : 0;
             LinItem it;
             it.req = i;
             it.nseg = nseg;
-            it.base = nseg > 1 ? atomicAdd(&n_segs, nseg) : 0;
             it.in = req_state[i].x;
+            // several CTAs on one state: they start from a copy
+            it.base = nseg > 1 || (p.head_parts > 1 && it.in >= 0) ? atomicAdd(&n_segs, nseg) : -1;
+            if (it.in >= 0) req_base[i] = it.base;
             it.out = req_state[i].y;
             for (int s = 0; s < nseg; ++s) {
                 it.seg = s;
@@ -218,7 +223,9 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
     const uint32_t errors = reinterpret_cast<const PlanHeader*>(p.ws + p.lay.header)->error_bits;
     const int2 slots = reinterpret_cast<const int2*>(p.ws + p.lay.req_state)[req];
     const int c0 = p.cu[req], n = p.cu[req + 1] - c0;
-    if ((errors & kErrFatal) || n <= 0 || n > kStepTokens || slots.x == -2) return;
+    if ((errors & kErrFatal) || n <= 0 || slots.x == -2) return;
+    const int copy = n > kStepTokens ? reinterpret_cast<const int32_t*>(p.ws + p.lay.req_base)[req] : -1;
+    if (n > kStepTokens && copy < 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int col = 4 * (tid % L::kLanes), row0 = (tid / L::kLanes) * R;
 
@@ -231,6 +238,13 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
     } else {
 #pragma unroll
         for (int i = 0; i < R; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (copy >= 0) {
+        float* dst = reinterpret_cast<float*>(p.ws + p.lay.seg_state) + ((int64_t)copy * p.num_kv_heads + kvh) * per_head +
+                     row0 * D + col0 + col;
+#pragma unroll
+        for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(dst + i * D) = S[i];
+        return;
     }
     int buf = 0;
     for (int t = 0; t < n; ++t) {

@@ -1,24 +1,26 @@
 // K11: linear attention of requests with many new tokens, in chunks of 128 on the 5th-generation tensor
 // cores.  For a chunk with c_i the sum of the log decays up to token i and S the state before it:
-//   o_i = scale (e^{c_i} q_i^T S + sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j)
+//   o_i = scale e^{c_i} (q_i^T S + sum_{j <= i} (q_i . k_j) e^{-c_j} v_j)
 //   S'  = e^{c_end} S + sum_j (e^{c_end - c_j} k_j) v_j^T
-// Four products of 128 rows: Q K^T, P V and Q S for each q head, (w K)^T V once for its kv head.
+// Four products of 128 rows: Q K^T, Q S and P V for each q head, (w K)^T V once for its kv head.
 //
-// A work unit is a segment of a request and a kv head; its chunks run one after another, with the state
-// in the registers of a warpgroup (fp32, a row of S a thread) and every product's accumulator in TMEM:
-//   warps 0-3    P: a row of Q K^T a thread, times 2^(c_i - c_j) below the diagonal, to bf16 in TMEM (the
-//                A operand of P V); then the row of O: scale (e^{c_i} (Q S) + P V), to bf16 in HBM.  The two
-//                accumulators stay apart because e^{c_i} would otherwise be rounded into q or S a second time;
+// A work unit is a segment of a request, a kv head and some of its q heads; its chunks run one after
+// another, with the state in the registers of a warpgroup (fp32, a row of S a thread) and every product's
+// accumulator in TMEM (two of Q K^T, so that the next head's runs while this one's weights are made):
+//   warps 0-3    P: a row of Q K^T a thread, times e^{-c_j} up to the diagonal, to bf16 in TMEM (the A
+//                operand of P V, which adds to Q S); then the row of O, times scale e^{c_i}, to bf16 in HBM;
 //   warps 4-7    S <- e^{c_end} S + (w K)^T V, and its bf16 copy in shared memory for the next chunk's Q S;
-//   warps 8-11   w K, as three bf16 parts that together hold all 24 bits of the fp32 product (so that the
+//   warps 8-15   w K, as three bf16 parts that together hold all 24 bits of the fp32 product (so that the
 //                fp32 state keeps its own), 16 tokens at a time; also zero the rows of V behind the request's
 //                last token, and note whether V holds an infinity or a NaN;
-//   warp 12      issues the MMAs; warp 13 loads K, warp 14 V and Q (TMA, 128-byte swizzle); warp 15
+//   warp 16      issues the MMAs; warp 17 loads K, warp 18 V and Q (TMA, 128-byte swizzle); warp 19
 //                sums the decays (in 64 bits: differences of far sums keep their bits).
 // Roundings to bf16: P and the copy of S, each half a step of the term it scales; out.
 //
-// Weight 0 times an infinity or a NaN of V behind the diagonal would reach the chunk's earlier tokens, so a
-// chunk with one takes P V row by row on the CUDA cores, over the keys that each row sees.
+// e^{-c_j} is held to 2^40: in a chunk with sums beyond that ("deep") row i's weights are e^{c_i - r_i - c_j}
+// with r_i = c_i held to +-40 (log2), its part of Q S is scaled by e^{c_i - r_i} in TMEM before P V adds to it,
+// and O takes e^{r_i}.  Weight 0 times an infinity or a NaN of V behind the diagonal would reach the chunk's
+// earlier tokens, so a chunk with one takes P V row by row on the CUDA cores, over the keys that each row sees.
 //
 // States pass: only w K, V and the state update; the segments' own states and decays go to the workspace,
 // and the main pass starts a segment from those before it.
@@ -39,63 +41,77 @@
 namespace pva {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kMmaWarp = 12, kLoadK = 13, kLoadQV = 14, kDecayWarp = 15;
-// Registers a thread: launched with 128, the state's warpgroup rises to what the others give away
-// (128 + 208 + 96 + 80 = 4 x 128, so the increase never waits for registers that are not there).
-constexpr int kRegsLaunch = 128, kRegsState = 208, kRegsScale = 96, kRegsCtrl = 80;
-static_assert(kRegsLaunch + kRegsState + kRegsScale + kRegsCtrl == 4 * kRegsLaunch, "register split must balance");
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kLoadK = 17, kLoadQV = 18, kDecayWarp = 19;
+// Registers a thread: launched with 96, the state's warpgroup rises to what the others give away
+// (88 + 192 + 2 x 64 + 72 = 5 x 96, so the increase never waits for registers that are not there).
+constexpr int kRegsLaunch = 96, kRegsP = 88, kRegsState = 192, kRegsScale = 64, kRegsCtrl = 72;
+static_assert(kRegsP + kRegsState + 2 * kRegsScale + kRegsCtrl == 5 * kRegsLaunch, "register split must balance");
 constexpr int kRegion = kChunk * 128;  // 128 rows of 128 bytes (64 bf16 columns), swizzled
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColP = 0, kColQS = 128, kColPV = 256, kColState = 384;  // TMEM columns
+constexpr uint32_t kColP = 0, kColO = 256, kColState = 384;  // TMEM columns (two buffers of Q K^T)
+constexpr float kDeep = 40.f;             // largest |c_i| (log2) whose power enters the weights
 constexpr int kPart = 16;                 // tokens of a staged part of w K
 constexpr int kParts = kChunk / kPart;
 constexpr int kPartRegion = kPart * 128;  // 16 rows of 128 bytes
 
-template <int D>
+template <int D, bool STATES>
 struct SmemMap {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kRegion * kHalves;
     static constexpr int kStateRegion = D * 128;
     static constexpr int kSplit = kPartRegion * kHalves;  // one of the three bf16 parts of 16 tokens
-    static constexpr int kQ = 0;                          // two stages
-    static constexpr int kK = kQ + 2 * kTile;             // one
-    static constexpr int kV = kK + kTile;                 // two
-    static constexpr int kS = kV + 2 * kTile;             // bf16 copy of the state
-    static constexpr int kW = kS + kStateRegion * kHalves;  // two stages of w K
+    static constexpr int kStagesK = STATES ? 2 : 1;
+    static constexpr int kQ = 0;                                    // two stages
+    static constexpr int kK = kQ + (STATES ? 0 : 2 * kTile);
+    static constexpr int kV = kK + kStagesK * kTile;                // two stages
+    static constexpr int kS = kV + 2 * kTile;                       // bf16 copy of the state
+    static constexpr int kW = kS + (STATES ? 0 : kStateRegion * kHalves);  // two stages of w K
     // (D 64: the 128-row A operand of the state's product reaches one region past the part it is of;
     // what lies there ends in TMEM lanes that nobody reads)
     static constexpr int kBytes = kW + 2 * 3 * kSplit + (D == 64 ? kPartRegion : 0);
 };
 
 struct Bars {
-    uint64_t q_full[2], q_empty[2], k_full, k_empty, v_full[2], v_empty[2], v_ok[2];
-    uint64_t p_full, p_ready, o_ready, o_free;
-    uint64_t w_full[2], w_empty[2], ds_full, ds_free, s_full, s_empty;
+    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], v_ok[2];
+    uint64_t p_full[2], p_ready[2], qs_full, o_ready, o_free;
+    uint64_t w_full[4], w_empty[4], ds_full, ds_free, s_full, s_empty;
     uint64_t dec_full[2], dec_empty[2], drain;
     alignas(16) float c[2][kChunk];  // sums of the log decays up to each token of the chunk, in log2 units
-    float w[2][kChunk];  // 2^(c_end - c_j); 0 behind the last token
-    float end[2];        // 2^c_end
-    int32_t v_bad[2][4];
+    alignas(16) float f[2][kChunk];  // 2^-c_j
+    float w[2][kChunk];              // 2^(c_end - c_j); 0 behind the last token
+    float end[2];                    // 2^c_end
+    int32_t deep[2];                 // some |c_i| > kDeep
+    alignas(16) int32_t v_bad[2][8];
     uint32_t tmem_base;
     int32_t abort_flag;
     uint64_t wait_limit;
 };
 
 // Work waits: of a converged warp (voted, so that it leaves together or not at all), and of one thread.
-__device__ __forceinline__ bool give_up(Bars* b, uint32_t* err) {
-    b->abort_flag = 1;
-    dev::set_error(err, kErrTimeout);
-    return false;
-}
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* b, uint32_t* err) {
-    if (__all_sync(0xffffffffu, dev::mbar_wait(bar, parity, b->wait_limit))) return true;
-    if ((threadIdx.x & 31) == 0) give_up(b, err);
-    __syncwarp();
-    return false;
-}
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Bars* b, uint32_t* err) {
-    return dev::mbar_wait(bar, parity, b->wait_limit) || give_up(b, err);
+struct Waits {
+    Bars* b;
+    uint32_t* err;
+    uint64_t limit;
+    __device__ __forceinline__ bool give_up() const {
+        b->abort_flag = 1;
+        dev::set_error(err, kErrTimeout);
+        return false;
+    }
+    __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+        if (__all_sync(0xffffffffu, dev::mbar_wait(bar, parity, limit))) return true;
+        if ((threadIdx.x & 31) == 0) (void)give_up();
+        __syncwarp();
+        return false;
+    }
+    __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
+        return dev::mbar_wait(bar, parity, limit) || give_up();
+    }
+};
+
+// Whether a phase has completed, without waiting: for a converged warp.
+__device__ __forceinline__ bool seen_warp(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, dev::mbar_test_wait(bar, parity));
 }
 
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
@@ -109,18 +125,95 @@ __device__ __forceinline__ int unit_at(int k, int n_units) {
     const int g = gridDim.x, u = k * g + ((k & 1) ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
     return u < n_units ? u : -1;
 }
+
+// A unit's segment, kv head and q heads g0 .. g1 - 1 of that head's group.
+struct Unit {
+    LinItem it;
+    int kvh, g0, g1;
+};
+template <bool STATES>
+__device__ __forceinline__ Unit unit_of(const LinItem* items, int u, const LinParams& p) {
+    const int parts = STATES ? 1 : p.head_parts, per = p.num_kv_heads * parts;
+    Unit x;
+    x.it = items[u / per];
+    x.kvh = u % per / parts;
+    const int part = u % parts;
+    x.g0 = STATES ? 0 : p.group * part / parts;
+    x.g1 = STATES ? 0 : p.group * (part + 1) / parts;
+    return x;
+}
+__device__ __forceinline__ bool v_is_bad(const Bars* b, int st) {
+    const int4 x = *reinterpret_cast<const int4*>(&b->v_bad[st][0]), y = *reinterpret_cast<const int4*>(&b->v_bad[st][4]);
+    return (x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) != 0;
+}
 __device__ __forceinline__ int chunks_of(int ntok) { return (ntok + kChunk - 1) / kChunk; }
 
-// Whether a pair of bf16 holds an infinity or a NaN.
-__device__ __forceinline__ uint32_t odd_pair(uint32_t w) {
-    return ((w & 0x7F80u) == 0x7F80u) | ((w & 0x7F800000u) == 0x7F800000u);
+// acc + 0 x, for pairs of bf16: stays 0 unless x is an infinity or a NaN.
+__device__ __forceinline__ uint32_t note_odd(uint32_t acc, uint32_t x) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    return r;
+}
+__device__ __forceinline__ bool is_odd(uint32_t acc) { return (acc & 0x7FFF7FFFu) != 0; }
+
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// (a0, a1) * (b0, b1), one packed instruction.
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// What truncation to bf16 leaves of a pair (exact): f - (upper 16 bits of f).
+__device__ __forceinline__ void rest2(float& m0, float& m1, float f0, float f1) {
+    dev::ffma2(m0, m1, hi_f32(__float_as_uint(f0)), hi_f32(__float_as_uint(f1)), -1.f, -1.f, f0, f1);
+}
+
+// A chunk with an infinity or a NaN in V, or with deep sums: this warp's rows of O (Q S so far) times `part`,
+// plus (bad) the product of their weights with V over the keys each row sees.  Rarely called, so kept small.
+template <int D>
+__device__ __noinline__ void finish_rows(uint32_t t_o, uint32_t t_p, const uint8_t* V, int row, float part, bool bad) {
+    const int last = row | 31;  // of the warp's rows
+#pragma unroll 1
+    for (int x = 0; x < D / 32; ++x) {
+        float o[32];
+        tc::tmem_ld32_async(t_o + 32 * x, o);
+        tc::tmem_wait_ld_regs(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= part;
+#pragma unroll 1
+        for (int j = 0; bad && j <= last; ++j) {
+            const uint32_t w2 = tc::tmem_ld1(t_p + j / 2);
+            const float w = (j & 1) ? hi_f32(w2) : lo_f32(w2);
+            if (j <= row) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(V + (x >> 1) * kRegion + j * 128 +
+                                                                    ((((x & 1) * 4 + e) ^ (j & 7)) << 4));
+                    const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[8 * e + 2 * i] = fmaf(w, lo_f32(v[i]), o[8 * e + 2 * i]);
+                        o[8 * e + 2 * i + 1] = fmaf(w, hi_f32(v[i]), o[8 * e + 2 * i + 1]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        tc::tmem_st32(t_o + 32 * x, o);
+    }
+    tc::tmem_wait_st();
 }
 
 template <int D, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const LinParams p, const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using L = SmemMap<D>;
+    using L = SmemMap<D, STATES>;
+    constexpr uint32_t KS = L::kStagesK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Bars bars;
@@ -130,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::grid_dep_launch();
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
     uint32_t* err = &hdr->error_bits;
-    const int Hkv = p.num_kv_heads, G = STATES ? 0 : p.group;
-    const int n_units = (STATES ? hdr->n_casc_tiles : hdr->n_pre_tiles) * Hkv;
+    const int Hkv = p.num_kv_heads;
+    const int n_units = STATES ? hdr->n_casc_tiles * Hkv : hdr->n_pre_tiles * Hkv * p.head_parts;
     if ((hdr->error_bits & kErrFatal) || (int)blockIdx.x >= n_units) return;
     const LinItem* items = reinterpret_cast<const LinItem*>(p.ws + (STATES ? p.lay.pre_items : p.lay.items));
     float* seg_state = reinterpret_cast<float*>(p.ws + p.lay.seg_state);
@@ -142,18 +235,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 2; ++s) {
             dev::mbar_init(&b->q_full[s], 1);
             dev::mbar_init(&b->q_empty[s], 1);
+            dev::mbar_init(&b->k_full[s], 1);
+            dev::mbar_init(&b->k_empty[s], 9);
             dev::mbar_init(&b->v_full[s], 1);
             dev::mbar_init(&b->v_empty[s], 1);
-            dev::mbar_init(&b->v_ok[s], 4);
-            dev::mbar_init(&b->w_full[s], 4);
-            dev::mbar_init(&b->w_empty[s], 1);
+            dev::mbar_init(&b->v_ok[s], 8);
+            dev::mbar_init(&b->p_full[s], 1);
+            dev::mbar_init(&b->p_ready[s], 4);
             dev::mbar_init(&b->dec_full[s], 1);
-            dev::mbar_init(&b->dec_empty[s], STATES ? 8 : 12);
+            dev::mbar_init(&b->dec_empty[s], STATES ? 12 : 16);
         }
-        dev::mbar_init(&b->k_full, 1);
-        dev::mbar_init(&b->k_empty, 5);
-        dev::mbar_init(&b->p_full, 1);
-        dev::mbar_init(&b->p_ready, 4);
+        for (int s = 0; s < 4; ++s) {
+            dev::mbar_init(&b->w_full[s], 2);
+            dev::mbar_init(&b->w_empty[s], 1);
+        }
+        dev::mbar_init(&b->qs_full, 1);
         dev::mbar_init(&b->o_ready, 1);
         dev::mbar_init(&b->o_free, 4);
         dev::mbar_init(&b->ds_full, 1);
@@ -173,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = b->tmem_base;
+    const Waits wait{b, err, b->wait_limit};
 
-    if (warp >= 12) {
+    if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
         if (warp == kMmaWarp) {
             // ========================================================== MMA issuer (the whole warp, one lane elected)
@@ -186,74 +283,110 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kV), kRegion);
             const uint32_t s_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kS), L::kStateRegion);
             const uint32_t w_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kW), kPartRegion);
-            auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, b, err); };
             uint32_t n = 0, h = 0;  // chunks and q heads so far
             // the state's product of chunk n: 16 tokens at a time, three parts of w K each
             auto state_product = [&]() -> bool {
                 const int st = n & 1;
-                if (!wait(&b->v_ok[st], (n >> 1) & 1) || (n > 0 && !wait(&b->ds_free, (n - 1) & 1))) return false;
+                if (!wait.warp(&b->v_ok[st], (n >> 1) & 1) || (n > 0 && !wait.warp(&b->ds_free, (n - 1) & 1))) return false;
                 for (int s = 0; s < kParts; ++s) {
                     const uint32_t i = n * kParts + s;
-                    if (!wait(&b->w_full[i & 1], (i >> 1) & 1)) return false;
+                    if (!wait.warp(&b->w_full[i & 3], (i >> 2) & 1)) return false;
                     tc::fence_after_sync();
                     const uint32_t b0 = v_lo + ((st * L::kTile + s * kPartRegion) >> 4);
 #pragma unroll
                     for (int x = 0; x < 3; ++x)
                         tc::mma_ss_warp(tmem + kColState, w_lo + (((i & 1) * 3 + x) * L::kSplit >> 4), b0, kDescHi, id_kv,
                                         s > 0 || x > 0 ? 1u : 0u);
-                    tc::mma_commit_warp(&b->w_empty[i & 1]);
+                    tc::mma_commit_warp(&b->w_empty[i & 3]);
                 }
                 tc::mma_commit_warp(&b->ds_full);
                 return true;
             };
             bool ok = true;
-            for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const int nch = chunks_of(items[u / Hkv].ntok);
-                for (int c = 0; ok && c < nch; ++c, ++n) {
-                    const int st = n & 1;
-                    if constexpr (STATES) {
+            if constexpr (STATES) {
+                for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
+                    const int nch = chunks_of(unit_of<STATES>(items, u, p).it.ntok);
+                    for (int c = 0; ok && c < nch; ++c, ++n) {
                         ok = state_product();
-                        tc::mma_commit_warp(&b->k_empty);
-                        tc::mma_commit_warp(&b->v_empty[st]);
-                        continue;
+                        tc::mma_commit_warp(&b->k_empty[n % KS]);
+                        tc::mma_commit_warp(&b->v_empty[n & 1]);
                     }
-                    if (!(ok = wait(&b->k_full, n & 1))) break;
-                    for (int g = 0; g < G; ++g, ++h) {
-                        const int qs = h & 1;
-                        if (!(ok = wait(&b->q_full[qs], (h >> 1) & 1))) break;
-                        tc::fence_after_sync();
-                        const uint32_t q0 = q_lo + (qs * L::kTile >> 4);
-                        // Q K^T (the P of the head before was read by its P V, issued before this)
+                }
+            } else {
+                // Q K^T runs one head ahead: its own place in the sequence of heads
+                int qk = 0, q_left = 0, q_heads = 0, qg = 0;  // unit, chunks left of it, its heads, head
+                uint32_t qn = 0, qh = 0;
+                bool more = true;
+                auto next_unit = [&] {
+                    const int u = unit_at(qk++, n_units);
+                    more = u >= 0;
+                    if (more) {
+                        const Unit x = unit_of<STATES>(items, u, p);
+                        q_left = chunks_of(x.it.ntok);
+                        q_heads = x.g1 - x.g0;
+                    }
+                };
+                next_unit();
+                auto inputs_seen = [&] {
+                    return seen_warp(&b->q_full[qh & 1], (qh >> 1) & 1) && (qg > 0 || seen_warp(&b->k_full[0], qn & 1));
+                };
+                // (the weights that lay in this buffer were read by the P V of two heads before, issued already)
+                auto issue_qk = [&]() -> bool {
+                    if ((qg == 0 && !wait.warp(&b->k_full[0], qn & 1)) || !wait.warp(&b->q_full[qh & 1], (qh >> 1) & 1)) return false;
+                    tc::fence_after_sync();
+                    const uint32_t q0 = q_lo + ((qh & 1) * L::kTile >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (uint32_t)((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
-                            tc::mma_ss_warp(tmem + kColP, q0 + off, k_lo + off, kDescHi, id_qk, kk > 0 ? 1u : 0u);
-                        }
-                        tc::mma_commit_warp(&b->p_full);
-                        if (g == G - 1) tc::mma_commit_warp(&b->k_empty);
-                        if (g == 0 && !(ok = state_product() && wait(&b->s_full, n & 1))) break;
-                        if (h > 0 && !(ok = wait(&b->o_free, (h - 1) & 1))) break;
-                        tc::fence_after_sync();
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (uint32_t)((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
+                        tc::mma_ss_warp(tmem + kColP + 128 * (qh & 1), q0 + off, k_lo + off, kDescHi, id_qk, kk > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit_warp(&b->p_full[qh & 1]);
+                    ++qh;
+                    if (++qg == q_heads) {
+                        tc::mma_commit_warp(&b->k_empty[0]);
+                        qg = 0;
+                        ++qn;
+                        if (--q_left == 0) next_unit();
+                    }
+                    return true;
+                };
+                ok = issue_qk();
+                for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
+                    const Unit x = unit_of<STATES>(items, u, p);
+                    const int nch = chunks_of(x.it.ntok), G = x.g1 - x.g0;
+                    for (int c = 0; ok && c < nch; ++c, ++n) {
+                        const int st = n & 1;
+                        for (int g = 0; g < G; ++g, ++h) {
+                            if (g == 0 && !(ok = state_product() && wait.warp(&b->s_full, n & 1))) break;
+                            if (h > 0 && !(ok = wait.warp(&b->o_free, (h - 1) & 1))) break;
+                            tc::fence_after_sync();
+                            const uint32_t q0 = q_lo + ((h & 1) * L::kTile >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (uint32_t)((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
-                            tc::mma_ss_warp(tmem + kColQS, q0 + off, s_lo + (kk * 2048 >> 4), kDescHi, id_v, kk > 0 ? 1u : 0u);
-                        }
-                        if (!(ok = wait(&b->p_ready, h & 1))) break;
-                        tc::fence_after_sync();
-                        const bool bad = (b->v_bad[st][0] | b->v_bad[st][1] | b->v_bad[st][2] | b->v_bad[st][3]) != 0;
-                        if (!bad) {
-                            const uint32_t b0 = v_lo + (st * L::kTile >> 4);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = (uint32_t)((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
+                                tc::mma_ss_warp(tmem + kColO, q0 + off, s_lo + (kk * 2048 >> 4), kDescHi, id_v, kk > 0 ? 1u : 0u);
+                            }
+                            tc::mma_commit_warp(&b->qs_full);
+                            // the next head's scores now if their operands are there, else behind P V
+                            const bool early = more && inputs_seen();
+                            if (early && !(ok = issue_qk())) break;
+                            if (!(ok = wait.warp(&b->p_ready[h & 1], (h >> 1) & 1))) break;
+                            tc::fence_after_sync();
+                            const bool bad = v_is_bad(b, st);
+                            if (!bad) {
+                                const uint32_t b0 = v_lo + (st * L::kTile >> 4);
 #pragma unroll
-                            for (int kk = 0; kk < kChunk / 16; ++kk)
-                                tc::mma_ts_warp(tmem + kColPV, tmem + kColP + kk * 8, b0 + (kk * 2048 >> 4), kDescHi, id_v,
-                                                kk > 0 ? 1u : 0u);
-                        }
-                        tc::mma_commit_warp(&b->o_ready);
-                        tc::mma_commit_warp(&b->q_empty[qs]);
-                        if (g == G - 1) {
-                            tc::mma_commit_warp(&b->v_empty[st]);
-                            tc::mma_commit_warp(&b->s_empty);
+                                for (int kk = 0; kk < kChunk / 16; ++kk)
+                                    tc::mma_ts_warp(tmem + kColO, tmem + kColP + 128 * (h & 1) + kk * 8, b0 + (kk * 2048 >> 4),
+                                                    kDescHi, id_v, 1u);
+                            }
+                            tc::mma_commit_warp(&b->o_ready);
+                            tc::mma_commit_warp(&b->q_empty[h & 1]);
+                            if (g == G - 1) {
+                                tc::mma_commit_warp(&b->v_empty[st]);
+                                tc::mma_commit_warp(&b->s_empty);
+                            }
+                            if (!early && more && !(ok = issue_qk())) break;
                         }
                     }
                 }
@@ -266,47 +399,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t n = 0;
             bool ok = true;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const LinItem it = items[u / Hkv];
-                const int kvh = u % Hkv;
-                for (int c = 0; c < chunks_of(it.ntok); ++c, ++n) {
-                    if (!(ok = wait_one(&b->k_empty, (n & 1) ^ 1, b, err)) || b->abort_flag) {
+                const Unit x = unit_of<STATES>(items, u, p);
+                for (int c = 0; c < chunks_of(x.it.ntok); ++c, ++n) {
+                    if (!(ok = wait.one(&b->k_empty[n % KS], ((n / KS) & 1) ^ 1)) || b->abort_flag) {
                         ok = false;
                         break;
                     }
-                    dev::mbar_arrive_expect_tx(&b->k_full, L::kTile);
+                    dev::mbar_arrive_expect_tx(&b->k_full[n % KS], L::kTile);
 #pragma unroll
-                    for (int x = 0; x < L::kHalves; ++x)
-                        tc::tma_load_3d(smem + L::kK + x * kRegion, &k_map, 64 * x, kvh, it.tok0 + c * kChunk, &b->k_full);
+                    for (int i = 0; i < L::kHalves; ++i)
+                        tc::tma_load_3d(smem + L::kK + (n % KS) * L::kTile + i * kRegion, &k_map, 64 * i, x.kvh,
+                                        x.it.tok0 + c * kChunk, &b->k_full[n % KS]);
                 }
             }
-            if (n > 0) (void)dev::mbar_wait(&b->k_full, (n - 1) & 1);  // its copies land before the CTA leaves
+            for (uint32_t s = 0; s < KS; ++s)  // its copies land before the CTA leaves
+                if (n > s) (void)dev::mbar_wait(&b->k_full[(n - 1 - s) % KS], ((n - 1 - s) / KS) & 1);
         } else if (warp == kLoadQV && lane == 0) {
             uint32_t n = 0, h = 0;
             bool ok = true;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const LinItem it = items[u / Hkv];
-                const int kvh = u % Hkv;
-                for (int c = 0; ok && c < chunks_of(it.ntok); ++c) {
-                    if (!(ok = wait_one(&b->v_empty[n & 1], ((n >> 1) & 1) ^ 1, b, err)) || b->abort_flag) {
+                const Unit x = unit_of<STATES>(items, u, p);
+                for (int c = 0; ok && c < chunks_of(x.it.ntok); ++c) {
+                    if (!(ok = wait.one(&b->v_empty[n & 1], ((n >> 1) & 1) ^ 1)) || b->abort_flag) {
                         ok = false;
                         break;
                     }
                     dev::mbar_arrive_expect_tx(&b->v_full[n & 1], L::kTile);
 #pragma unroll
-                    for (int x = 0; x < L::kHalves; ++x)
-                        tc::tma_load_3d(smem + L::kV + (n & 1) * L::kTile + x * kRegion, &v_map, 64 * x, kvh,
-                                        it.tok0 + c * kChunk, &b->v_full[n & 1]);
+                    for (int i = 0; i < L::kHalves; ++i)
+                        tc::tma_load_3d(smem + L::kV + (n & 1) * L::kTile + i * kRegion, &v_map, 64 * i, x.kvh,
+                                        x.it.tok0 + c * kChunk, &b->v_full[n & 1]);
                     ++n;
-                    for (int g = 0; g < G; ++g, ++h) {
-                        if (!(ok = wait_one(&b->q_empty[h & 1], ((h >> 1) & 1) ^ 1, b, err)) || b->abort_flag) {
+                    for (int g = x.g0; g < x.g1; ++g, ++h) {
+                        if (!(ok = wait.one(&b->q_empty[h & 1], ((h >> 1) & 1) ^ 1)) || b->abort_flag) {
                             ok = false;
                             break;
                         }
                         dev::mbar_arrive_expect_tx(&b->q_full[h & 1], L::kTile);
 #pragma unroll
-                        for (int x = 0; x < L::kHalves; ++x)
-                            tc::tma_load_3d(smem + L::kQ + (h & 1) * L::kTile + x * kRegion, &q_map, 64 * x, kvh * G + g,
-                                            it.tok0 + c * kChunk, &b->q_full[h & 1]);
+                        for (int i = 0; i < L::kHalves; ++i)
+                            tc::tma_load_3d(smem + L::kQ + (h & 1) * L::kTile + i * kRegion, &q_map, 64 * i,
+                                            x.kvh * p.group + g, x.it.tok0 + c * kChunk, &b->q_full[h & 1]);
                     }
                 }
             }
@@ -319,117 +452,156 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t n = 0;
             bool ok = true;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const LinItem it = items[u / Hkv];
-                const int kvh = u % Hkv, nch = chunks_of(it.ntok);
+                const Unit x = unit_of<STATES>(items, u, p);
+                const int nch = chunks_of(x.it.ntok);
                 double total = 0.0;  // of the unit
-                for (int c = 0; ok && c < nch; ++c, ++n) {
-                    double sum[4], x = 0.0;
+                float g4[4];
+                auto load = [&](int c) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int t = c * kChunk + 4 * lane + i;
-                        if (t < it.ntok) {
-                            const float g = p.log_decay[(p.ld_decay ? (int64_t)(it.tok0 + t) * p.ld_decay : 0) + kvh];
-                            x += (double)(g < kLeastLogDecay ? kLeastLogDecay : g) * 1.4426950408889634074;
-                        }
-                        sum[i] = x;
+                        g4[i] = t < x.it.ntok ? p.log_decay[(p.ld_decay ? (int64_t)(x.it.tok0 + t) * p.ld_decay : 0) + x.kvh] : 0.f;
                     }
+                };
+                load(0);
+                for (int c = 0; ok && c < nch; ++c, ++n) {
+                    double sum[4], y = 0.0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y += (double)(g4[i] < kLeastLogDecay ? kLeastLogDecay : g4[i]) * 1.4426950408889634074;
+                        sum[i] = y;
+                    }
+                    if (c + 1 < nch) load(c + 1);
 #pragma unroll
                     for (int d = 1; d < 32; d *= 2) {
-                        const double y = __shfl_up_sync(0xffffffffu, x, d);
-                        if (lane >= d) x += y;
+                        const double z = __shfl_up_sync(0xffffffffu, y, d);
+                        if (lane >= d) y += z;
                     }
-                    const double before = x - sum[3], end = __shfl_sync(0xffffffffu, x, 31);
+                    const double up = __shfl_up_sync(0xffffffffu, y, 1), before = lane > 0 ? up : 0.0;
+                    const double end = __shfl_sync(0xffffffffu, y, 31);
                     const int st = n & 1;
-                    if (!(ok = wait_warp(&b->dec_empty[st], ((n >> 1) & 1) ^ 1, b, err))) break;
+                    if (!(ok = wait.warp(&b->dec_empty[st], ((n >> 1) & 1) ^ 1))) break;
+                    bool deep = false;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const double ci = before + sum[i];
-                        b->c[st][4 * lane + i] = (float)ci;
-                        b->w[st][4 * lane + i] = c * kChunk + 4 * lane + i < it.ntok ? exp2f((float)(end - ci)) : 0.f;
+                        const float cf = (float)ci;
+                        b->c[st][4 * lane + i] = cf;
+                        b->f[st][4 * lane + i] = exp2f(-cf);
+                        b->w[st][4 * lane + i] = c * kChunk + 4 * lane + i < x.it.ntok ? exp2f((float)(end - ci)) : 0.f;
+                        deep |= !(fabsf(cf) <= kDeep);
                     }
-                    if (lane == 0) b->end[st] = exp2f((float)end);
+                    deep = __any_sync(0xffffffffu, deep);
+                    if (lane == 0) {
+                        b->end[st] = exp2f((float)end);
+                        b->deep[st] = deep;
+                    }
                     arrive_warp(&b->dec_full[st]);
                     total += end;
                 }
-                if (STATES && ok && lane == 0) seg_decay[(int64_t)(it.base + it.seg + 1) * Hkv + kvh] = exp2f((float)total);
+                if (STATES && ok && lane == 0)
+                    seg_decay[(int64_t)(x.it.base + x.it.seg + 1) * Hkv + x.kvh] = exp2f((float)total);
             }
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScale));
         // ============================================================== w K in three bf16 parts; a look at V
-        const int tid = threadIdx.x - 256, wq = warp - 8;
-        const int r = tid >> 3, cc = tid & 7;  // token of a part, 16-byte chunk of its row
+        // Two warps make a part of 16 tokens: pair i (of four) the parts i and i + 4.
+        const int wq = warp - 8, pair = wq >> 1;
+        const int r0 = (wq & 1) * 8 + (lane >> 3), cc = lane & 7;  // first token of a part's, 16-byte chunk of its row
         uint32_t n = 0;
         bool ok = true;
         for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-            const int ntok = items[u / Hkv].ntok;
+            const int ntok = unit_of<STATES>(items, u, p).it.ntok;
             for (int c = 0; ok && c < chunks_of(ntok); ++c, ++n) {
                 const int st = n & 1, nval = min(kChunk, ntok - c * kChunk);
                 uint8_t* V = smem + L::kV + st * L::kTile;
-                if (!(ok = wait_warp(&b->v_full[st], (n >> 1) & 1, b, err))) break;
-                {   // row tid of V
-                    uint32_t odd = 0;
+                if (!(ok = wait.warp(&b->v_full[st], (n >> 1) & 1))) break;
+                {   // half a row of V a lane (D 64: a quarter of one in either half)
+                    const int row = wq * 16 + (lane >> 1);
+                    constexpr int kEach = D / 16;
+                    uint4* at[kEach];
 #pragma unroll
-                    for (int x = 0; x < D / 8; ++x) {
-                        uint4* at = reinterpret_cast<uint4*>(V + (x >> 3) * kRegion + tid * 128 + (((x ^ tid) & 7) << 4));
-                        if (tid < nval) {
-                            const uint4 y = *at;
-                            odd |= odd_pair(y.x) | odd_pair(y.y) | odd_pair(y.z) | odd_pair(y.w);
-                        } else {
-                            *at = make_uint4(0, 0, 0, 0);
-                        }
+                    for (int x = 0; x < kEach; ++x) {
+                        const int ch = (lane & 1) * kEach + x;
+                        at[x] = reinterpret_cast<uint4*>(V + (ch >> 3) * kRegion + row * 128 + (((ch ^ row) & 7) << 4));
                     }
-                    const int any = __any_sync(0xffffffffu, odd != 0);
+                    uint32_t odd = 0;
+                    if (row < nval) {
+                        uint4 y[kEach];
+#pragma unroll
+                        for (int x = 0; x < kEach; ++x) y[x] = *at[x];
+#pragma unroll
+                        for (int x = 0; x < kEach; ++x)
+                            odd = note_odd(note_odd(note_odd(note_odd(odd, y[x].x), y[x].y), y[x].z), y[x].w);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < kEach; ++x) *at[x] = make_uint4(0, 0, 0, 0);
+                    }
+                    const int any = __any_sync(0xffffffffu, is_odd(odd));
                     if (lane == 0) b->v_bad[st][wq] = any;
                     if (nval < kChunk) tc::fence_proxy_async_smem();
                     arrive_warp(&b->v_ok[st]);
                 }
-                if (!(ok = wait_warp(&b->k_full, n & 1, b, err) && wait_warp(&b->dec_full[st], (n >> 1) & 1, b, err))) break;
-                const uint8_t* K = smem + L::kK;
-                for (int s = 0; s < kParts; ++s) {
+                if (!(ok = wait.warp(&b->k_full[n % KS], (n / KS) & 1) && wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
+                const uint8_t* K = smem + L::kK + (n % KS) * L::kTile;
+#pragma unroll 1
+                for (int s = pair; s < kParts; s += 4) {
                     const uint32_t i = n * kParts + s;
-                    const int row = s * kPart + r;
-                    const float w = b->w[st][row];
-                    uint4 part[L::kHalves][3];
+                    uint4 y[2][L::kHalves];
+                    float w[2];
+                    uint32_t odd = 0;
 #pragma unroll
-                    for (int x = 0; x < L::kHalves; ++x) {
-                        const uint4 y = *reinterpret_cast<const uint4*>(K + x * kRegion + row * 128 + (((cc ^ row) & 7) << 4));
-                        const uint32_t e[4] = {y.x, y.y, y.z, y.w};
-                        uint32_t hi[4], mid[4], lo[4];
+                    for (int z = 0; z < 2; ++z) {
+                        const int row = s * kPart + r0 + 4 * z;
+                        w[z] = b->w[st][row];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float f[2] = {__uint_as_float(e[q] << 16) * w, __uint_as_float(e[q] & 0xFFFF0000u) * w};
-                            float m[2], l[2];
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                if (row >= nval) f[z] = 0.f;  // (whatever lies there times 0)
-                                // the upper 8 bits, the next 8 and the rest: each difference is exact; an
-                                // infinity keeps nothing behind its first part
-                                const float top = __uint_as_float(__float_as_uint(f[z]) & 0xFFFF0000u);
-                                m[z] = fabsf(f[z]) == INFINITY ? 0.f : f[z] - top;
-                                l[z] = m[z] - __uint_as_float(__float_as_uint(m[z]) & 0xFFFF0000u);
-                            }
-                            hi[q] = dev::prmt(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x7632);
-                            mid[q] = dev::prmt(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x7632);
-                            lo[q] = dev::pack_bf16x2(l[0], l[1]);
+                        for (int x = 0; x < L::kHalves; ++x) {
+                            y[z][x] = *reinterpret_cast<const uint4*>(K + x * kRegion + row * 128 + (((cc ^ row) & 7) << 4));
+                            if (row >= nval) y[z][x] = make_uint4(0, 0, 0, 0);  // (whatever lies there times 0)
+                            odd = note_odd(note_odd(note_odd(note_odd(odd, y[z][x].x), y[z][x].y), y[z][x].z), y[z][x].w);
                         }
-                        part[x][0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        part[x][1] = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                        part[x][2] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    if (!(ok = wait_warp(&b->w_empty[i & 1], ((i >> 1) & 1) ^ 1, b, err))) break;
-                    uint8_t* W = smem + L::kW + (i & 1) * 3 * L::kSplit;
+                    uint8_t* W = smem + L::kW + (s & 1) * 3 * L::kSplit;
+                    // an infinity keeps nothing behind its first part (its rest would be a NaN)
+                    const bool plain = !__any_sync(0xffffffffu, is_odd(odd));
 #pragma unroll
-                    for (int x = 0; x < L::kHalves; ++x)
+                    for (int z = 0; z < 2; ++z) {
 #pragma unroll
-                        for (int q = 0; q < 3; ++q)
-                            *reinterpret_cast<uint4*>(W + q * L::kSplit + x * kPartRegion + r * 128 + (((cc ^ r) & 7) << 4)) =
-                                part[x][q];
+                        for (int x = 0; x < L::kHalves; ++x) {
+                            const uint32_t e[4] = {y[z][x].x, y[z][x].y, y[z][x].z, y[z][x].w};
+                            uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                // the upper 8 bits, the next 8 and the rest: each difference is exact
+                                float f0, f1, m0, m1, l0, l1;
+                                fmul2(f0, f1, lo_f32(e[q]), hi_f32(e[q]), w[z], w[z]);
+                                rest2(m0, m1, f0, f1);
+                                if (!plain) {
+                                    if (fabsf(f0) == INFINITY) m0 = 0.f;
+                                    if (fabsf(f1) == INFINITY) m1 = 0.f;
+                                }
+                                rest2(l0, l1, m0, m1);
+                                hi[q] = dev::prmt(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
+                                mid[q] = dev::prmt(__float_as_uint(m0), __float_as_uint(m1), 0x7632);
+                                lo[q] = dev::pack_bf16x2(l0, l1);
+                            }
+                            // (its buffer held part i - 2, whose barriers are two pairs on)
+                            if (z == 0 && x == 0 && i >= 2 && !(ok = wait.warp(&b->w_empty[(i - 2) & 3], ((i - 2) >> 2) & 1))) break;
+                            const int r = r0 + 4 * z;
+                            uint8_t* at = W + x * kPartRegion + r * 128 + (((cc ^ r) & 7) << 4);
+                            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(at + L::kSplit) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                            *reinterpret_cast<uint4*>(at + 2 * L::kSplit) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
+                        if (!ok) break;
+                    }
+                    if (!ok) break;
                     tc::fence_proxy_async_smem();
-                    arrive_warp(&b->w_full[i & 1]);
+                    arrive_warp(&b->w_full[s & 3]);
                 }
                 if (!ok) break;
-                arrive_warp(&b->k_empty);
+                arrive_warp(&b->k_empty[n % KS]);
                 arrive_warp(&b->dec_empty[st]);
             }
         }
@@ -443,12 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         const int64_t per_head = (int64_t)D * D;
         for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-            const LinItem it = items[u / Hkv];
-            const int kvh = u % Hkv, nch = chunks_of(it.ntok);
+            const Unit un = unit_of<STATES>(items, u, p);
+            const LinItem& it = un.it;
+            const int nch = chunks_of(it.ntok);
             float S[D / 32][32];
 #pragma unroll
             for (int x = 0; x < D; ++x) S[x >> 5][x & 31] = 0.f;
-            auto segment_state = [&](int i) { return seg_state + ((int64_t)(it.base + i) * Hkv + kvh) * per_head + row * D; };
+            auto slot = [&](int i) { return p.states + ((int64_t)i * Hkv + un.kvh) * per_head + row * D; };
+            auto segment_state = [&](int i) { return seg_state + ((int64_t)(it.base + i) * Hkv + un.kvh) * per_head + row * D; };
             auto add = [&](const float* src, float f) {  // S <- f S + src
 #pragma unroll
                 for (int x = 0; x < D; x += 4) {
@@ -465,25 +639,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<float4*>(dst + x) = make_float4(S[x >> 5][x & 31], S[x >> 5][(x & 31) + 1],
                                                                       S[x >> 5][(x & 31) + 2], S[x >> 5][(x & 31) + 3]);
             };
-            // The start.  Of a request in segments the states pass leaves a copy of the first one's start (in
-            // the main pass the last segment may write the slot before the first has read it), and the end of
-            // the first segment from there, of the others from zero.
+            // The start.  Where other CTAs work on the same request and kv head it is a copy that the kernel before
+            // has made: the one that ends with the request's last token may write the slot before the others have
+            // read it.  The states pass leaves the first segment's end from there, the others' from zero.
             if (live) {
                 if (it.seg == 0) {
-                    if (it.in >= 0)
-                        add(STATES || it.nseg == 1 ? p.states + ((int64_t)it.in * Hkv + kvh) * per_head + row * D
-                                                   : segment_state(0), 0.f);
-                    if (STATES) put(segment_state(0));
+                    if (it.in >= 0) add(it.base >= 0 ? segment_state(0) : slot(it.in), 0.f);
                 } else if (!STATES) {
                     add(segment_state(1), 0.f);
 #pragma unroll 1
-                    for (int i = 2; i <= it.seg; ++i) add(segment_state(i), seg_decay[(int64_t)(it.base + i) * Hkv + kvh]);
+                    for (int i = 2; i <= it.seg; ++i) add(segment_state(i), seg_decay[(int64_t)(it.base + i) * Hkv + un.kvh]);
                 }
             }
             for (int c = 0; ok && c < nch; ++c, ++n) {
                 const int st = n & 1;
                 if constexpr (!STATES) {
-                    if (n > 0 && !(ok = wait_warp(&b->s_empty, (n - 1) & 1, b, err))) break;
+                    if (n > 0 && !(ok = wait.warp(&b->s_empty, (n - 1) & 1))) break;
                     if (live) {
 #pragma unroll
                         for (int x = 0; x < D; x += 8) {
@@ -497,62 +668,116 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::fence_proxy_async_smem();
                     arrive_warp(&b->s_full);
                 }
-                if (!(ok = wait_warp(&b->dec_full[st], (n >> 1) & 1, b, err))) break;
+                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
                 const float end = b->end[st];
                 arrive_warp(&b->dec_empty[st]);
-                if (!(ok = wait_warp(&b->ds_full, n & 1, b, err))) break;
+                if (!(ok = wait.warp(&b->ds_full, n & 1))) break;
                 tc::fence_after_sync();
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    float d[32];
-                    tc::tmem_ld32_async(t_ds + 32 * x, d);
-                    tc::tmem_wait_ld_regs(d);
+                for (int x = 0; x < D / 16; ++x) {
+                    float d[16];
+                    tc::tmem_ld16_async(t_ds + 16 * x, d);
+                    tc::tmem_wait_ld16_regs(d);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) S[x][i] = fmaf(end, S[x][i], d[i]);
+                    for (int i = 0; i < 16; i += 2) {
+                        float &s0 = S[x >> 1][(x & 1) * 16 + i], &s1 = S[x >> 1][(x & 1) * 16 + i + 1];
+                        dev::ffma2(s0, s1, end, end, s0, s1, d[i], d[i + 1]);
+                    }
                 }
                 tc::fence_before_sync();
                 arrive_warp(&b->ds_free);
             }
             if (ok && live) {
                 if (STATES) put(segment_state(it.seg + 1));
-                else if (it.out >= 0 && it.seg == it.nseg - 1) put(p.states + ((int64_t)it.out * Hkv + kvh) * per_head + row * D);
+                else if (it.out >= 0 && it.seg == it.nseg - 1 && un.g0 == 0) put(slot(it.out));
             }
         }
-    } else if constexpr (!STATES) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsP));  // (in the states pass too: the split counts on it)
+        if constexpr (!STATES) {
         // ============================================================== P and O, a row a thread
         const int row = threadIdx.x;
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const uint32_t t_p = tmem + kColP + lane_base, t_qs = tmem + kColQS + lane_base, t_pv = tmem + kColPV + lane_base;
+        const uint32_t t_o = tmem + kColO + lane_base;
         uint32_t n = 0, h = 0;
         bool ok = true;
+        // the head whose O is still to be written: where to (null: none of this row), and its factor
+        bool pending = false;
+        uint16_t* o_dst = nullptr;
+        float o_factor = 0.f;
+        auto write_o = [&]() -> bool {  // of head h - 1
+            if (!wait.warp(&b->o_ready, (h - 1) & 1)) return false;
+            tc::fence_after_sync();
+            float o[2][32];
+            tc::tmem_ld32_async(t_o, o[0]);
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                tc::tmem_wait_ld_regs(o[x & 1]);
+                if (x + 1 < D / 32) {
+                    tc::tmem_ld32_async(t_o + 32 * (x + 1), o[(x + 1) & 1]);
+                } else {
+                    tc::fence_before_sync();
+                    arrive_warp(&b->o_free);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float y0, y1;
+                        fmul2(y0, y1, o[x & 1][8 * e + 2 * i], o[x & 1][8 * e + 2 * i + 1], o_factor, o_factor);
+                        w[i] = dev::pack_bf16x2(y0, y1);
+                    }
+                    if (o_dst != nullptr) reinterpret_cast<uint4*>(o_dst)[4 * x + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            __syncwarp();
+            return true;
+        };
         for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-            const LinItem it = items[u / Hkv];
-            const int kvh = u % Hkv;
+            const Unit un = unit_of<STATES>(items, u, p);
+            const LinItem& it = un.it;
             for (int c = 0; ok && c < chunks_of(it.ntok); ++c, ++n) {
                 const int st = n & 1, nval = min(kChunk, it.ntok - c * kChunk);
-                if (!(ok = wait_warp(&b->dec_full[st], (n >> 1) & 1, b, err) && wait_warp(&b->v_ok[st], (n >> 1) & 1, b, err)))
+                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1) && wait.warp(&b->v_ok[st], (n >> 1) & 1)))
                     break;
-                const bool bad = (b->v_bad[st][0] | b->v_bad[st][1] | b->v_bad[st][2] | b->v_bad[st][3]) != 0;
-                const float ci = b->c[st][row], ei = dev::fast_exp2(ci) * p.scale;
-                for (int g = 0; g < G; ++g, ++h) {
-                    if (!(ok = wait_warp(&b->p_full, h & 1, b, err))) break;
+                const bool bad = v_is_bad(b, st);
+                const bool deep = b->deep[st] != 0;
+                const float ci = b->c[st][row], ri = fminf(fmaxf(ci, -kDeep), kDeep);
+                for (int g = un.g0; g < un.g1; ++g, ++h) {
+                    const uint32_t t_p = tmem + kColP + 128 * (h & 1) + lane_base;
+                    // the head before's O behind this one's weights, unless these are late, or need O themselves
+                    if (pending && (deep || bad || !seen_warp(&b->p_full[h & 1], (h >> 1) & 1))) {
+                        if (!(ok = write_o())) break;
+                        pending = false;
+                    }
+                    if (!(ok = wait.warp(&b->p_full[h & 1], (h >> 1) & 1))) break;
                     tc::fence_after_sync();
                     // 32 keys at a time; those past the warp's own rows have no weight.  (The packed weights of
                     // block x lie in columns 16 x .. of the scores, which are read by then.)
-#pragma unroll
+                    const float up = ci - ri;
+                    const float* other = deep ? b->c[st] : b->f[st];
+#pragma unroll 1
                     for (int x = 0; x < kChunk / 32; ++x) {
                         uint32_t pk[16];
                         if (x <= warp) {
                             float s[32];
                             tc::tmem_ld32_async(t_p + 32 * x, s);
                             tc::tmem_wait_ld_regs(s);
+                            if (deep) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 cj = *reinterpret_cast<const float4*>(&b->c[st][32 * x + i]);
-                                s[i] *= dev::fast_exp2(ci - cj.x);
-                                s[i + 1] *= dev::fast_exp2(ci - cj.y);
-                                s[i + 2] *= dev::fast_exp2(ci - cj.z);
-                                s[i + 3] *= dev::fast_exp2(ci - cj.w);
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 cj = *reinterpret_cast<const float4*>(other + 32 * x + i);
+                                    fmul2(s[i], s[i + 1], s[i], s[i + 1], dev::fast_exp2(up - cj.x), dev::fast_exp2(up - cj.y));
+                                    fmul2(s[i + 2], s[i + 3], s[i + 2], s[i + 3], dev::fast_exp2(up - cj.z), dev::fast_exp2(up - cj.w));
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 f = *reinterpret_cast<const float4*>(other + 32 * x + i);
+                                    fmul2(s[i], s[i + 1], s[i], s[i + 1], f.x, f.y);
+                                    fmul2(s[i + 2], s[i + 3], s[i + 2], s[i + 3], f.z, f.w);
+                                }
                             }
                             if (x == warp) {  // the diagonal (whatever the hidden ones hold)
 #pragma unroll
@@ -567,78 +792,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::tmem_st16u(t_p + 16 * x, pk);
                     }
                     tc::tmem_wait_st();
-                    if (bad) {  // P V over the keys that the row sees, from the same bf16 weights
-                        const uint8_t* V = smem + L::kV + st * L::kTile;
-#pragma unroll 1
-                        for (int x = 0; x < D / 32; ++x) {
-                            float o[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-#pragma unroll 1
-                            for (int j0 = 0; j0 < kChunk; j0 += 64) {
-                                if (j0 > 32 * warp + 31) break;
-                                float pw[32];  // 64 weights
-                                tc::tmem_ld32_async(t_p + j0 / 2, pw);
-                                tc::tmem_wait_ld_regs(pw);
-#pragma unroll
-                                for (int j = 0; j < 64; ++j) {
-                                    const uint32_t w2 = __float_as_uint(pw[j >> 1]);
-                                    const float wj = __uint_as_float((j & 1) ? w2 & 0xFFFF0000u : w2 << 16);
-                                    const int vr = j0 + j;
-                                    if (vr > row) continue;
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const uint4 y = *reinterpret_cast<const uint4*>(
-                                            V + (x >> 1) * kRegion + vr * 128 + ((((x & 1) * 4 + e) ^ (vr & 7)) << 4));
-                                        const uint32_t vw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            o[8 * e + 2 * i] = fmaf(wj, __uint_as_float(vw[i] << 16), o[8 * e + 2 * i]);
-                                            o[8 * e + 2 * i + 1] =
-                                                fmaf(wj, __uint_as_float(vw[i] & 0xFFFF0000u), o[8 * e + 2 * i + 1]);
-                                        }
-                                    }
-                                }
-                            }
-                            __syncwarp();
-                            tc::tmem_st32(t_pv + 32 * x, o);
-                        }
-                        tc::tmem_wait_st();
+                    if (bad || (deep && __any_sync(0xffffffffu, up != 0.f))) {
+                        if (!(ok = wait.warp(&b->qs_full, h & 1))) break;
+                        tc::fence_after_sync();
+                        finish_rows<D>(t_o, t_p, smem + L::kV + st * L::kTile, row, dev::fast_exp2(up), bad);
                     }
                     tc::fence_before_sync();
-                    arrive_warp(&b->p_ready);
-                    // O
-                    if (!(ok = wait_warp(&b->o_ready, h & 1, b, err))) break;
-                    tc::fence_after_sync();
-                    uint16_t* dst = p.out + ((int64_t)(it.tok0 + c * kChunk + row) * p.num_qo_heads + kvh * G + g) * D;
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        float a[32], o[32];
-                        tc::tmem_ld32_async(t_qs + 32 * x, a);
-                        tc::tmem_ld32_async(t_pv + 32 * x, o);
-                        tc::tmem_wait_ld_regs(a);
-                        tc::tmem_wait_ld_regs(o);
-                        if (x == D / 32 - 1) {
-                            tc::fence_before_sync();
-                            arrive_warp(&b->o_free);
-                        }
-                        if (row < nval) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int z = 8 * e + 2 * i;
-                                    w[i] = dev::pack_bf16x2(fmaf(ei, a[z], p.scale * o[z]), fmaf(ei, a[z + 1], p.scale * o[z + 1]));
-                                }
-                                *reinterpret_cast<uint4*>(dst + 32 * x + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
-                        __syncwarp();
-                    }
+                    arrive_warp(&b->p_ready[h & 1]);
+                    if (pending && !(ok = write_o())) break;
+                    pending = true;
+                    o_factor = p.scale * dev::fast_exp2(ri);
+                    o_dst = row < nval ? p.out + ((int64_t)(it.tok0 + c * kChunk + row) * p.num_qo_heads + un.kvh * p.group + g) * D
+                                       : nullptr;
                 }
                 if (ok) arrive_warp(&b->dec_empty[st]);
             }
+        }
+        if (ok && pending) (void)write_o();
         }
     }
     __syncwarp();
@@ -684,8 +854,8 @@ bool encode(CUtensorMap* m, const uint16_t* x, int64_t tokens, int heads, int D,
 template <int D, bool STATES>
 cudaError_t launch(const LinParams& p, int ctas, cudaStream_t s) {
     auto kernel = linear_chunk_kernel<D, STATES>;
-    const size_t smem = SmemMap<D>::kBytes + 1024;
-    static_assert(SmemMap<D>::kBytes + 1024 + sizeof(Bars) <= 227 * 1024, "shared memory per block");
+    const size_t smem = SmemMap<D, STATES>::kBytes + 1024;
+    static_assert(SmemMap<D, STATES>::kBytes + 1024 + sizeof(Bars) <= 227 * 1024, "shared memory per block");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // The register split assumes that the launch allocates exactly kRegsLaunch registers a thread: with

@@ -103,3 +103,45 @@ LENS = [
 def test_against_the_recurrence(heads, gate, lens):
     c = Case(heads, *lens, gate=gate, seed=len(lens[0]), packed=gate == "token", in_place=gate != "head")
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64)], ids=["128", "64"])
+@pytest.mark.parametrize("where", [("v", 200), ("v", 3), ("k", 200), ("q", 150), ("g", 210)], ids=lambda w: f"{w[0]}{w[1]}")
+@pytest.mark.parametrize("value", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_hidden_infinities_and_nan(heads, where, value):
+    """An infinity or a NaN in one token's v, k, q or decay changes no token before it, no other request, and
+    of the tokens after it (in v's case) only the columns that it lies in."""
+    lens, cached = [300, 130, 9], [5, 0, 2]
+    c = Case(heads, lens, cached, gate="token", seed=3)
+    was, want = c.run()
+    after, gates = c.states.clone(), c.log_decay.clone()
+    ref, _, mag, _ = R.attend(c.q, c.k, c.v, c.log_decay, c.starts(was), lens)
+    name, t = where
+    x = {"v": c.v, "k": c.k, "q": c.q, "g": c.log_decay}[name]
+    if name == "g":
+        x[t, 1] = value
+    else:
+        x[t, 1, 7] = value
+    c.states.copy_(was)
+    _, out = c.run()
+    bad = ~torch.isfinite(out.float())
+    odd = torch.zeros_like(bad)
+    G = c.Hq // c.Hkv
+    if name == "q":
+        odd[t, 1] = True
+    elif name == "v":
+        odd[t:300, G:2 * G, 7] = True
+    else:
+        odd[t:300, G:2 * G] = True
+    assert bool((~bad | odd).all())
+    # (their sums may be taken in another order)
+    lim = R.out_limit(ref, mag, gates, lens)
+    assert bool(((out.double() - ref).abs() <= lim)[~odd].all())
+    assert torch.equal(out[300:], want[300:]) and torch.equal(out[:128 * (t // 128)], want[:128 * (t // 128)])
+    if name == "v":                # it stays in every later token's sum
+        assert bool(bad[t:300, G:2 * G, 7].all())
+    same = torch.ones(c.num_states, dtype=torch.bool, device=DEV)
+    same[int(c.state_out[0])] = False
+    assert torch.equal(c.states[same], after[same])
+    i = int(c.state_out[0])
+    assert torch.equal(c.states[i, 0], after[i, 0])
