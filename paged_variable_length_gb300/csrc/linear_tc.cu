@@ -13,8 +13,8 @@
 //   warps 8-15   w K, as three bf16 parts that together hold all 24 bits of the fp32 product (so that the
 //                fp32 state keeps its own), 16 tokens at a time; also zero the rows of V behind the request's
 //                last token, and note whether V holds an infinity or a NaN;
-//   warp 16      issues the MMAs; warp 17 loads K, warp 18 V and Q (TMA, 128-byte swizzle); warp 19
-//                sums the decays (in 64 bits: differences of far sums keep their bits).
+//   warp 16      issues the MMAs of the outputs, warp 17 the state's; warp 18 loads Q, K and V (TMA, 128-byte
+//                swizzle); warp 19 sums the decays (in 64 bits: differences of far sums keep their bits).
 // Roundings to bf16: P and the copy of S, each half a step of the term it scales; out.
 //
 // e^{-c_j} is held to 2^40: in a chunk with sums beyond that ("deep") row i's weights are e^{c_i - r_i - c_j}
@@ -42,7 +42,7 @@ namespace pva {
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16, kLoadK = 17, kLoadQV = 18, kDecayWarp = 19;
+constexpr int kMmaWarp = 16, kStateMmaWarp = 17, kLoadWarp = 18, kDecayWarp = 19;
 // Registers a thread: launched with 96, the state's warpgroup rises to what the others give away
 // (88 + 192 + 2 x 64 + 72 = 5 x 96, so the increase never waits for registers that are not there).
 constexpr int kRegsLaunch = 96, kRegsP = 88, kRegsState = 192, kRegsScale = 64, kRegsCtrl = 72;
@@ -61,22 +61,24 @@ struct SmemMap {
     static constexpr int kTile = kRegion * kHalves;
     static constexpr int kStateRegion = D * 128;
     static constexpr int kSplit = kPartRegion * kHalves;  // one of the three bf16 parts of 16 tokens
-    static constexpr int kStagesK = STATES ? 2 : 1;
+    static constexpr int kStagesK = STATES || D == 64 ? 2 : 1;
+    // staged parts of w K: a part takes about 1200 cycles from one hand to the next and back, its MMAs 200
+    static constexpr int kStagesW = D == 64 ? 8 : STATES ? 4 : 2;
     static constexpr int kQ = 0;                                    // two stages
     static constexpr int kK = kQ + (STATES ? 0 : 2 * kTile);
     static constexpr int kV = kK + kStagesK * kTile;                // two stages
     static constexpr int kS = kV + 2 * kTile;                       // bf16 copy of the state
-    static constexpr int kW = kS + (STATES ? 0 : kStateRegion * kHalves);  // two stages of w K
+    static constexpr int kW = kS + (STATES ? 0 : kStateRegion * kHalves);
     // (D 64: the 128-row A operand of the state's product reaches one region past the part it is of;
     // what lies there ends in TMEM lanes that nobody reads)
-    static constexpr int kBytes = kW + 2 * 3 * kSplit + (D == 64 ? kPartRegion : 0);
+    static constexpr int kBytes = kW + kStagesW * 3 * kSplit + (D == 64 ? kPartRegion : 0);
 };
 
 struct Bars {
     uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], v_ok[2];
     uint64_t p_full[2], p_ready[2], qs_full, o_ready, o_free;
-    uint64_t w_full[4], w_empty[4], ds_full, ds_free, s_full, s_empty;
-    uint64_t dec_full[2], dec_empty[2], drain;
+    uint64_t w_full[kParts], w_empty[kParts], ds_full, ds_free, s_full, s_empty;
+    uint64_t dec_full[2], dec_empty[2], drain[2];
     alignas(16) float c[2][kChunk];  // sums of the log decays up to each token of the chunk, in log2 units
     alignas(16) float f[2][kChunk];  // 2^-c_j
     float w[2][kChunk];              // 2^(c_end - c_j); 0 behind the last token
@@ -236,16 +238,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&b->q_full[s], 1);
             dev::mbar_init(&b->q_empty[s], 1);
             dev::mbar_init(&b->k_full[s], 1);
-            dev::mbar_init(&b->k_empty[s], 9);
+            dev::mbar_init(&b->k_empty[s], STATES ? 8 : 9);
             dev::mbar_init(&b->v_full[s], 1);
-            dev::mbar_init(&b->v_empty[s], 1);
+            dev::mbar_init(&b->v_empty[s], STATES ? 1 : 2);
             dev::mbar_init(&b->v_ok[s], 8);
             dev::mbar_init(&b->p_full[s], 1);
             dev::mbar_init(&b->p_ready[s], 4);
             dev::mbar_init(&b->dec_full[s], 1);
             dev::mbar_init(&b->dec_empty[s], STATES ? 12 : 16);
         }
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < kParts; ++s) {
             dev::mbar_init(&b->w_full[s], 2);
             dev::mbar_init(&b->w_empty[s], 1);
         }
@@ -256,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dev::mbar_init(&b->ds_free, 4);
         dev::mbar_init(&b->s_full, 4);
         dev::mbar_init(&b->s_empty, 1);
-        dev::mbar_init(&b->drain, 1);
+        dev::mbar_init(&b->drain[0], 1);
+        dev::mbar_init(&b->drain[1], 1);
         b->abort_flag = 0;
         b->wait_limit = dev::wait_limit(hdr->wait_override);
         dev::fence_barrier_init();
@@ -273,46 +276,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
+        constexpr uint32_t kDescHi = tc::smem_desc_hi(1024, tc::kSwizzle128B);
+        const uint32_t v_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kV), kRegion);
         if (warp == kMmaWarp) {
-            // ========================================================== MMA issuer (the whole warp, one lane elected)
-            const uint32_t id_qk = tc::idesc_bf16_f32(128, 128, 0, 0), id_v = tc::idesc_bf16_f32(128, D, 0, 1);
-            const uint32_t id_kv = tc::idesc_bf16_f32(128, D, 1, 1);
-            constexpr uint32_t kDescHi = tc::smem_desc_hi(1024, tc::kSwizzle128B);
-            const uint32_t q_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kQ), 16);
-            const uint32_t k_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kK), 16);
-            const uint32_t v_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kV), kRegion);
-            const uint32_t s_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kS), L::kStateRegion);
-            const uint32_t w_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kW), kPartRegion);
-            uint32_t n = 0, h = 0;  // chunks and q heads so far
-            // the state's product of chunk n: 16 tokens at a time, three parts of w K each
-            auto state_product = [&]() -> bool {
-                const int st = n & 1;
-                if (!wait.warp(&b->v_ok[st], (n >> 1) & 1) || (n > 0 && !wait.warp(&b->ds_free, (n - 1) & 1))) return false;
-                for (int s = 0; s < kParts; ++s) {
-                    const uint32_t i = n * kParts + s;
-                    if (!wait.warp(&b->w_full[i & 3], (i >> 2) & 1)) return false;
-                    tc::fence_after_sync();
-                    const uint32_t b0 = v_lo + ((st * L::kTile + s * kPartRegion) >> 4);
-#pragma unroll
-                    for (int x = 0; x < 3; ++x)
-                        tc::mma_ss_warp(tmem + kColState, w_lo + (((i & 1) * 3 + x) * L::kSplit >> 4), b0, kDescHi, id_kv,
-                                        s > 0 || x > 0 ? 1u : 0u);
-                    tc::mma_commit_warp(&b->w_empty[i & 3]);
-                }
-                tc::mma_commit_warp(&b->ds_full);
-                return true;
-            };
-            bool ok = true;
-            if constexpr (STATES) {
-                for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                    const int nch = chunks_of(unit_of<STATES>(items, u, p).it.ntok);
-                    for (int c = 0; ok && c < nch; ++c, ++n) {
-                        ok = state_product();
-                        tc::mma_commit_warp(&b->k_empty[n % KS]);
-                        tc::mma_commit_warp(&b->v_empty[n & 1]);
-                    }
-                }
-            } else {
+            // ========================================================== MMAs of the outputs (one lane elected)
+            if constexpr (!STATES) {
+                const uint32_t id_qk = tc::idesc_bf16_f32(128, 128, 0, 0), id_v = tc::idesc_bf16_f32(128, D, 0, 1);
+                const uint32_t q_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kQ), 16);
+                const uint32_t k_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kK), 16);
+                const uint32_t s_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kS), L::kStateRegion);
+                uint32_t n = 0, h = 0;  // chunks and q heads so far
                 // Q K^T runs one head ahead: its own place in the sequence of heads
                 int qk = 0, q_left = 0, q_heads = 0, qg = 0;  // unit, chunks left of it, its heads, head
                 uint32_t qn = 0, qh = 0;
@@ -326,38 +299,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                         q_heads = x.g1 - x.g0;
                     }
                 };
-                next_unit();
                 auto inputs_seen = [&] {
-                    return seen_warp(&b->q_full[qh & 1], (qh >> 1) & 1) && (qg > 0 || seen_warp(&b->k_full[0], qn & 1));
+                    return seen_warp(&b->q_full[qh & 1], (qh >> 1) & 1) && (qg > 0 || seen_warp(&b->k_full[qn % KS], (qn / KS) & 1));
                 };
                 // (the weights that lay in this buffer were read by the P V of two heads before, issued already)
-                auto issue_qk = [&]() -> bool {
-                    if ((qg == 0 && !wait.warp(&b->k_full[0], qn & 1)) || !wait.warp(&b->q_full[qh & 1], (qh >> 1) & 1)) return false;
+                auto issue_qk = [&](bool seen) -> bool {
+                    if (!seen && ((qg == 0 && !wait.warp(&b->k_full[qn % KS], (qn / KS) & 1)) ||
+                                  !wait.warp(&b->q_full[qh & 1], (qh >> 1) & 1)))
+                        return false;
                     tc::fence_after_sync();
-                    const uint32_t q0 = q_lo + ((qh & 1) * L::kTile >> 4);
+                    const uint32_t q0 = q_lo + ((qh & 1) * L::kTile >> 4), k0 = k_lo + (qn % KS * L::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (uint32_t)((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
-                        tc::mma_ss_warp(tmem + kColP + 128 * (qh & 1), q0 + off, k_lo + off, kDescHi, id_qk, kk > 0 ? 1u : 0u);
+                        tc::mma_ss_warp(tmem + kColP + 128 * (qh & 1), q0 + off, k0 + off, kDescHi, id_qk, kk > 0 ? 1u : 0u);
                     }
                     tc::mma_commit_warp(&b->p_full[qh & 1]);
                     ++qh;
                     if (++qg == q_heads) {
-                        tc::mma_commit_warp(&b->k_empty[0]);
+                        tc::mma_commit_warp(&b->k_empty[qn % KS]);
                         qg = 0;
                         ++qn;
                         if (--q_left == 0) next_unit();
                     }
                     return true;
                 };
-                ok = issue_qk();
+                next_unit();
+                bool ok = true, early = false;
                 for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
                     const Unit x = unit_of<STATES>(items, u, p);
                     const int nch = chunks_of(x.it.ntok), G = x.g1 - x.g0;
                     for (int c = 0; ok && c < nch; ++c, ++n) {
                         const int st = n & 1;
                         for (int g = 0; g < G; ++g, ++h) {
-                            if (g == 0 && !(ok = state_product() && wait.warp(&b->s_full, n & 1))) break;
+                            // this head's scores, if they were not issued a head ahead
+                            if (!early && !(ok = issue_qk(false))) break;
+                            if (g == 0 && !(ok = wait.warp(&b->s_full, n & 1))) break;
                             if (h > 0 && !(ok = wait.warp(&b->o_free, (h - 1) & 1))) break;
                             tc::fence_after_sync();
                             const uint32_t q0 = q_lo + ((h & 1) * L::kTile >> 4);
@@ -367,13 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tc::mma_ss_warp(tmem + kColO, q0 + off, s_lo + (kk * 2048 >> 4), kDescHi, id_v, kk > 0 ? 1u : 0u);
                             }
                             tc::mma_commit_warp(&b->qs_full);
+                            if (g == G - 1) tc::mma_commit_warp(&b->s_empty);
                             // the next head's scores now if their operands are there, else behind P V
-                            const bool early = more && inputs_seen();
-                            if (early && !(ok = issue_qk())) break;
+                            early = more && inputs_seen();
+                            if (early) (void)issue_qk(true);
                             if (!(ok = wait.warp(&b->p_ready[h & 1], (h >> 1) & 1))) break;
                             tc::fence_after_sync();
-                            const bool bad = v_is_bad(b, st);
-                            if (!bad) {
+                            if (!v_is_bad(b, st)) {
                                 const uint32_t b0 = v_lo + (st * L::kTile >> 4);
 #pragma unroll
                                 for (int kk = 0; kk < kChunk / 16; ++kk)
@@ -382,70 +359,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             tc::mma_commit_warp(&b->o_ready);
                             tc::mma_commit_warp(&b->q_empty[h & 1]);
-                            if (g == G - 1) {
-                                tc::mma_commit_warp(&b->v_empty[st]);
-                                tc::mma_commit_warp(&b->s_empty);
-                            }
-                            if (!early && more && !(ok = issue_qk())) break;
+                            if (g == G - 1) tc::mma_commit_warp(&b->v_empty[st]);
                         }
                     }
                 }
             }
             // every MMA issued must complete before TMEM is released
-            tc::mma_commit_warp(&b->drain);
-            (void)dev::mbar_wait(&b->drain, 0);
+            tc::mma_commit_warp(&b->drain[0]);
+            (void)dev::mbar_wait(&b->drain[0], 0);
             __syncwarp();
-        } else if (warp == kLoadK && lane == 0) {
+        } else if (warp == kStateMmaWarp) {
+            // ========================================================== MMAs of the state: 16 tokens at a time, three
+            // parts of w K each
+            const uint32_t id_kv = tc::idesc_bf16_f32(128, D, 1, 1);
+            const uint32_t w_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kW), kPartRegion);
             uint32_t n = 0;
             bool ok = true;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const Unit x = unit_of<STATES>(items, u, p);
-                for (int c = 0; c < chunks_of(x.it.ntok); ++c, ++n) {
-                    if (!(ok = wait.one(&b->k_empty[n % KS], ((n / KS) & 1) ^ 1)) || b->abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    dev::mbar_arrive_expect_tx(&b->k_full[n % KS], L::kTile);
+                const int nch = chunks_of(unit_of<STATES>(items, u, p).it.ntok);
+                for (int c = 0; ok && c < nch; ++c, ++n) {
+                    const int st = n & 1;
+                    if (!(ok = wait.warp(&b->v_ok[st], (n >> 1) & 1) && (n == 0 || wait.warp(&b->ds_free, (n - 1) & 1)))) break;
+                    uint32_t b0 = v_lo + (st * L::kTile >> 4);
+#pragma unroll 1
+                    for (int s = 0; s < kParts; ++s, b0 += kPartRegion >> 4) {
+                        if (!(ok = wait.warp(&b->w_full[s], n & 1))) break;
+                        tc::fence_after_sync();
+                        const uint32_t a0 = w_lo + ((s % L::kStagesW) * (3 * L::kSplit) >> 4);
 #pragma unroll
-                    for (int i = 0; i < L::kHalves; ++i)
-                        tc::tma_load_3d(smem + L::kK + (n % KS) * L::kTile + i * kRegion, &k_map, 64 * i, x.kvh,
-                                        x.it.tok0 + c * kChunk, &b->k_full[n % KS]);
+                        for (int x = 0; x < 3; ++x)
+                            tc::mma_ss_warp(tmem + kColState, a0 + (x * L::kSplit >> 4), b0, kDescHi, id_kv, x > 0 ? 1u : (uint32_t)s);
+                        tc::mma_commit_warp(&b->w_empty[s]);
+                    }
+                    if (!ok) break;
+                    tc::mma_commit_warp(&b->ds_full);
+                    tc::mma_commit_warp(&b->v_empty[st]);
                 }
             }
-            for (uint32_t s = 0; s < KS; ++s)  // its copies land before the CTA leaves
-                if (n > s) (void)dev::mbar_wait(&b->k_full[(n - 1 - s) % KS], ((n - 1 - s) / KS) & 1);
-        } else if (warp == kLoadQV && lane == 0) {
+            tc::mma_commit_warp(&b->drain[1]);
+            (void)dev::mbar_wait(&b->drain[1], 0);
+            __syncwarp();
+        } else if (warp == kLoadWarp && lane == 0) {
+            // ========================================================== loads: of a chunk V, its first Q, K, its other Q
             uint32_t n = 0, h = 0;
             bool ok = true;
+            // n counts chunks whose V is on its way, nk those whose K is
+            uint32_t nk = 0;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
                 const Unit x = unit_of<STATES>(items, u, p);
                 for (int c = 0; ok && c < chunks_of(x.it.ntok); ++c) {
-                    if (!(ok = wait.one(&b->v_empty[n & 1], ((n >> 1) & 1) ^ 1)) || b->abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    dev::mbar_arrive_expect_tx(&b->v_full[n & 1], L::kTile);
-#pragma unroll
-                    for (int i = 0; i < L::kHalves; ++i)
-                        tc::tma_load_3d(smem + L::kV + (n & 1) * L::kTile + i * kRegion, &v_map, 64 * i, x.kvh,
-                                        x.it.tok0 + c * kChunk, &b->v_full[n & 1]);
-                    ++n;
-                    for (int g = x.g0; g < x.g1; ++g, ++h) {
-                        if (!(ok = wait.one(&b->q_empty[h & 1], ((h >> 1) & 1) ^ 1)) || b->abort_flag) {
-                            ok = false;
-                            break;
-                        }
-                        dev::mbar_arrive_expect_tx(&b->q_full[h & 1], L::kTile);
+                    const int t0 = x.it.tok0 + c * kChunk;
+                    auto load = [&](uint64_t* empty, uint64_t* full, uint32_t turn, int at, const CUtensorMap* map, int head) -> bool {
+                        if (!wait.one(empty, (turn & 1) ^ 1) || b->abort_flag) return ok = false;
+                        dev::mbar_arrive_expect_tx(full, L::kTile);
 #pragma unroll
                         for (int i = 0; i < L::kHalves; ++i)
-                            tc::tma_load_3d(smem + L::kQ + (h & 1) * L::kTile + i * kRegion, &q_map, 64 * i,
-                                            x.kvh * p.group + g, x.it.tok0 + c * kChunk, &b->q_full[h & 1]);
+                            tc::tma_load_3d(smem + at + i * kRegion, map, 64 * i, head, t0, full);
+                        return true;
+                    };
+                    if (!load(&b->v_empty[n & 1], &b->v_full[n & 1], n >> 1, L::kV + (n & 1) * L::kTile, &v_map, x.kvh)) break;
+                    ++n;
+#pragma unroll 1
+                    for (int g = x.g0; ok && (g < x.g1 || nk < n); ++g) {
+                        if (g < x.g1) {
+                            if (!load(&b->q_empty[h & 1], &b->q_full[h & 1], h >> 1, L::kQ + (h & 1) * L::kTile, &q_map,
+                                      x.kvh * p.group + g))
+                                break;
+                            ++h;
+                        }
+                        if (nk < n) {
+                            if (!load(&b->k_empty[nk % KS], &b->k_full[nk % KS], nk / KS, L::kK + (nk % KS) * L::kTile, &k_map, x.kvh))
+                                break;
+                            ++nk;
+                        }
                     }
                 }
             }
-            for (uint32_t s = 0; s < 2; ++s) {  // the last copies into either stage
+            // the last copies into every stage land before the CTA leaves
+            for (uint32_t s = 0; s < 2; ++s) {
                 if (n > s) (void)dev::mbar_wait(&b->v_full[(n - 1 - s) & 1], ((n - 1 - s) >> 1) & 1);
                 if (h > s) (void)dev::mbar_wait(&b->q_full[(h - 1 - s) & 1], ((h - 1 - s) >> 1) & 1);
+                if (s < KS && nk > s) (void)dev::mbar_wait(&b->k_full[(nk - 1 - s) % KS], ((nk - 1 - s) / KS) & 1);
             }
         } else if (warp == kDecayWarp) {
             // ========================================================== sums of the log decays, four tokens a lane
@@ -547,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint8_t* K = smem + L::kK + (n % KS) * L::kTile;
 #pragma unroll 1
                 for (int s = pair; s < kParts; s += 4) {
-                    const uint32_t i = n * kParts + s;
+                    const int held = (int)(n * kParts + s) - L::kStagesW;  // the part that its stage held
                     uint4 y[2][L::kHalves];
                     float w[2];
                     uint32_t odd = 0;
@@ -562,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             odd = note_odd(note_odd(note_odd(note_odd(odd, y[z][x].x), y[z][x].y), y[z][x].z), y[z][x].w);
                         }
                     }
-                    uint8_t* W = smem + L::kW + (s & 1) * 3 * L::kSplit;
+                    uint8_t* W = smem + L::kW + (s % L::kStagesW) * 3 * L::kSplit;
                     // an infinity keeps nothing behind its first part (its rest would be a NaN)
                     const bool plain = !__any_sync(0xffffffffu, is_odd(odd));
 #pragma unroll
@@ -586,8 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mid[q] = dev::prmt(__float_as_uint(m0), __float_as_uint(m1), 0x7632);
                                 lo[q] = dev::pack_bf16x2(l0, l1);
                             }
-                            // (its buffer held part i - 2, whose barriers are two pairs on)
-                            if (z == 0 && x == 0 && i >= 2 && !(ok = wait.warp(&b->w_empty[(i - 2) & 3], ((i - 2) >> 2) & 1))) break;
+                            if (z == 0 && x == 0 && held >= 0 &&
+                                !(ok = wait.warp(&b->w_empty[held % kParts], (held / kParts) & 1)))
+                                break;
                             const int r = r0 + 4 * z;
                             uint8_t* at = W + x * kPartRegion + r * 128 + (((cc ^ r) & 7) << 4);
                             *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -598,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!ok) break;
                     tc::fence_proxy_async_smem();
-                    arrive_warp(&b->w_full[s & 3]);
+                    arrive_warp(&b->w_full[s]);
                 }
                 if (!ok) break;
                 arrive_warp(&b->k_empty[n % KS]);
