@@ -44,8 +44,8 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kMmaWarp = 16, kStateMmaWarp = 17, kLoadWarp = 18, kDecayWarp = 19;
 // Registers a thread: launched with 96, the state's warpgroup rises to what the others give away
-// (88 + 192 + 2 x 64 + 72 = 5 x 96, so the increase never waits for registers that are not there).
-constexpr int kRegsLaunch = 96, kRegsP = 88, kRegsState = 192, kRegsScale = 64, kRegsCtrl = 72;
+// (88 + 184 + 2 x 64 + 80 = 5 x 96, so the increase never waits for registers that are not there).
+constexpr int kRegsLaunch = 96, kRegsP = 88, kRegsState = 184, kRegsScale = 64, kRegsCtrl = 80;
 static_assert(kRegsP + kRegsState + 2 * kRegsScale + kRegsCtrl == 5 * kRegsLaunch, "register split must balance");
 constexpr int kRegion = kChunk * 128;  // 128 rows of 128 bytes (64 bf16 columns), swizzled
 constexpr uint32_t kTmemCols = 512;
@@ -90,25 +90,30 @@ struct Bars {
     uint64_t wait_limit;
 };
 
-// Work waits: of a converged warp (voted, so that it leaves together or not at all), and of one thread.
+// The kernel is some 20 warps in half a dozen roles, each going through its own code once a chunk: what keeps it
+// from running is the fetching of instructions (at 126 KB of code a weighted part of 16 keys took 3000 cycles,
+// 600 alone).  So the code is kept short: loops rolled where they can be, one site for what a role does twice,
+// no inlined handling of waits that ran out.
+
+// Waits for a phase, at most limit ns (0: a look).
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    if (dev::mbar_test_wait(bar, parity)) return true;
+    const uint64_t t0 = dev::globaltimer();
+    do {
+        if (limit == 0) return false;
+        if (dev::mbar_try_wait(bar, parity)) return true;
+    } while (dev::globaltimer() - t0 <= limit);
+    return false;
+}
+
+// Work waits: of a converged warp (voted, so that it leaves together or not at all), and of one thread.  A role
+// whose wait ran out leaves its loops and then calls give_up.
 struct Waits {
-    Bars* b;
-    uint32_t* err;
     uint64_t limit;
-    __device__ __forceinline__ bool give_up() const {
-        b->abort_flag = 1;
-        dev::set_error(err, kErrTimeout);
-        return false;
-    }
     __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
-        if (__all_sync(0xffffffffu, dev::mbar_wait(bar, parity, limit))) return true;
-        if ((threadIdx.x & 31) == 0) (void)give_up();
-        __syncwarp();
-        return false;
+        return __all_sync(0xffffffffu, phase_done(bar, parity, limit));
     }
-    __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
-        return dev::mbar_wait(bar, parity, limit) || give_up();
-    }
+    __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const { return phase_done(bar, parity, limit); }
 };
 
 // Whether a phase has completed, without waiting: for a converged warp.
@@ -135,13 +140,13 @@ struct Unit {
 };
 template <bool STATES>
 __device__ __forceinline__ Unit unit_of(const LinItem* items, int u, const LinParams& p) {
-    const int parts = STATES ? 1 : p.head_parts, per = p.num_kv_heads * parts;
+    const unsigned parts = STATES ? 1 : p.head_parts, head = (unsigned)u / parts, part = (unsigned)u - head * parts;
+    const unsigned item = head / (unsigned)p.num_kv_heads;
     Unit x;
-    x.it = items[u / per];
-    x.kvh = u % per / parts;
-    const int part = u % parts;
-    x.g0 = STATES ? 0 : p.group * part / parts;
-    x.g1 = STATES ? 0 : p.group * (part + 1) / parts;
+    x.it = items[item];
+    x.kvh = (int)(head - item * p.num_kv_heads);
+    x.g0 = STATES ? 0 : (int)((unsigned)p.group * part / parts);
+    x.g1 = STATES ? 0 : (int)((unsigned)p.group * (part + 1) / parts);
     return x;
 }
 __device__ __forceinline__ bool v_is_bad(const Bars* b, int st) {
@@ -172,6 +177,21 @@ __device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, 
 // What truncation to bf16 leaves of a pair (exact): f - (upper 16 bits of f).
 __device__ __forceinline__ void rest2(float& m0, float& m1, float f0, float f1) {
     dev::ffma2(m0, m1, hi_f32(__float_as_uint(f0)), hi_f32(__float_as_uint(f1)), -1.f, -1.f, f0, f1);
+}
+
+// D[tmem] = A B for 128 rows and D columns of A (K-major tile): by a converged warp, one lane elected.  B advances by
+// the same steps of 16 (K-major, `bk`) or by 16 rows.
+template <int D>
+__device__ __noinline__ void products(uint32_t d, uint32_t a, uint32_t b, bool bk, uint32_t idesc) {
+    constexpr uint32_t kDescHi = tc::smem_desc_hi(1024, tc::kSwizzle128B);
+#pragma unroll 1
+    for (int half = 0; half < D / 64; ++half) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            tc::mma_ss_warp(d, a + (32 * i >> 4), b + ((bk ? 32 : 2048) * i >> 4), kDescHi, idesc, i > 0 ? 1u : (uint32_t)half);
+        a += kRegion >> 4;
+        b += (bk ? kRegion : 4 * 2048) >> 4;
+    }
 }
 
 // A chunk with an infinity or a NaN in V, or with deep sums: this warp's rows of O (Q S so far) times `part`,
@@ -272,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = b->tmem_base;
-    const Waits wait{b, err, b->wait_limit};
+    const Waits wait{b->wait_limit};
+    bool ok = true;  // none of this warp's waits ran out
 
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
@@ -287,72 +308,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t s_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kS), L::kStateRegion);
                 uint32_t n = 0, h = 0;  // chunks and q heads so far
                 // Q K^T runs one head ahead: its own place in the sequence of heads
-                int qk = 0, q_left = 0, q_heads = 0, qg = 0;  // unit, chunks left of it, its heads, head
+                // (the unit after the one at hand is looked up while that one runs)
+                int q_left = 0, q_heads = 0, qg = 0;  // chunks left of its unit, the unit's heads, head
                 uint32_t qn = 0, qh = 0;
-                bool more = true;
-                auto next_unit = [&] {
-                    const int u = unit_at(qk++, n_units);
-                    more = u >= 0;
-                    if (more) {
-                        const Unit x = unit_of<STATES>(items, u, p);
-                        q_left = chunks_of(x.it.ntok);
-                        q_heads = x.g1 - x.g0;
-                    }
-                };
+                bool more = false;
+                int next_left = 0, next_heads = 0;
                 auto inputs_seen = [&] {
                     return seen_warp(&b->q_full[qh & 1], (qh >> 1) & 1) && (qg > 0 || seen_warp(&b->k_full[qn % KS], (qn / KS) & 1));
                 };
                 // (the weights that lay in this buffer were read by the P V of two heads before, issued already)
-                auto issue_qk = [&](bool seen) -> bool {
-                    if (!seen && ((qg == 0 && !wait.warp(&b->k_full[qn % KS], (qn / KS) & 1)) ||
-                                  !wait.warp(&b->q_full[qh & 1], (qh >> 1) & 1)))
+                auto issue_qk = [&]() -> bool {
+                    if ((qg == 0 && !wait.warp(&b->k_full[qn % KS], (qn / KS) & 1)) || !wait.warp(&b->q_full[qh & 1], (qh >> 1) & 1))
                         return false;
                     tc::fence_after_sync();
                     const uint32_t q0 = q_lo + ((qh & 1) * L::kTile >> 4), k0 = k_lo + (qn % KS * L::kTile >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (uint32_t)((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
-                        tc::mma_ss_warp(tmem + kColP + 128 * (qh & 1), q0 + off, k0 + off, kDescHi, id_qk, kk > 0 ? 1u : 0u);
-                    }
+                    products<D>(tmem + kColP + 128 * (qh & 1), q0, k0, true, id_qk);
                     tc::mma_commit_warp(&b->p_full[qh & 1]);
                     ++qh;
                     if (++qg == q_heads) {
                         tc::mma_commit_warp(&b->k_empty[qn % KS]);
                         qg = 0;
                         ++qn;
-                        if (--q_left == 0) next_unit();
+                        if (--q_left == 0) {
+                            q_left = next_left, q_heads = next_heads;
+                            more = next_left > 0;
+                        }
                     }
                     return true;
                 };
-                next_unit();
-                bool ok = true, early = false;
+                bool early = false;
                 for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                    const Unit x = unit_of<STATES>(items, u, p);
-                    const int nch = chunks_of(x.it.ntok), G = x.g1 - x.g0;
+                    int nch = next_left, G = next_heads;
+                    next_left = next_heads = 0;
+                    for (int i = k == 0 ? 0 : 1; i < 2; ++i) {  // (at first this one as well)
+                        const int v = unit_at(k + i, n_units);
+                        if (v < 0) break;
+                        const Unit x = unit_of<STATES>(items, v, p);
+                        next_left = chunks_of(x.it.ntok), next_heads = x.g1 - x.g0;
+                        if (i == 0) nch = q_left = next_left, G = q_heads = next_heads, more = true, next_left = 0;
+                    }
                     for (int c = 0; ok && c < nch; ++c, ++n) {
                         const int st = n & 1;
                         for (int g = 0; g < G; ++g, ++h) {
-                            // this head's scores, if they were not issued a head ahead
-                            if (!early && !(ok = issue_qk(false))) break;
-                            if (g == 0 && !(ok = wait.warp(&b->s_full, n & 1))) break;
-                            if (h > 0 && !(ok = wait.warp(&b->o_free, (h - 1) & 1))) break;
-                            tc::fence_after_sync();
-                            const uint32_t q0 = q_lo + ((h & 1) * L::kTile >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t off = (uint32_t)((kk >> 2) * kRegion + (kk & 3) * 32) >> 4;
-                                tc::mma_ss_warp(tmem + kColO, q0 + off, s_lo + (kk * 2048 >> 4), kDescHi, id_v, kk > 0 ? 1u : 0u);
+                            // this head's scores (step 0) if they were not issued a head ahead; its Q S; the next head's
+                            // scores (step 1) if their operands are there by now
+#pragma unroll 1
+                            for (int step = 0; ok && step < 2; ++step) {
+                                const bool go = step == 0 ? !early : (early = more && inputs_seen());
+                                if (go && !(ok = issue_qk())) break;
+                                if (step == 1) break;
+                                if (g == 0 && !(ok = wait.warp(&b->s_full, n & 1))) break;
+                                if (h > 0 && !(ok = wait.warp(&b->o_free, (h - 1) & 1))) break;
+                                tc::fence_after_sync();
+                                products<D>(tmem + kColO, q_lo + ((h & 1) * L::kTile >> 4), s_lo, false, id_v);
+                                tc::mma_commit_warp(&b->qs_full);
+                                if (g == G - 1) tc::mma_commit_warp(&b->s_empty);
                             }
-                            tc::mma_commit_warp(&b->qs_full);
-                            if (g == G - 1) tc::mma_commit_warp(&b->s_empty);
-                            // the next head's scores now if their operands are there, else behind P V
-                            early = more && inputs_seen();
-                            if (early) (void)issue_qk(true);
+                            if (!ok) break;
                             if (!(ok = wait.warp(&b->p_ready[h & 1], (h >> 1) & 1))) break;
                             tc::fence_after_sync();
                             if (!v_is_bad(b, st)) {
                                 const uint32_t b0 = v_lo + (st * L::kTile >> 4);
-#pragma unroll
+#pragma unroll 2
                                 for (int kk = 0; kk < kChunk / 16; ++kk)
                                     tc::mma_ts_warp(tmem + kColO, tmem + kColP + 128 * (h & 1) + kk * 8, b0 + (kk * 2048 >> 4),
                                                     kDescHi, id_v, 1u);
@@ -374,7 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t id_kv = tc::idesc_bf16_f32(128, D, 1, 1);
             const uint32_t w_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kW), kPartRegion);
             uint32_t n = 0;
-            bool ok = true;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
                 const int nch = chunks_of(unit_of<STATES>(items, u, p).it.ntok);
                 for (int c = 0; ok && c < nch; ++c, ++n) {
@@ -402,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kLoadWarp && lane == 0) {
             // ========================================================== loads: of a chunk V, its first Q, K, its other Q
             uint32_t n = 0, h = 0;
-            bool ok = true;
             // n counts chunks whose V is on its way, nk those whose K is
             uint32_t nk = 0;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
@@ -444,7 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kDecayWarp) {
             // ========================================================== sums of the log decays, four tokens a lane
             uint32_t n = 0;
-            bool ok = true;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
                 const Unit x = unit_of<STATES>(items, u, p);
                 const int nch = chunks_of(x.it.ntok);
@@ -481,13 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const double ci = before + sum[i];
                         const float cf = (float)ci;
                         b->c[st][4 * lane + i] = cf;
-                        b->f[st][4 * lane + i] = exp2f(-cf);
-                        b->w[st][4 * lane + i] = c * kChunk + 4 * lane + i < x.it.ntok ? exp2f((float)(end - ci)) : 0.f;
+                        b->f[st][4 * lane + i] = dev::fast_exp2(-cf);
+                        b->w[st][4 * lane + i] = c * kChunk + 4 * lane + i < x.it.ntok ? dev::fast_exp2((float)(end - ci)) : 0.f;
                         deep |= !(fabsf(cf) <= kDeep);
                     }
                     deep = __any_sync(0xffffffffu, deep);
                     if (lane == 0) {
-                        b->end[st] = exp2f((float)end);
+                        b->end[st] = dev::fast_exp2((float)end);
                         b->deep[st] = deep;
                     }
                     arrive_warp(&b->dec_full[st]);
@@ -504,7 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wq = warp - 8, pair = wq >> 1;
         const int r0 = (wq & 1) * 8 + (lane >> 3), cc = lane & 7;  // first token of a part's, 16-byte chunk of its row
         uint32_t n = 0;
-        bool ok = true;
         for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
             const int ntok = unit_of<STATES>(items, u, p).it.ntok;
             for (int c = 0; ok && c < chunks_of(ntok); ++c, ++n) {
@@ -544,7 +557,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int held = (int)(n * kParts + s) - L::kStagesW;  // the part that its stage held
                     uint4 y[2][L::kHalves];
                     float w[2];
-                    uint32_t odd = 0;
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const int row = s * kPart + r0 + 4 * z;
@@ -553,12 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < L::kHalves; ++x) {
                             y[z][x] = *reinterpret_cast<const uint4*>(K + x * kRegion + row * 128 + (((cc ^ row) & 7) << 4));
                             if (row >= nval) y[z][x] = make_uint4(0, 0, 0, 0);  // (whatever lies there times 0)
-                            odd = note_odd(note_odd(note_odd(note_odd(odd, y[z][x].x), y[z][x].y), y[z][x].z), y[z][x].w);
                         }
                     }
                     uint8_t* W = smem + L::kW + (s % L::kStagesW) * 3 * L::kSplit;
-                    // an infinity keeps nothing behind its first part (its rest would be a NaN)
-                    const bool plain = !__any_sync(0xffffffffu, is_odd(odd));
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
 #pragma unroll
@@ -567,14 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                // the upper 8 bits, the next 8 and the rest: each difference is exact
+                                // the upper 8 bits, the next 8 and the rest: each difference is exact (of an
+                                // infinity it is a NaN)
                                 float f0, f1, m0, m1, l0, l1;
                                 fmul2(f0, f1, lo_f32(e[q]), hi_f32(e[q]), w[z], w[z]);
                                 rest2(m0, m1, f0, f1);
-                                if (!plain) {
-                                    if (fabsf(f0) == INFINITY) m0 = 0.f;
-                                    if (fabsf(f1) == INFINITY) m1 = 0.f;
-                                }
                                 rest2(l0, l1, m0, m1);
                                 hi[q] = dev::prmt(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
                                 mid[q] = dev::prmt(__float_as_uint(m0), __float_as_uint(m1), 0x7632);
@@ -607,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = row < D;
         const uint32_t t_ds = tmem + kColState + ((uint32_t)((warp & 3) * 32) << 16);
         uint32_t n = 0;
-        bool ok = true;
         const int64_t per_head = (int64_t)D * D;
         for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
             const Unit un = unit_of<STATES>(items, u, p);
@@ -637,14 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The start.  Where other CTAs work on the same request and kv head it is a copy that the kernel before
             // has made: the one that ends with the request's last token may write the slot before the others have
             // read it.  The states pass leaves the first segment's end from there, the others' from zero.
-            if (live) {
-                if (it.seg == 0) {
-                    if (it.in >= 0) add(it.base >= 0 ? segment_state(0) : slot(it.in), 0.f);
-                } else if (!STATES) {
-                    add(segment_state(1), 0.f);
+            if (live && (it.seg == 0 ? it.in >= 0 : !STATES)) {
 #pragma unroll 1
-                    for (int i = 2; i <= it.seg; ++i) add(segment_state(i), seg_decay[(int64_t)(it.base + i) * Hkv + un.kvh]);
-                }
+                for (int i = it.seg == 0 ? 0 : 1; i <= it.seg; ++i)
+                    add(it.base >= 0 ? segment_state(i) : slot(it.in), i > 1 ? seg_decay[(int64_t)(it.base + i) * Hkv + un.kvh] : 0.f);
             }
             for (int c = 0; ok && c < nch; ++c, ++n) {
                 const int st = n & 1;
@@ -682,10 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 arrive_warp(&b->ds_free);
             }
-            if (ok && live) {
-                if (STATES) put(segment_state(it.seg + 1));
-                else if (it.out >= 0 && it.seg == it.nseg - 1 && un.g0 == 0) put(slot(it.out));
-            }
+            if (ok && live && (STATES || (it.out >= 0 && it.seg == it.nseg - 1 && un.g0 == 0)))
+                put(STATES ? segment_state(it.seg + 1) : slot(it.out));
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsP));  // (in the states pass too: the split counts on it)
@@ -695,7 +694,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
         const uint32_t t_o = tmem + kColO + lane_base;
         uint32_t n = 0, h = 0;
-        bool ok = true;
         // the head whose O is still to be written: where to (null: none of this row), and its factor
         bool pending = false;
         uint16_t* o_dst = nullptr;
@@ -729,23 +727,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return true;
         };
-        for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-            const Unit un = unit_of<STATES>(items, u, p);
-            const LinItem& it = un.it;
-            for (int c = 0; ok && c < chunks_of(it.ntok); ++c, ++n) {
-                const int st = n & 1, nval = min(kChunk, it.ntok - c * kChunk);
-                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1) && wait.warp(&b->v_ok[st], (n >> 1) & 1)))
-                    break;
-                const bool bad = v_is_bad(b, st);
-                const bool deep = b->deep[st] != 0;
-                const float ci = b->c[st][row], ri = fminf(fmaxf(ci, -kDeep), kDeep);
-                for (int g = un.g0; g < un.g1; ++g, ++h) {
-                    const uint32_t t_p = tmem + kColP + 128 * (h & 1) + lane_base;
-                    // the head before's O behind this one's weights, unless these are late, or need O themselves
-                    if (pending && (deep || bad || !seen_warp(&b->p_full[h & 1], (h >> 1) & 1))) {
-                        if (!(ok = write_o())) break;
-                        pending = false;
+        // a head after the other: its unit, its chunk's sums and flags
+        int k = 0, tok = 0, left = 0, head0 = 0, heads = 0, g = 0, st = 0;  // tokens: the chunk's first, the unit's left
+        bool bad = false, deep = false, last = false;
+        float ci = 0.f, ri = 0.f;
+        while (true) {
+            if (g == heads) {  // the next chunk
+                if (h > 0) {
+                    arrive_warp(&b->dec_empty[st]);
+                    ++n, tok += kChunk, left -= kChunk;
+                }
+                if (left <= 0) {
+                    const int u = unit_at(k++, n_units);
+                    last = u < 0;
+                    if (!last) {
+                        const Unit un = unit_of<STATES>(items, u, p);
+                        tok = un.it.tok0, left = un.it.ntok, head0 = un.kvh * p.group + un.g0, heads = un.g1 - un.g0;
                     }
+                }
+                if (!last) {
+                    g = 0, st = n & 1;
+                    if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1) && wait.warp(&b->v_ok[st], (n >> 1) & 1))) break;
+                    bad = v_is_bad(b, st), deep = b->deep[st] != 0;
+                    ci = b->c[st][row], ri = fminf(fmaxf(ci, -kDeep), kDeep);
+                }
+            }
+            // this head's weights and, behind them, the head before's O: before them if they are late, or need O
+            // themselves
+            const bool o_first = pending && (last || deep || bad || !seen_warp(&b->p_full[h & 1], (h >> 1) & 1));
+#pragma unroll 1
+            for (int step = 0; ok && step < 2; ++step) {
+                if ((step == 0) == o_first) {
+                    if (pending) ok = write_o();
+                } else if (!last) {
+                    const uint32_t t_p = tmem + kColP + 128 * (h & 1) + lane_base;
                     if (!(ok = wait.warp(&b->p_full[h & 1], (h >> 1) & 1))) break;
                     tc::fence_after_sync();
                     // 32 keys at a time; those past the warp's own rows have no weight.  (The packed weights of
@@ -794,17 +809,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc::fence_before_sync();
                     arrive_warp(&b->p_ready[h & 1]);
-                    if (pending && !(ok = write_o())) break;
-                    pending = true;
-                    o_factor = p.scale * dev::fast_exp2(ri);
-                    o_dst = row < nval ? p.out + ((int64_t)(it.tok0 + c * kChunk + row) * p.num_qo_heads + un.kvh * p.group + g) * D
-                                       : nullptr;
                 }
-                if (ok) arrive_warp(&b->dec_empty[st]);
             }
+            if (!ok || last) break;
+            pending = true;
+            o_factor = p.scale * dev::fast_exp2(ri);
+            o_dst = row < left ? p.out + ((int64_t)(tok + row) * p.num_qo_heads + head0 + g) * D : nullptr;
+            ++g, ++h;
         }
-        if (ok && pending) (void)write_o();
         }
+    }
+    if (!ok) {
+        b->abort_flag = 1;
+        dev::set_error(err, kErrTimeout);
     }
     __syncwarp();
     tc::fence_before_sync();
