@@ -6,8 +6,8 @@
 // with c_i the sum of g over the chunk's tokens up to i
 //   o_i = scale (sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j + e^{c_i} q_i^T S)
 //   S'  = e^{c_end} S + sum_j e^{c_end - c_j} k_j v_j^T.
-// A long request is cut into segments of whole chunks where its heads alone would not fill the GPU:
-// a first pass finds the segments' states, a second starts each from what lies before it.
+// A long request is cut into segments of whole chunks where its heads alone would not fill the GPU: a first pass
+// finds the segments' states, a scan what lies before each, and a second pass starts from there.
 #pragma once
 
 #include "pva_internal.h"
@@ -16,7 +16,6 @@ namespace pva {
 
 constexpr int kStepTokens = 16;   // most new tokens of a request that runs token by token
 constexpr int kChunk = 128;       // tokens of a tensor-core chunk
-constexpr int kMaxSegments = 32;  // most segments of a request
 constexpr uint32_t kErrState = PVA_DEVERR_STATE;
 // Log decays below this are taken as this: e^-110 is 0 in fp32, and -inf - -inf is never formed.
 constexpr float kLeastLogDecay = -110.f;
@@ -34,8 +33,44 @@ struct LinItem {
 };
 static_assert(sizeof(LinItem) == 32, "LinItem is one 32-byte record");
 
-// Workspace carve-up.  The header is a PlanHeader: error_bits, wait_override, n_pre_tiles (segments of
-// long requests) and n_casc_tiles (those of them whose states the first pass finds).
+// Tokens of a segment.  A long request is cut where its batch's heads and requests alone would leave SMs idle: the
+// long requests' tokens dealt out evenly to as many segments as there are SMs for a kv head each, kLeastSegment
+// at least.  A cut costs a first pass over K and V (about a third of the whole), so a request that is not longer
+// than two such shares stays whole: 8 prompts of 256-4096 tokens and 32 heads take 208 us cut at one share and 175
+// whole, one of 16001 tokens and 8 kv heads 1545 us whole and 126 cut.
+constexpr int kLeastSegment = 256;
+constexpr int kWholeSegment = 1 << 30;
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int segment_share(int64_t long_tokens, int kv_heads, int sms) {
+    const int64_t segments = sms / kv_heads > 0 ? sms / kv_heads : 1;
+    const int64_t n = ((long_tokens + segments - 1) / segments + kChunk - 1) / kChunk * kChunk;
+    return n < kLeastSegment ? kLeastSegment : n < kWholeSegment ? (int)n : kWholeSegment;
+}
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int segment_tokens(int64_t long_tokens, int longest, int kv_heads, int sms) {
+    const int n = segment_share(long_tokens, kv_heads, sms);
+    return longest <= 2 * (int64_t)n ? kWholeSegment : n;
+}
+
+// CTAs that share a kv head's q heads (two heads or more each), where the segments' kv heads are fewer than the SMs.
+// Each of them finds the state for itself: two chunks of 700-1500 tokens, 28/4 heads, take 49 us, with one CTA a kv
+// head 70.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int head_parts(int64_t segments, int group, int kv_heads, int sms) {
+    int64_t n = segments > 0 ? sms / (segments * kv_heads) : 1;
+    if (n > group / 2) n = group / 2;
+    return n < 1 ? 1 : (int)n;
+}
+
+// Workspace carve-up.  The header is a PlanHeader: error_bits, wait_override, n_pre_tiles (segments of long
+// requests), n_casc_tiles (those of them whose states the first pass finds), n_casc_groups (requests with such) and
+// n_casc_units (the CTAs that share a kv head's q heads).
 struct LinLayout {
     size_t header;
     size_t tok_req;     // int32 [max_tokens]: request of each new token
@@ -44,7 +79,9 @@ struct LinLayout {
     size_t claim;       // int32 [num_states]: the last request that claimed a slot as its out
     size_t items;       // LinItem [max_items], most tokens first
     size_t pre_items;   // LinItem [max_segs]: the segments of the first pass
-    size_t seg_state;   // fp32 [max_segs][Hkv][D][D]: a request's entry 0: a copy of its start; s: segment s - 1's end
+    size_t cut_items;   // LinItem [max_segs]: the first segments of requests that are cut
+    size_t seg_state;   // fp32 [max_segs][Hkv][D/4 (columns)][D (rows)][4]: a request's entry 0: a copy of its start; s:
+                        // segment s - 1's end from zero, after the scan the request's state there
     size_t seg_decay;   // fp32 [max_segs][Hkv]: entry s: the decay over segment s - 1
     size_t total;
     int32_t max_items;
@@ -59,8 +96,9 @@ struct LinPlanParams {
     int32_t batch;
     int32_t total_tokens;
     int32_t max_q_len;
-    int32_t seg_tokens;        // most tokens of a segment
-    int32_t head_parts;        // CTAs that share the q heads of a kv head
+    int32_t group;
+    int32_t num_kv_heads;
+    int32_t sm_count;
     int64_t num_states;
     uint8_t* ws;
     LinLayout lay;
@@ -82,7 +120,6 @@ struct LinParams {
     int32_t num_kv_heads;
     int32_t group;
     int32_t sm_count;
-    int32_t head_parts;
     float scale;
     uint8_t* ws;
     LinLayout lay;
@@ -96,8 +133,7 @@ struct LinHost {
     int32_t total_tokens;
     int32_t max_q_len;
     int32_t sm_count;
-    int32_t seg_tokens;
-    int32_t head_parts;
+    int32_t may_cut;    // some request may be cut into segments
     const int32_t* cu;
     const int32_t* seqlens;
     uint8_t* ws;
@@ -119,6 +155,7 @@ void set_rotation(const pva_rope* rope, const pva_qk_norm* norm, RopeParams* rp)
 
 cudaError_t launch_linear_plan(const LinPlanParams& p, cudaStream_t s);
 cudaError_t launch_linear_step(const LinParams& p, int head_dim, cudaStream_t s);
+cudaError_t launch_linear_scan(const LinParams& p, int head_dim, cudaStream_t s);
 // states: the first pass (the segments' states), else the outputs
 cudaError_t launch_linear_chunks(const LinParams& p, int head_dim, bool states, int ctas, cudaStream_t s);
 

@@ -33,10 +33,10 @@ pva_status check_config(const pva_linear_config* c) {
 LinLayout make_layout(const pva_linear_config* c, int sms) {
     LinLayout L{};
     L.max_items = (int32_t)(c->max_tokens / kChunk + c->max_batch + 1);
-    // a segment has at least T Hkv / sms of a batch's T tokens and only requests longer than one are cut
-    // (into at most twice what their length would fill): at most 2 sms / Hkv segments of those, and q heads are
-    // dealt out where all long requests' kv heads are fewer than the SMs
-    L.max_segs = 3 * sms / c->num_kv_heads + 3;
+    // Segments with a state in the workspace.  Of a cut request: at most twice what its tokens fill (it is longer than
+    // two shares), and all requests' tokens fill sms / Hkv shares or one; of whole ones whose q heads several CTAs
+    // share: there are at most sms / (2 Hkv) of those.
+    L.max_segs = 3 * (sms / c->num_kv_heads) + 3;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -50,22 +50,11 @@ LinLayout make_layout(const pva_linear_config* c, int sms) {
     L.claim = take(sizeof(int32_t) * (size_t)c->num_states);
     L.items = take(sizeof(LinItem) * (size_t)L.max_items);
     L.pre_items = take(sizeof(LinItem) * (size_t)L.max_segs);
+    L.cut_items = take(sizeof(LinItem) * (size_t)L.max_segs);
     L.seg_state = take(sizeof(float) * (size_t)L.max_segs * c->num_kv_heads * c->head_dim * c->head_dim);
     L.seg_decay = take(sizeof(float) * (size_t)L.max_segs * c->num_kv_heads);
     L.total = off;
     return L;
-}
-
-// Tokens of a segment: a long request is cut where its batch's heads and requests alone would leave SMs
-// idle, into pieces of about an SM's share of all (token, kv head) pairs, at most kMaxSegments of them.
-int32_t segment_tokens(int64_t tokens, int64_t kv_heads, int64_t longest, int sms) {
-    constexpr int64_t kLeast = 512;
-    int64_t n = cdiv(tokens * kv_heads, sms);
-    if (n < kLeast) n = kLeast;
-    const int64_t most = cdiv(longest, kMaxSegments);
-    if (n < most) n = most;
-    n = cdiv(n, kChunk) * kChunk;
-    return (int32_t)(n < ((int64_t)1 << 30) ? n : (int64_t)1 << 30);
 }
 
 // What attn_norm_rope and the linear calls need of a batch of either kind.
@@ -188,7 +177,6 @@ pva_status launch_linear(const LinHost* h, const pva_linear_args* a, const void*
     p.num_kv_heads = h->cfg.num_kv_heads;
     p.group = h->cfg.num_qo_heads / h->cfg.num_kv_heads;
     p.sm_count = h->sm_count;
-    p.head_parts = h->head_parts;
     p.scale = h->cfg.scale > 0.f ? h->cfg.scale : 1.0f / std::sqrt((float)h->cfg.head_dim);
     p.ws = h->ws;
     p.lay = h->lay;
@@ -196,15 +184,10 @@ pva_status launch_linear(const LinHost* h, const pva_linear_args* a, const void*
     // requests of few tokens first: their CTAs are short, and the tensor-core kernel's take whole SMs
     if (launch_linear_step(p, D, s) != cudaSuccess) return PVA_ERR_CUDA;
     if (h->max_q_len <= kStepTokens) return PVA_OK;
-    const int64_t Hkv = h->cfg.num_kv_heads;
-    if (h->max_q_len > h->seg_tokens) {
-        const int64_t most = h->lay.max_segs * Hkv;
-        if (launch_linear_chunks(p, D, true, (int)(most < h->sm_count ? most : h->sm_count), s) != cudaSuccess) return PVA_ERR_CUDA;
-    }
-    const int64_t longs = h->total_tokens / (kStepTokens + 1) < h->batch ? h->total_tokens / (kStepTokens + 1) : h->batch;
-    const int64_t most = (longs + (h->max_q_len > h->seg_tokens ? h->lay.max_segs : 0)) * Hkv * h->head_parts;
-    return launch_linear_chunks(p, D, false, (int)(most < h->sm_count ? most : h->sm_count), s) == cudaSuccess ? PVA_OK
-                                                                                                             : PVA_ERR_CUDA;
+    if (h->may_cut && (launch_linear_chunks(p, D, true, h->sm_count, s) != cudaSuccess ||
+                       launch_linear_scan(p, D, s) != cudaSuccess))
+        return PVA_ERR_CUDA;
+    return launch_linear_chunks(p, D, false, h->sm_count, s) == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
 
 }  // namespace
@@ -268,8 +251,9 @@ pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_s
     h.total_tokens = total_tokens;
     h.max_q_len = max_q_len > 0 && max_q_len < total_tokens ? max_q_len : (total_tokens > 0 ? total_tokens : 1);
     h.sm_count = sms;
-    h.seg_tokens = segment_tokens(total_tokens, cfg->num_kv_heads, h.max_q_len, sms);
-    h.head_parts = 1;
+    // (the long requests have all tokens but kStepTokens of each short one at most)
+    const int64_t least = (int64_t)total_tokens - (int64_t)kStepTokens * batch;
+    h.may_cut = segment_tokens(least > 0 ? least : 0, h.max_q_len, cfg->num_kv_heads, sms) < kWholeSegment ? 1 : 0;
     h.cu = cu_seqlens_q;
     h.seqlens = cache_seqlens;
     h.ws = static_cast<uint8_t*>(workspace);
@@ -282,8 +266,9 @@ pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_s
     pp.batch = batch;
     pp.total_tokens = total_tokens;
     pp.max_q_len = h.max_q_len;
-    pp.seg_tokens = h.seg_tokens;
-    pp.head_parts = h.head_parts;
+    pp.group = cfg->num_qo_heads / cfg->num_kv_heads;
+    pp.num_kv_heads = cfg->num_kv_heads;
+    pp.sm_count = sms;
     pp.num_states = cfg->num_states;
     pp.ws = h.ws;
     pp.lay = h.lay;

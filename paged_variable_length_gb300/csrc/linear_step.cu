@@ -1,4 +1,5 @@
-// K9, K10: linear attention's plan, and its recurrence for requests of few new tokens.
+// K9, K10, K12: linear attention's plan, its recurrence for requests of few new tokens, and the scan over a long
+// request's segments.
 //
 // K10, for one (request, kv head): S <- e^{g_t} S + k_t v_t^T, o_t = scale q_t^T S_t, token by token, all
 // in fp32.  The state is read once and written once for all of the request's new tokens, and the G q
@@ -26,7 +27,8 @@ constexpr int kBuckets = 256;  // segments sorted by chunks (more: the first buc
 // no one claimed is told by that request's own out slot being another.
 __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlanParams p) {
     __shared__ int32_t hist[kBuckets], first[kBuckets];
-    __shared__ int32_t n_items, n_pre, n_segs;
+    __shared__ int32_t n_items, n_pre, n_segs, n_cut, longest, n_long;
+    __shared__ unsigned long long long_tokens;
     __shared__ uint32_t all_err;
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
     int2* req_state = reinterpret_cast<int2*>(p.ws + p.lay.req_state);
@@ -35,9 +37,10 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
     int32_t* tok_req = reinterpret_cast<int32_t*>(p.ws + p.lay.tok_req);
     LinItem* items = reinterpret_cast<LinItem*>(p.ws + p.lay.items);
     LinItem* pre = reinterpret_cast<LinItem*>(p.ws + p.lay.pre_items);
+    LinItem* cuts = reinterpret_cast<LinItem*>(p.ws + p.lay.cut_items);
     const int tid = threadIdx.x, B = p.batch;
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
-    if (tid == 0) n_items = n_pre = n_segs = 0, all_err = 0;
+    if (tid == 0) n_items = n_pre = n_segs = n_cut = longest = n_long = 0, long_tokens = 0, all_err = 0;
 
     uint32_t err = 0;
     for (int i = tid; i < B; i += kPlanThreads) {
@@ -94,17 +97,29 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
         }
         __syncthreads();
     }
-    // how a request is cut: chunks of a segment, and segments
-    auto cut = [&](int n, int* per) -> int {
-        const int chunks = (n + kChunk - 1) / kChunk;
-        const int want = (n + p.seg_tokens - 1) / p.seg_tokens;
-        *per = (chunks + want - 1) / want;
-        return (chunks + *per - 1) / *per;
-    };
     auto is_long = [&](int i, int* n) {
         *n = p.cu[i + 1] - p.cu[i];
         return *n > kStepTokens && req_state[i].x != -2;
     };
+    if (!fatal) {
+        for (int i = tid; i < B; i += kPlanThreads) {
+            int n;
+            if (!is_long(i, &n)) continue;
+            atomicMax(&longest, n);
+            atomicAdd(&n_long, 1);
+            atomicAdd(&long_tokens, (unsigned long long)n);
+        }
+        __syncthreads();
+    }
+    // how a request is cut: chunks of a segment, and segments
+    const int seg_tokens = segment_tokens((int64_t)long_tokens, longest, p.num_kv_heads, p.sm_count);
+    auto cut = [&](int n, int* per) -> int {
+        const int chunks = (n + kChunk - 1) / kChunk;
+        const int want = (int)(((int64_t)n + seg_tokens - 1) / seg_tokens);
+        *per = (chunks + want - 1) / want;
+        return (chunks + *per - 1) / *per;
+    };
+    int parts = 1;
     if (!fatal) {
         for (int i = tid; i < B; i += kPlanThreads) {
             int n, per;
@@ -132,6 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
             if (tid == 0) n_items = sum;
         }
         __syncthreads();
+        parts = head_parts(n_items, p.group, p.num_kv_heads, p.sm_count);
         for (int i = tid; i < B; i += kPlanThreads) {
             int n, per;
             req_base[i] = -1;
@@ -143,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
             it.nseg = nseg;
             it.in = req_state[i].x;
             // several CTAs on one state: they start from a copy
-            it.base = nseg > 1 || (p.head_parts > 1 && it.in >= 0) ? atomicAdd(&n_segs, nseg) : -1;
+            it.base = nseg > 1 || (parts > 1 && it.in >= 0) ? atomicAdd(&n_segs, nseg) : -1;
             if (it.in >= 0) req_base[i] = it.base;
             it.out = req_state[i].y;
             for (int s = 0; s < nseg; ++s) {
@@ -152,6 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
                 it.ntok = min(per * kChunk, n - s * per * kChunk);
                 items[atomicAdd(&first[kBuckets - min((it.ntok + kChunk - 1) / kChunk, kBuckets)], 1)] = it;
                 if (s < nseg - 1) pre[at + s] = it;
+                if (s == 0 && nseg > 1) cuts[atomicAdd(&n_cut, 1)] = it;
             }
         }
         // requests of the tokens: a few tokens by one thread, many by the block
@@ -170,6 +187,8 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
     if (tid == 0) {
         hdr->n_pre_tiles = fatal ? 0 : n_items;
         hdr->n_casc_tiles = fatal ? 0 : n_pre;
+        hdr->n_casc_groups = fatal ? 0 : n_cut;
+        hdr->n_casc_units = parts;
         hdr->wait_override = 0;
         hdr->error_bits = all_err;
     }
@@ -240,10 +259,11 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
         for (int i = 0; i < R; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (copy >= 0) {
-        float* dst = reinterpret_cast<float*>(p.ws + p.lay.seg_state) + ((int64_t)copy * p.num_kv_heads + kvh) * per_head +
-                     row0 * D + col0 + col;
+        // (as the tensor-core kernel reads it: four columns of a row, then those of the next row)
+        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.ws + p.lay.seg_state) +
+                                                ((int64_t)copy * p.num_kv_heads + kvh) * per_head) + (col0 + col) / 4 * D + row0;
 #pragma unroll
-        for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(dst + i * D) = S[i];
+        for (int i = 0; i < R; ++i) dst[i] = S[i];
         return;
     }
     int buf = 0;
@@ -307,6 +327,46 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
     }
 }
 
+// ---------------------------------------------------------------- K12: the scan over a request's segments
+//
+// Entry i of a request's segment states, i >= 2, holds the end of segment i - 1 from zero: X_i; it becomes that
+// segment's end from the request's start, S_i = (decay over segment i - 1) S_{i-1} + X_i.  Four elements of a state a
+// thread, every segment's in turn, four loads in flight.  Bound: the L2's latency (18 segments of 8 heads of 128 x 128:
+// 18 MB in 7.3 us; each segment's CTAs summing what lies before it took up to 20).
+constexpr int kScanThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinParams p) {
+    dev::grid_dep_wait();
+    dev::grid_dep_launch();
+    const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(p.ws + p.lay.header);
+    if (hdr->error_bits & kErrFatal) return;
+    constexpr int kParts = D * D / 4 / kScanThreads;  // blocks of a state
+    const int work = hdr->n_casc_groups * p.num_kv_heads * kParts;
+    for (int x = blockIdx.x; x < work; x += gridDim.x) {
+        const LinItem it = reinterpret_cast<const LinItem*>(p.ws + p.lay.cut_items)[x / (p.num_kv_heads * kParts)];
+        const int kvh = x / kParts % p.num_kv_heads;
+        const int64_t step = (int64_t)p.num_kv_heads * D * D / 4, first = (int64_t)it.base * p.num_kv_heads + kvh;
+        float4* s = reinterpret_cast<float4*>(p.ws + p.lay.seg_state) + first * (D * D / 4) + x % kParts * kScanThreads + threadIdx.x;
+        const float* decay = reinterpret_cast<const float*>(p.ws + p.lay.seg_decay) + first;
+        float4 S = s[step];
+        for (int i = 2; i < it.nseg; i += 4) {
+            float4 y[4];
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j < it.nseg) y[j] = s[(i + j) * step], f[j] = decay[(int64_t)(i + j) * p.num_kv_heads];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j < it.nseg) {
+                    S.x = fmaf(f[j], S.x, y[j].x), S.y = fmaf(f[j], S.y, y[j].y);
+                    S.z = fmaf(f[j], S.z, y[j].z), S.w = fmaf(f[j], S.w, y[j].w);
+                    s[(i + j) * step] = S;
+                }
+        }
+    }
+}
+
 template <int D, int P>
 cudaError_t launch_step(const LinParams& p, cudaStream_t s) {
     return launch_programmatic(linear_step_kernel<D, P>, dim3((unsigned)(p.num_kv_heads * P), (unsigned)p.batch),
@@ -325,6 +385,13 @@ cudaError_t launch_step_d(const LinParams& p, cudaStream_t s) {
 cudaError_t launch_linear_plan(const LinPlanParams& p, cudaStream_t s) {
     linear_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t launch_linear_scan(const LinParams& p, int head_dim, cudaStream_t s) {
+    auto go = [&](auto kernel) { return launch_programmatic(kernel, dim3((unsigned)(4 * p.sm_count)), (unsigned)kScanThreads, 0, s, p); };
+    if (head_dim == 128) return go(linear_scan_kernel<128>);
+    if (head_dim == 64) return go(linear_scan_kernel<64>);
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_linear_step(const LinParams& p, int head_dim, cudaStream_t s) {

@@ -1,15 +1,15 @@
 // K11: linear attention of requests with many new tokens, in chunks of 128 on the 5th-generation tensor
 // cores.  For a chunk with c_i the sum of the log decays up to token i and S the state before it:
-//   o_i = scale e^{c_i} (q_i^T S + sum_{j <= i} (q_i . k_j) e^{-c_j} v_j)
+//   o_i = scale e^{c_i + r} (q_i^T (e^{-r} S) + sum_{j <= i} (q_i . k_j) e^{-c_j - r} v_j)      for any r
 //   S'  = e^{c_end} S + sum_j (e^{c_end - c_j} k_j) v_j^T
 // Four products of 128 rows: Q K^T, Q S and P V for each q head, (w K)^T V once for its kv head.
 //
 // A work unit is a segment of a request, a kv head and some of its q heads; its chunks run one after
 // another, with the state in the registers of a warpgroup (fp32, a row of S a thread) and every product's
 // accumulator in TMEM (two of Q K^T, so that the next head's runs while this one's weights are made):
-//   warps 0-3    P: a row of Q K^T a thread, times e^{-c_j} up to the diagonal, to bf16 in TMEM (the A
-//                operand of P V, which adds to Q S); then the row of O, times scale e^{c_i}, to bf16 in HBM;
-//   warps 4-7    S <- e^{c_end} S + (w K)^T V, and its bf16 copy in shared memory for the next chunk's Q S;
+//   warps 0-3    P: a row of Q K^T a thread, times e^{-c_j - r} up to the diagonal, to bf16 in TMEM (the A
+//                operand of P V, which adds to Q S); then the row of O, times scale e^{c_i + r}, to bf16 in HBM;
+//   warps 4-7    S <- e^{c_end} S + (w K)^T V, and e^{-r} S as bf16 in shared memory for the next chunk's Q S;
 //   warps 8-15   w K, as three bf16 parts that together hold all 24 bits of the fp32 product (so that the
 //                fp32 state keeps its own), 16 tokens at a time; also zero the rows of V behind the request's
 //                last token, and note whether V holds an infinity or a NaN;
@@ -17,13 +17,15 @@
 //                swizzle); warp 19 sums the decays (in 64 bits: differences of far sums keep their bits).
 // Roundings to bf16: P and the copy of S, each half a step of the term it scales; out.
 //
-// e^{-c_j} is held to 2^40: in a chunk with sums beyond that ("deep") row i's weights are e^{c_i - r_i - c_j}
-// with r_i = c_i held to +-40 (log2), its part of Q S is scaled by e^{c_i - r_i} in TMEM before P V adds to it,
-// and O takes e^{r_i}.  Weight 0 times an infinity or a NaN of V behind the diagonal would reach the chunk's
+// r (a whole number of powers of two) is 0, or halfway in a chunk whose sums go further than 2^60, so that weights stay
+// within 2^+-60: up to sums of 2^120 (0.65 a token).  In chunks beyond that ("deep") row i's weights are
+// e^{c_i - r_i - c_j} with r_i = c_i held to +-40 (log2), its part of Q S is scaled by e^{c_i - r_i} in TMEM before
+// P V adds to it, and O takes e^{r_i}.  (With an r of 0 alone a prompt of 16 k tokens, 8 kv heads, took 135 us for 126.)
+// Weight 0 times an infinity or a NaN of V behind the diagonal would reach the chunk's
 // earlier tokens, so a chunk with one takes P V row by row on the CUDA cores, over the keys that each row sees.
 //
-// States pass: only w K, V and the state update; the segments' own states and decays go to the workspace,
-// and the main pass starts a segment from those before it.
+// States pass: only w K, V and the state update; the segments' own states and decays go to the workspace, where
+// the scan (K12) makes of them the states that the main pass starts its segments from.
 //
 // Every wait is bounded; a timeout sets PVA_DEVERR_TIMEOUT and the CTA winds down (outstanding copies
 // and MMAs waited for, TMEM freed) without trapping.
@@ -50,7 +52,8 @@ static_assert(kRegsP + kRegsState + 2 * kRegsScale + kRegsCtrl == 5 * kRegsLaunc
 constexpr int kRegion = kChunk * 128;  // 128 rows of 128 bytes (64 bf16 columns), swizzled
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColP = 0, kColO = 256, kColState = 384;  // TMEM columns (two buffers of Q K^T)
-constexpr float kDeep = 40.f;             // largest |c_i| (log2) whose power enters the weights
+constexpr float kReach = 60.f;            // largest power (log2) that enters the weights of a chunk with one r
+constexpr float kDeep = 40.f;             // the same of one with an r for each row
 constexpr int kPart = 16;                 // tokens of a staged part of w K
 constexpr int kParts = kChunk / kPart;
 constexpr int kPartRegion = kPart * 128;  // 16 rows of 128 bytes
@@ -61,47 +64,59 @@ struct SmemMap {
     static constexpr int kTile = kRegion * kHalves;
     static constexpr int kStateRegion = D * 128;
     static constexpr int kSplit = kPartRegion * kHalves;  // one of the three bf16 parts of 16 tokens
-    static constexpr int kStagesK = STATES || D == 64 ? 2 : 1;
+    // K lies in halves of 64 tokens, each let go by itself: with one tile the load of the next first half (some
+    // 3000 cycles) runs behind the weighting of this second one
+    static constexpr int kHalvesK = STATES || D == 64 ? 4 : 2;
     // staged parts of w K: a part takes about 1200 cycles from one hand to the next and back, its MMAs 200
     static constexpr int kStagesW = D == 64 ? 8 : STATES ? 4 : 2;
     static constexpr int kQ = 0;                                    // two stages
     static constexpr int kK = kQ + (STATES ? 0 : 2 * kTile);
-    static constexpr int kV = kK + kStagesK * kTile;                // two stages
-    static constexpr int kS = kV + 2 * kTile;                       // bf16 copy of the state
-    static constexpr int kW = kS + (STATES ? 0 : kStateRegion * kHalves);
+    static constexpr int kV = kK + kHalvesK / 2 * kTile;            // two stages
+    static constexpr int kS = kV + 2 * kTile;                       // bf16 copy of the state (and its way to memory)
+    static constexpr int kW = kS + kStateRegion * kHalves;
     // (D 64: the 128-row A operand of the state's product reaches one region past the part it is of;
     // what lies there ends in TMEM lanes that nobody reads)
     static constexpr int kBytes = kW + kStagesW * 3 * kSplit + (D == 64 ? kPartRegion : 0);
 };
 
 struct Bars {
-    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], v_ok[2];
+    uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[2], v_empty[2], v_ok[2];
     uint64_t p_full[2], p_ready[2], qs_full, o_ready, o_free;
     uint64_t w_full[kParts], w_empty[kParts], ds_full, ds_free, s_full, s_empty;
     uint64_t dec_full[2], dec_empty[2], drain[2];
     alignas(16) float c[2][kChunk];  // sums of the log decays up to each token of the chunk, in log2 units
-    alignas(16) float f[2][kChunk];  // 2^-c_j
+    alignas(16) float f[2][kChunk];  // 2^(-c_j - r)
     float w[2][kChunk];              // 2^(c_end - c_j); 0 behind the last token
-    float end[2];                    // 2^c_end
-    int32_t deep[2];                 // some |c_i| > kDeep
+    float end[2], r[2], down[2];     // 2^c_end; r (log2); 2^-r
+    int32_t deep[2];                 // no r will do
     alignas(16) int32_t v_bad[2][8];
     uint32_t tmem_base;
     int32_t abort_flag;
     uint64_t wait_limit;
 };
 
-// The kernel is some 20 warps in half a dozen roles, each going through its own code once a chunk: what keeps it
+// The kernel is 20 warps in half a dozen roles, each going through its own code once a chunk: much of what keeps it
 // from running is the fetching of instructions (at 126 KB of code a weighted part of 16 keys took 3000 cycles,
 // 600 alone).  So the code is kept short: loops rolled where they can be, one site for what a role does twice,
 // no inlined handling of waits that ran out.
 
-// Waits for a phase, at most limit ns (0: a look).
+// Waits for a phase, at most limit ns (0: a look), asleep for up to kNap ns at a time (without that the warps that wait
+// look some sixty times a chunk each, and take more than half of all issue slots).
+constexpr uint32_t kNap = 20000;
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity, uint64_t limit) {
     if (dev::mbar_test_wait(bar, parity)) return true;
+    if (limit == 0) return false;
     const uint64_t t0 = dev::globaltimer();
     do {
-        if (limit == 0) return false;
-        if (dev::mbar_try_wait(bar, parity)) return true;
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(dev::smem_u32(bar)), "r"(parity), "r"(kNap)
+            : "memory");
+        if (done) return true;
     } while (dev::globaltimer() - t0 <= limit);
     return false;
 }
@@ -139,8 +154,8 @@ struct Unit {
     int kvh, g0, g1;
 };
 template <bool STATES>
-__device__ __forceinline__ Unit unit_of(const LinItem* items, int u, const LinParams& p) {
-    const unsigned parts = STATES ? 1 : p.head_parts, head = (unsigned)u / parts, part = (unsigned)u - head * parts;
+__device__ __forceinline__ Unit unit_of(const LinItem* items, int u, const LinParams& p, unsigned parts) {
+    const unsigned head = (unsigned)u / parts, part = (unsigned)u - head * parts;
     const unsigned item = head / (unsigned)p.num_kv_heads;
     Unit x;
     x.it = items[item];
@@ -235,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const LinParams p, const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using L = SmemMap<D, STATES>;
-    constexpr uint32_t KS = L::kStagesK;
+    constexpr uint32_t KH = L::kHalvesK, KS = KH / 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Bars bars;
@@ -246,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
     uint32_t* err = &hdr->error_bits;
     const int Hkv = p.num_kv_heads;
-    const int n_units = STATES ? hdr->n_casc_tiles * Hkv : hdr->n_pre_tiles * Hkv * p.head_parts;
+    const unsigned parts = STATES ? 1 : hdr->n_casc_units;  // CTAs that share a kv head's q heads
+    const int n_units = (STATES ? hdr->n_casc_tiles : hdr->n_pre_tiles) * Hkv * (int)parts;
     if ((hdr->error_bits & kErrFatal) || (int)blockIdx.x >= n_units) return;
     const LinItem* items = reinterpret_cast<const LinItem*>(p.ws + (STATES ? p.lay.pre_items : p.lay.items));
     float* seg_state = reinterpret_cast<float*>(p.ws + p.lay.seg_state);
@@ -257,8 +273,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 2; ++s) {
             dev::mbar_init(&b->q_full[s], 1);
             dev::mbar_init(&b->q_empty[s], 1);
-            dev::mbar_init(&b->k_full[s], 1);
-            dev::mbar_init(&b->k_empty[s], STATES ? 8 : 9);
             dev::mbar_init(&b->v_full[s], 1);
             dev::mbar_init(&b->v_empty[s], STATES ? 1 : 2);
             dev::mbar_init(&b->v_ok[s], 8);
@@ -266,6 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&b->p_ready[s], 4);
             dev::mbar_init(&b->dec_full[s], 1);
             dev::mbar_init(&b->dec_empty[s], STATES ? 12 : 16);
+        }
+        for (uint32_t s = 0; s < KH; ++s) {
+            dev::mbar_init(&b->k_full[s], 1);
+            dev::mbar_init(&b->k_empty[s], STATES ? 8 : 9);
         }
         for (int s = 0; s < kParts; ++s) {
             dev::mbar_init(&b->w_full[s], 2);
@@ -314,19 +332,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool more = false;
                 int next_left = 0, next_heads = 0;
                 auto inputs_seen = [&] {
-                    return seen_warp(&b->q_full[qh & 1], (qh >> 1) & 1) && (qg > 0 || seen_warp(&b->k_full[qn % KS], (qn / KS) & 1));
+                    return seen_warp(&b->q_full[qh & 1], (qh >> 1) & 1) &&
+                           (qg > 0 || seen_warp(&b->k_full[2 * (qn % KS) + 1], (qn / KS) & 1));
                 };
                 // (the weights that lay in this buffer were read by the P V of two heads before, issued already)
-                auto issue_qk = [&]() -> bool {
-                    if ((qg == 0 && !wait.warp(&b->k_full[qn % KS], (qn / KS) & 1)) || !wait.warp(&b->q_full[qh & 1], (qh >> 1) & 1))
-                        return false;
+                auto inputs_there = [&] {
+                    return (qg > 0 || (wait.warp(&b->k_full[2 * (qn % KS)], (qn / KS) & 1) &&
+                                       wait.warp(&b->k_full[2 * (qn % KS) + 1], (qn / KS) & 1))) &&
+                           wait.warp(&b->q_full[qh & 1], (qh >> 1) & 1);
+                };
+                auto issue_qk = [&] {
                     tc::fence_after_sync();
                     const uint32_t q0 = q_lo + ((qh & 1) * L::kTile >> 4), k0 = k_lo + (qn % KS * L::kTile >> 4);
                     products<D>(tmem + kColP + 128 * (qh & 1), q0, k0, true, id_qk);
                     tc::mma_commit_warp(&b->p_full[qh & 1]);
                     ++qh;
                     if (++qg == q_heads) {
-                        tc::mma_commit_warp(&b->k_empty[qn % KS]);
+                        tc::mma_commit_warp(&b->k_empty[2 * (qn % KS)]);
+                        tc::mma_commit_warp(&b->k_empty[2 * (qn % KS) + 1]);
                         qg = 0;
                         ++qn;
                         if (--q_left == 0) {
@@ -334,49 +357,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                             more = next_left > 0;
                         }
                     }
-                    return true;
                 };
-                bool early = false;
                 for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
                     int nch = next_left, G = next_heads;
                     next_left = next_heads = 0;
                     for (int i = k == 0 ? 0 : 1; i < 2; ++i) {  // (at first this one as well)
                         const int v = unit_at(k + i, n_units);
                         if (v < 0) break;
-                        const Unit x = unit_of<STATES>(items, v, p);
+                        const Unit x = unit_of<STATES>(items, v, p, parts);
                         next_left = chunks_of(x.it.ntok), next_heads = x.g1 - x.g0;
                         if (i == 0) nch = q_left = next_left, G = q_heads = next_heads, more = true, next_left = 0;
                     }
                     for (int c = 0; ok && c < nch; ++c, ++n) {
                         const int st = n & 1;
-                        for (int g = 0; g < G; ++g, ++h) {
-                            // this head's scores (step 0) if they were not issued a head ahead; its Q S; the next head's
-                            // scores (step 1) if their operands are there by now
+                        for (int g = 0; ok && g < G; ++g, ++h) {
+                            // What a head takes: its scores (issued during the head before, if their operands were there by
+                            // then), Q S, P V.  Steps 0: scores, if not issued yet; 1: Q S; 2: the next head's scores if P is
+                            // not there yet and their operands are; 3: P V; 4: the next head's scores if their operands are there.
 #pragma unroll 1
-                            for (int step = 0; ok && step < 2; ++step) {
-                                const bool go = step == 0 ? !early : (early = more && inputs_seen());
-                                if (go && !(ok = issue_qk())) break;
-                                if (step == 1) break;
-                                if (g == 0 && !(ok = wait.warp(&b->s_full, n & 1))) break;
-                                if (h > 0 && !(ok = wait.warp(&b->o_free, (h - 1) & 1))) break;
-                                tc::fence_after_sync();
-                                products<D>(tmem + kColO, q_lo + ((h & 1) * L::kTile >> 4), s_lo, false, id_v);
-                                tc::mma_commit_warp(&b->qs_full);
-                                if (g == G - 1) tc::mma_commit_warp(&b->s_empty);
+                            for (int step = 0; ok && step < 5; ++step) {
+                                if (step == 1) {
+                                    ok = (g > 0 || wait.warp(&b->s_full, n & 1)) && (h == 0 || wait.warp(&b->o_free, (h - 1) & 1));
+                                    if (!ok) break;
+                                    tc::fence_after_sync();
+                                    products<D>(tmem + kColO, q_lo + ((h & 1) * L::kTile >> 4), s_lo, false, id_v);
+                                    tc::mma_commit_warp(&b->qs_full);
+                                    tc::mma_commit_warp(&b->q_empty[h & 1]);
+                                    if (g == G - 1) tc::mma_commit_warp(&b->s_empty);
+                                } else if (step == 3) {
+                                    if (!(ok = wait.warp(&b->p_ready[h & 1], (h >> 1) & 1))) break;
+                                    tc::fence_after_sync();
+                                    if (!v_is_bad(b, st)) {
+                                        const uint32_t b0 = v_lo + (st * L::kTile >> 4);
+#pragma unroll 4
+                                        for (int kk = 0; kk < kChunk / 16; ++kk)
+                                            tc::mma_ts_warp(tmem + kColO, tmem + kColP + 128 * (h & 1) + kk * 8,
+                                                            b0 + (kk * 2048 >> 4), kDescHi, id_v, 1u);
+                                    }
+                                    tc::mma_commit_warp(&b->o_ready);
+                                    if (g == G - 1) tc::mma_commit_warp(&b->v_empty[st]);
+                                } else if (more && qh == h + (step > 0) &&
+                                           (step != 2 || !seen_warp(&b->p_ready[h & 1], (h >> 1) & 1)) &&
+                                           (step == 0 || inputs_seen())) {
+                                    if (step == 0) ok = inputs_there();
+                                    if (ok) issue_qk();
+                                }
                             }
-                            if (!ok) break;
-                            if (!(ok = wait.warp(&b->p_ready[h & 1], (h >> 1) & 1))) break;
-                            tc::fence_after_sync();
-                            if (!v_is_bad(b, st)) {
-                                const uint32_t b0 = v_lo + (st * L::kTile >> 4);
-#pragma unroll 2
-                                for (int kk = 0; kk < kChunk / 16; ++kk)
-                                    tc::mma_ts_warp(tmem + kColO, tmem + kColP + 128 * (h & 1) + kk * 8, b0 + (kk * 2048 >> 4),
-                                                    kDescHi, id_v, 1u);
-                            }
-                            tc::mma_commit_warp(&b->o_ready);
-                            tc::mma_commit_warp(&b->q_empty[h & 1]);
-                            if (g == G - 1) tc::mma_commit_warp(&b->v_empty[st]);
                         }
                     }
                 }
@@ -392,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t w_lo = tc::smem_desc_lo(dev::smem_u32(smem + L::kW), kPartRegion);
             uint32_t n = 0;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const int nch = chunks_of(unit_of<STATES>(items, u, p).it.ntok);
+                const int nch = chunks_of(unit_of<STATES>(items, u, p, parts).it.ntok);
                 for (int c = 0; ok && c < nch; ++c, ++n) {
                     const int st = n & 1;
                     if (!(ok = wait.warp(&b->v_ok[st], (n >> 1) & 1) && (n == 0 || wait.warp(&b->ds_free, (n - 1) & 1)))) break;
@@ -416,51 +442,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             (void)dev::mbar_wait(&b->drain[1], 0);
             __syncwarp();
         } else if (warp == kLoadWarp && lane == 0) {
-            // ========================================================== loads: of a chunk V, its first Q, K, its other Q
-            uint32_t n = 0, h = 0;
-            // n counts chunks whose V is on its way, nk those whose K is
-            uint32_t nk = 0;
-            for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const Unit x = unit_of<STATES>(items, u, p);
-                for (int c = 0; ok && c < chunks_of(x.it.ntok); ++c) {
-                    const int t0 = x.it.tok0 + c * kChunk;
-                    auto load = [&](uint64_t* empty, uint64_t* full, uint32_t turn, int at, const CUtensorMap* map, int head) -> bool {
-                        if (!wait.one(empty, (turn & 1) ^ 1) || b->abort_flag) return ok = false;
-                        dev::mbar_arrive_expect_tx(full, L::kTile);
+            // ========================================================== loads: of a chunk V, its first Q, K (as two
+            // halves), its other Q
+            uint32_t n = 0, h = 0, kh = 0;  // loads begun: V, Q, halves of K
+            auto load = [&](uint64_t* empty, uint64_t* full, uint32_t turn, uint8_t* at, const CUtensorMap* map, int head, int t0,
+                            uint32_t bytes) -> bool {
+                if (!wait.one(empty, (turn & 1) ^ 1) || b->abort_flag) return ok = false;
+                dev::mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
-                        for (int i = 0; i < L::kHalves; ++i)
-                            tc::tma_load_3d(smem + at + i * kRegion, map, 64 * i, head, t0, full);
-                        return true;
-                    };
-                    if (!load(&b->v_empty[n & 1], &b->v_full[n & 1], n >> 1, L::kV + (n & 1) * L::kTile, &v_map, x.kvh)) break;
-                    ++n;
+                for (int i = 0; i < L::kHalves; ++i) tc::tma_load_3d(at + i * kRegion, map, 64 * i, head, t0, full);
+                return true;
+            };
+            for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
+                const Unit x = unit_of<STATES>(items, u, p, parts);
+                for (int c = 0; ok && c < chunks_of(x.it.ntok); ++c) {
+                    const int t0 = x.it.tok0 + c * kChunk, heads = x.g1 - x.g0;
 #pragma unroll 1
-                    for (int g = x.g0; ok && (g < x.g1 || nk < n); ++g) {
-                        if (g < x.g1) {
-                            if (!load(&b->q_empty[h & 1], &b->q_full[h & 1], h >> 1, L::kQ + (h & 1) * L::kTile, &q_map,
-                                      x.kvh * p.group + g))
-                                break;
-                            ++h;
-                        }
-                        if (nk < n) {
-                            if (!load(&b->k_empty[nk % KS], &b->k_full[nk % KS], nk / KS, L::kK + (nk % KS) * L::kTile, &k_map, x.kvh))
-                                break;
-                            ++nk;
+                    for (int i = 0; ok && i < heads + 3; ++i) {  // (0: V, 1: Q 0, 2 and 3: K, 4 ..: Q 1 ..)
+                        const int j = STATES && i > 0 ? i + 1 : i;
+                        if (j == 0) {
+                            n += load(&b->v_empty[n & 1], &b->v_full[n & 1], n >> 1, smem + L::kV + (n & 1) * L::kTile, &v_map, x.kvh,
+                                      t0, L::kTile);
+                        } else if (j == 2 || j == 3) {
+                            kh += load(&b->k_empty[kh % KH], &b->k_full[kh % KH], kh / KH,
+                                       smem + L::kK + (kh % KH / 2) * L::kTile + (kh & 1) * (kRegion / 2), &k_map, x.kvh,
+                                       t0 + 64 * (j - 2), L::kTile / 2);
+                        } else if (j < heads + 3) {
+                            h += load(&b->q_empty[h & 1], &b->q_full[h & 1], h >> 1, smem + L::kQ + (h & 1) * L::kTile, &q_map,
+                                      x.kvh * p.group + x.g0 + (j == 1 ? 0 : j - 3), t0, L::kTile);
                         }
                     }
                 }
             }
             // the last copies into every stage land before the CTA leaves
-            for (uint32_t s = 0; s < 2; ++s) {
-                if (n > s) (void)dev::mbar_wait(&b->v_full[(n - 1 - s) & 1], ((n - 1 - s) >> 1) & 1);
-                if (h > s) (void)dev::mbar_wait(&b->q_full[(h - 1 - s) & 1], ((h - 1 - s) >> 1) & 1);
-                if (s < KS && nk > s) (void)dev::mbar_wait(&b->k_full[(nk - 1 - s) % KS], ((nk - 1 - s) / KS) & 1);
+            for (uint32_t s = 0; s < 4; ++s) {
+                if (s < 2 && n > s) (void)dev::mbar_wait(&b->v_full[(n - 1 - s) & 1], ((n - 1 - s) >> 1) & 1);
+                if (s < 2 && h > s) (void)dev::mbar_wait(&b->q_full[(h - 1 - s) & 1], ((h - 1 - s) >> 1) & 1);
+                if (s < KH && kh > s) (void)dev::mbar_wait(&b->k_full[(kh - 1 - s) % KH], ((kh - 1 - s) / KH) & 1);
             }
         } else if (warp == kDecayWarp) {
             // ========================================================== sums of the log decays, four tokens a lane
             uint32_t n = 0;
             for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-                const Unit x = unit_of<STATES>(items, u, p);
+                const Unit x = unit_of<STATES>(items, u, p, parts);
                 const int nch = chunks_of(x.it.ntok);
                 double total = 0.0;  // of the unit
                 float g4[4];
@@ -489,20 +513,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const double end = __shfl_sync(0xffffffffu, y, 31);
                     const int st = n & 1;
                     if (!(ok = wait.warp(&b->dec_empty[st], ((n >> 1) & 1) ^ 1))) break;
-                    bool deep = false;
+                    float cf[4], least = INFINITY, most = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const double ci = before + sum[i];
-                        const float cf = (float)ci;
-                        b->c[st][4 * lane + i] = cf;
-                        b->f[st][4 * lane + i] = dev::fast_exp2(-cf);
-                        b->w[st][4 * lane + i] = c * kChunk + 4 * lane + i < x.it.ntok ? dev::fast_exp2((float)(end - ci)) : 0.f;
-                        deep |= !(fabsf(cf) <= kDeep);
+                        cf[i] = (float)(before + sum[i]);
+                        least = fminf(least, cf[i]), most = fmaxf(most, cf[i]);
+                        if (cf[i] != cf[i]) most = INFINITY;  // (a NaN: deep)
                     }
-                    deep = __any_sync(0xffffffffu, deep);
+#pragma unroll
+                    for (int d = 1; d < 32; d *= 2) {
+                        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                    }
+                    const float r = least >= -kReach && most <= kReach ? 0.f : rintf(-0.5f * (least + most));
+                    const bool deep = !(fabsf(r) <= kReach && -least - r <= kReach && -most - r >= -kReach);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        b->c[st][4 * lane + i] = cf[i];
+                        b->f[st][4 * lane + i] = dev::fast_exp2(-cf[i] - r);
+                        b->w[st][4 * lane + i] =
+                            c * kChunk + 4 * lane + i < x.it.ntok ? dev::fast_exp2((float)(end - (before + sum[i]))) : 0.f;
+                    }
                     if (lane == 0) {
                         b->end[st] = dev::fast_exp2((float)end);
                         b->deep[st] = deep;
+                        b->r[st] = deep ? 0.f : r;
+                        b->down[st] = deep ? 1.f : dev::fast_exp2(-r);
                     }
                     arrive_warp(&b->dec_full[st]);
                     total += end;
@@ -519,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r0 = (wq & 1) * 8 + (lane >> 3), cc = lane & 7;  // first token of a part's, 16-byte chunk of its row
         uint32_t n = 0;
         for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-            const int ntok = unit_of<STATES>(items, u, p).it.ntok;
+            const int ntok = unit_of<STATES>(items, u, p, parts).it.ntok;
             for (int c = 0; ok && c < chunks_of(ntok); ++c, ++n) {
                 const int st = n & 1, nval = min(kChunk, ntok - c * kChunk);
                 uint8_t* V = smem + L::kV + st * L::kTile;
@@ -550,59 +586,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (nval < kChunk) tc::fence_proxy_async_smem();
                     arrive_warp(&b->v_ok[st]);
                 }
-                if (!(ok = wait.warp(&b->k_full[n % KS], (n / KS) & 1) && wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
+                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
                 const uint8_t* K = smem + L::kK + (n % KS) * L::kTile;
 #pragma unroll 1
                 for (int s = pair; s < kParts; s += 4) {
+                    const uint32_t half = 2 * (n % KS) + (s >= 4);
+                    if (!(ok = wait.warp(&b->k_full[half], (n / KS) & 1))) break;
                     const int held = (int)(n * kParts + s) - L::kStagesW;  // the part that its stage held
-                    uint4 y[2][L::kHalves];
-                    float w[2];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int row = s * kPart + r0 + 4 * z;
-                        w[z] = b->w[st][row];
-#pragma unroll
-                        for (int x = 0; x < L::kHalves; ++x) {
-                            y[z][x] = *reinterpret_cast<const uint4*>(K + x * kRegion + row * 128 + (((cc ^ row) & 7) << 4));
-                            if (row >= nval) y[z][x] = make_uint4(0, 0, 0, 0);  // (whatever lies there times 0)
-                        }
-                    }
                     uint8_t* W = smem + L::kW + (s % L::kStagesW) * 3 * L::kSplit;
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
+                    for (int z = 0; z < 2 * L::kHalves; ++z) {  // two tokens, their row's halves
+                        const int x = z % L::kHalves, r = r0 + 4 * (z / L::kHalves), row = s * kPart + r;
+                        const float w = b->w[st][row];
+                        uint4 y = *reinterpret_cast<const uint4*>(K + x * kRegion + row * 128 + (((cc ^ row) & 7) << 4));
+                        if (row >= nval) y = make_uint4(0, 0, 0, 0);  // (whatever lies there times 0)
+                        const uint32_t e[4] = {y.x, y.y, y.z, y.w};
+                        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                        for (int x = 0; x < L::kHalves; ++x) {
-                            const uint32_t e[4] = {y[z][x].x, y[z][x].y, y[z][x].z, y[z][x].w};
-                            uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                // the upper 8 bits, the next 8 and the rest: each difference is exact (of an
-                                // infinity it is a NaN)
-                                float f0, f1, m0, m1, l0, l1;
-                                fmul2(f0, f1, lo_f32(e[q]), hi_f32(e[q]), w[z], w[z]);
-                                rest2(m0, m1, f0, f1);
-                                rest2(l0, l1, m0, m1);
-                                hi[q] = dev::prmt(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
-                                mid[q] = dev::prmt(__float_as_uint(m0), __float_as_uint(m1), 0x7632);
-                                lo[q] = dev::pack_bf16x2(l0, l1);
-                            }
-                            if (z == 0 && x == 0 && held >= 0 &&
-                                !(ok = wait.warp(&b->w_empty[held % kParts], (held / kParts) & 1)))
-                                break;
-                            const int r = r0 + 4 * z;
-                            uint8_t* at = W + x * kPartRegion + r * 128 + (((cc ^ r) & 7) << 4);
-                            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(at + L::kSplit) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                            *reinterpret_cast<uint4*>(at + 2 * L::kSplit) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int q = 0; q < 4; ++q) {
+                            // the upper 8 bits, the next 8 and the rest: each difference is exact (of an infinity it is
+                            // a NaN)
+                            float f0, f1, m0, m1, l0, l1;
+                            fmul2(f0, f1, lo_f32(e[q]), hi_f32(e[q]), w, w);
+                            rest2(m0, m1, f0, f1);
+                            rest2(l0, l1, m0, m1);
+                            hi[q] = dev::prmt(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
+                            mid[q] = dev::prmt(__float_as_uint(m0), __float_as_uint(m1), 0x7632);
+                            lo[q] = dev::pack_bf16x2(l0, l1);
                         }
-                        if (!ok) break;
+                        if (z == 0 && held >= 0 && !(ok = wait.warp(&b->w_empty[held % kParts], (held / kParts) & 1))) break;
+                        uint8_t* at = W + x * kPartRegion + r * 128 + (((cc ^ r) & 7) << 4);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(at + L::kSplit) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                        *reinterpret_cast<uint4*>(at + 2 * L::kSplit) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     if (!ok) break;
                     tc::fence_proxy_async_smem();
                     arrive_warp(&b->w_full[s]);
+                    if ((threadIdx.x & 31) == 0) dev::mbar_arrive(&b->k_empty[half]);
                 }
                 if (!ok) break;
-                arrive_warp(&b->k_empty[n % KS]);
                 arrive_warp(&b->dec_empty[st]);
             }
         }
@@ -615,58 +638,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t n = 0;
         const int64_t per_head = (int64_t)D * D;
         for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
-            const Unit un = unit_of<STATES>(items, u, p);
+            const Unit un = unit_of<STATES>(items, u, p, parts);
             const LinItem& it = un.it;
             const int nch = chunks_of(it.ntok);
             float S[D / 32][32];
 #pragma unroll
             for (int x = 0; x < D; ++x) S[x >> 5][x & 31] = 0.f;
-            auto slot = [&](int i) { return p.states + ((int64_t)i * Hkv + un.kvh) * per_head + row * D; };
-            auto segment_state = [&](int i) { return seg_state + ((int64_t)(it.base + i) * Hkv + un.kvh) * per_head + row * D; };
-            auto add = [&](const float* src, float f) {  // S <- f S + src
+            // a state slot of this warp's rows, to or from S: through shared memory, so that whole rows are read
+            // and written together (by each thread's own row a state took 4000 cycles)
+            auto move = [&](float* rows, bool in) {
+                constexpr int kCols = D / 2, kPer = kCols / 4;  // columns at a time, 16-byte chunks of those
+                // (in the warp's own rows of the bf16 copy: 4 KiB in each of its regions)
+                auto at = [&](int chunk) {
+                    return reinterpret_cast<float4*>(smem + L::kS + (chunk >> 8) * L::kStateRegion + (warp & 3) * 4096 + (chunk & 255) * 16);
+                };
+                rows += (int64_t)(warp & 3) * 32 * D;
 #pragma unroll
-                for (int x = 0; x < D; x += 4) {
-                    const float4 y = *reinterpret_cast<const float4*>(src + x);
-                    S[x >> 5][x & 31] = fmaf(f, S[x >> 5][x & 31], y.x);
-                    S[x >> 5][(x & 31) + 1] = fmaf(f, S[x >> 5][(x & 31) + 1], y.y);
-                    S[x >> 5][(x & 31) + 2] = fmaf(f, S[x >> 5][(x & 31) + 2], y.z);
-                    S[x >> 5][(x & 31) + 3] = fmaf(f, S[x >> 5][(x & 31) + 3], y.w);
+                for (int half = 0; half < 2; ++half) {
+                    auto own = [&](int q) { return at(lane * kPer + (q ^ (lane & 7))); };
+                    auto all = [&] {
+                        // (every load in flight before the first is used)
+                        float4 y[kPer];
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i) {
+                            const int r = (i * 32 + lane) / kPer, q = (i * 32 + lane) % kPer;
+                            y[i] = in ? *reinterpret_cast<const float4*>(rows + r * D + half * kCols + 4 * q) : *at(r * kPer + (q ^ (r & 7)));
+                        }
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i) {
+                            const int r = (i * 32 + lane) / kPer, q = (i * 32 + lane) % kPer;
+                            if (in) *at(r * kPer + (q ^ (r & 7))) = y[i];
+                            else *reinterpret_cast<float4*>(rows + r * D + half * kCols + 4 * q) = y[i];
+                        }
+                        __syncwarp();
+                    };
+                    if (in) all();
+#pragma unroll
+                    for (int q = 0; q < kPer; ++q) {
+                        float* x = &S[(half * kCols + 4 * q) >> 5][(half * kCols + 4 * q) & 31];
+                        if (in) {
+                            const float4 y = *own(q);
+                            x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+                        } else {
+                            *own(q) = make_float4(x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                    __syncwarp();
+                    if (!in) all();
                 }
             };
-            auto put = [&](float* dst) {
-#pragma unroll
-                for (int x = 0; x < D; x += 4)
-                    *reinterpret_cast<float4*>(dst + x) = make_float4(S[x >> 5][x & 31], S[x >> 5][(x & 31) + 1],
-                                                                      S[x >> 5][(x & 31) + 2], S[x >> 5][(x & 31) + 3]);
+            auto slot = [&](int i) { return p.states + ((int64_t)i * Hkv + un.kvh) * per_head; };
+            // states in the workspace: four columns of a row, then those of the next row
+            auto segment_state = [&](int i) {
+                return reinterpret_cast<float4*>(seg_state + ((int64_t)(it.base + i) * Hkv + un.kvh) * per_head) + row;
             };
             // The start.  Where other CTAs work on the same request and kv head it is a copy that the kernel before
             // has made: the one that ends with the request's last token may write the slot before the others have
-            // read it.  The states pass leaves the first segment's end from there, the others' from zero.
+            // read it.  The states pass leaves the first segment's end from there, the others' from zero, and the scan
+            // makes the request's state of each.
+            if (n > 0 && !STATES && !(ok = wait.warp(&b->s_empty, (n - 1) & 1))) break;
             if (live && (it.seg == 0 ? it.in >= 0 : !STATES)) {
-#pragma unroll 1
-                for (int i = it.seg == 0 ? 0 : 1; i <= it.seg; ++i)
-                    add(it.base >= 0 ? segment_state(i) : slot(it.in), i > 1 ? seg_decay[(int64_t)(it.base + i) * Hkv + un.kvh] : 0.f);
+                if (it.base < 0) {
+                    move(slot(it.in), true);
+                } else {
+                    const float4* src = segment_state(it.seg);
+#pragma unroll
+                    for (int x = 0; x < D; x += 4) {
+                        const float4 y = src[x / 4 * D];
+                        float* z = &S[x >> 5][x & 31];
+                        z[0] = y.x, z[1] = y.y, z[2] = y.z, z[3] = y.w;
+                    }
+                }
             }
             for (int c = 0; ok && c < nch; ++c, ++n) {
                 const int st = n & 1;
+                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
+                const float end = b->end[st], down = b->down[st];
+                arrive_warp(&b->dec_empty[st]);
                 if constexpr (!STATES) {
-                    if (n > 0 && !(ok = wait.warp(&b->s_empty, (n - 1) & 1))) break;
+                    if (c > 0 && !(ok = wait.warp(&b->s_empty, (n - 1) & 1))) break;
                     if (live) {
 #pragma unroll
                         for (int x = 0; x < D; x += 8) {
-                            const float* y = &S[x >> 5][x & 31];
-                            const uint32_t at = dev::smem_u32(smem + L::kS) + (x >> 6) * L::kStateRegion + row * 128 +
-                                                ((((x >> 3) ^ row) & 7) << 4);
-                            dev::st_shared_v4(at, dev::pack_bf16x2(y[0], y[1]), dev::pack_bf16x2(y[2], y[3]),
-                                              dev::pack_bf16x2(y[4], y[5]), dev::pack_bf16x2(y[6], y[7]));
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float y0, y1;
+                                fmul2(y0, y1, S[x >> 5][(x & 31) + 2 * i], S[x >> 5][(x & 31) + 2 * i + 1], down, down);
+                                w[i] = dev::pack_bf16x2(y0, y1);
+                            }
+                            dev::st_shared_v4(dev::smem_u32(smem + L::kS) + (x >> 6) * L::kStateRegion + row * 128 +
+                                                  ((((x >> 3) ^ row) & 7) << 4), w[0], w[1], w[2], w[3]);
                         }
                     }
                     tc::fence_proxy_async_smem();
                     arrive_warp(&b->s_full);
                 }
-                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
-                const float end = b->end[st];
-                arrive_warp(&b->dec_empty[st]);
                 if (!(ok = wait.warp(&b->ds_full, n & 1))) break;
                 tc::fence_after_sync();
 #pragma unroll
@@ -683,8 +750,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 arrive_warp(&b->ds_free);
             }
-            if (ok && live && (STATES || (it.out >= 0 && it.seg == it.nseg - 1 && un.g0 == 0)))
-                put(STATES ? segment_state(it.seg + 1) : slot(it.out));
+            if (!ok || !live) continue;
+            if constexpr (STATES) {
+                float4* dst = segment_state(it.seg + 1);
+#pragma unroll
+                for (int x = 0; x < D; x += 4) {
+                    const float* z = &S[x >> 5][x & 31];
+                    dst[x / 4 * D] = make_float4(z[0], z[1], z[2], z[3]);
+                }
+            } else if (it.out >= 0 && it.seg == it.nseg - 1 && un.g0 == 0) {
+                if (!(ok = wait.warp(&b->s_empty, (n - 1) & 1))) break;
+                move(slot(it.out), false);
+            }
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsP));  // (in the states pass too: the split counts on it)
@@ -694,37 +771,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
         const uint32_t t_o = tmem + kColO + lane_base;
         uint32_t n = 0, h = 0;
-        // the head whose O is still to be written: where to (null: none of this row), and its factor
+        // the head whose O is still to be written: its first token, how many, and the factor of this row
         bool pending = false;
-        uint16_t* o_dst = nullptr;
+        int o_tok = 0, o_left = 0, o_head = 0;
         float o_factor = 0.f;
-        auto write_o = [&]() -> bool {  // of head h - 1
+        // O of head h - 1.  Four lanes turn 4 x 4 chunks of 16 bytes among them, so that a row's 64 bytes go out together
+        // (by each thread's own row, 16 bytes at a time, it took 3800 cycles).
+        auto write_o = [&]() -> bool {
             if (!wait.warp(&b->o_ready, (h - 1) & 1)) return false;
             tc::fence_after_sync();
-            float o[2][32];
-            tc::tmem_ld32_async(t_o, o[0]);
-#pragma unroll
+            const int first = row & ~3;
+            uint16_t* dst = p.out + ((int64_t)(o_tok + first) * p.num_qo_heads + o_head) * D + 8 * (lane & 3);
+            const int64_t step = (int64_t)p.num_qo_heads * D;
+#pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
-                tc::tmem_wait_ld_regs(o[x & 1]);
-                if (x + 1 < D / 32) {
-                    tc::tmem_ld32_async(t_o + 32 * (x + 1), o[(x + 1) & 1]);
-                } else {
+                float o[32];
+                tc::tmem_ld32_async(t_o + 32 * x, o);
+                tc::tmem_wait_ld_regs(o);
+                if (x == D / 32 - 1) {
                     tc::fence_before_sync();
                     arrive_warp(&b->o_free);
                 }
+                uint32_t w[4][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float y0, y1;
-                        fmul2(y0, y1, o[x & 1][8 * e + 2 * i], o[x & 1][8 * e + 2 * i + 1], o_factor, o_factor);
-                        w[i] = dev::pack_bf16x2(y0, y1);
-                    }
-                    if (o_dst != nullptr) reinterpret_cast<uint4*>(o_dst)[4 * x + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 16; ++i) {
+                    float y0, y1;
+                    fmul2(y0, y1, o[2 * i], o[2 * i + 1], o_factor, o_factor);
+                    w[i >> 2][i & 3] = dev::pack_bf16x2(y0, y1);
                 }
+#pragma unroll
+                for (int m = 1; m <= 2; m *= 2) {
+                    const bool up = (lane & m) != 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e & m) continue;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[e][i] : w[e | m][i], m);
+                            if (up) w[e][i] = got;
+                            else w[e | m][i] = got;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (first + e < o_left)
+                        *reinterpret_cast<uint4*>(dst + e * step + 32 * x) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+                __syncwarp();
             }
-            __syncwarp();
             return true;
         };
         // a head after the other: its unit, its chunk's sums and flags
@@ -741,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int u = unit_at(k++, n_units);
                     last = u < 0;
                     if (!last) {
-                        const Unit un = unit_of<STATES>(items, u, p);
+                        const Unit un = unit_of<STATES>(items, u, p, parts);
                         tok = un.it.tok0, left = un.it.ntok, head0 = un.kvh * p.group + un.g0, heads = un.g1 - un.g0;
                     }
                 }
@@ -749,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g = 0, st = n & 1;
                     if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1) && wait.warp(&b->v_ok[st], (n >> 1) & 1))) break;
                     bad = v_is_bad(b, st), deep = b->deep[st] != 0;
-                    ci = b->c[st][row], ri = fminf(fmaxf(ci, -kDeep), kDeep);
+                    ci = b->c[st][row], ri = deep ? fminf(fmaxf(ci, -kDeep), kDeep) : ci + b->r[st];
                 }
             }
             // this head's weights and, behind them, the head before's O: before them if they are late, or need O
@@ -805,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (bad || (deep && __any_sync(0xffffffffu, up != 0.f))) {
                         if (!(ok = wait.warp(&b->qs_full, h & 1))) break;
                         tc::fence_after_sync();
-                        finish_rows<D>(t_o, t_p, smem + L::kV + st * L::kTile, row, dev::fast_exp2(up), bad);
+                        finish_rows<D>(t_o, t_p, smem + L::kV + st * L::kTile, row, deep ? dev::fast_exp2(up) : 1.f, bad);
                     }
                     tc::fence_before_sync();
                     arrive_warp(&b->p_ready[h & 1]);
@@ -814,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok || last) break;
             pending = true;
             o_factor = p.scale * dev::fast_exp2(ri);
-            o_dst = row < left ? p.out + ((int64_t)(tok + row) * p.num_qo_heads + head0 + g) * D : nullptr;
+            o_tok = tok, o_left = left, o_head = head0 + g;
             ++g, ++h;
         }
         }
@@ -850,13 +944,13 @@ EncodeTiledFn tensor_map_encoder() {
     return fn;
 }
 
-// [T, heads, D] with ld elements between tokens; a box is 64 columns of one head for 128 tokens.
-bool encode(CUtensorMap* m, const uint16_t* x, int64_t tokens, int heads, int D, int64_t ld) {
+// [T, heads, D] with ld elements between tokens; a box is 64 columns of one head for so many tokens.
+bool encode(CUtensorMap* m, const uint16_t* x, int64_t tokens, int heads, int D, int64_t ld, int rows) {
     const EncodeTiledFn enc = tensor_map_encoder();
     if (enc == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kChunk};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     const cuuint32_t elem_strides[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(x), dims, strides, box, elem_strides,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -881,9 +975,9 @@ cudaError_t launch(const LinParams& p, int ctas, cudaStream_t s) {
     }
     if (launch_regs.load(std::memory_order_relaxed) != kRegsLaunch) return cudaErrorInvalidConfiguration;
     CUtensorMap q, k, v;
-    if (!encode(&q, p.q, p.total_tokens, p.num_qo_heads, D, p.ld_q) ||
-        !encode(&k, p.k, p.total_tokens, p.num_kv_heads, D, p.ld_k) ||
-        !encode(&v, p.v, p.total_tokens, p.num_kv_heads, D, p.ld_v))
+    if (!encode(&q, p.q, p.total_tokens, p.num_qo_heads, D, p.ld_q, kChunk) ||
+        !encode(&k, p.k, p.total_tokens, p.num_kv_heads, D, p.ld_k, kChunk / 2) ||
+        !encode(&v, p.v, p.total_tokens, p.num_kv_heads, D, p.ld_v, kChunk))
         return cudaErrorInvalidValue;
     return launch_programmatic(kernel, dim3((unsigned)ctas), (unsigned)kThreads, smem, s, p, q, k, v);
 }

@@ -108,11 +108,13 @@ def test_against_the_recurrence(heads, gate, lens):
 @pytest.mark.parametrize("heads", [(4, 2, 128), (2, 2, 64)], ids=["128", "64"])
 @pytest.mark.parametrize("where", [("v", 200), ("v", 3), ("k", 200), ("q", 150), ("g", 210)], ids=lambda w: f"{w[0]}{w[1]}")
 @pytest.mark.parametrize("value", [float("nan"), float("inf")], ids=["nan", "inf"])
-def test_hidden_infinities_and_nan(heads, where, value):
+@pytest.mark.parametrize("fast", [0.0, 0.6, 2.0])
+def test_hidden_infinities_and_nan(heads, where, value, fast):
     """An infinity or a NaN in one token's v, k, q or decay changes no token before it, no other request, and
     of the tokens after it (in v's case) only the columns that it lies in."""
     lens, cached = [300, 130, 9], [5, 0, 2]
     c = Case(heads, lens, cached, gate="token", seed=3)
+    c.log_decay[:, 1] -= fast       # (chunks whose sums go further than one power for all rows reaches, or not)
     was, want = c.run()
     after, gates = c.states.clone(), c.log_decay.clone()
     ref, _, mag, _ = R.attend(c.q, c.k, c.v, c.log_decay, c.starts(was), lens)
@@ -138,7 +140,7 @@ def test_hidden_infinities_and_nan(heads, where, value):
     lim = R.out_limit(ref, mag, gates, lens)
     assert bool(((out.double() - ref).abs() <= lim)[~odd].all())
     assert torch.equal(out[300:], want[300:]) and torch.equal(out[:128 * (t // 128)], want[:128 * (t // 128)])
-    if name == "v":                # it stays in every later token's sum
+    if name == "v" and fast == 0:   # it stays in every later token's sum
         assert bool(bad[t:300, G:2 * G, 7].all())
     same = torch.ones(c.num_states, dtype=torch.bool, device=DEV)
     same[int(c.state_out[0])] = False
