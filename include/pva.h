@@ -452,11 +452,12 @@ typedef struct pva_linear_args {
 } pva_linear_args;
 
 /*
- * Once per layer.  q, k, v: bf16 [T, heads, D], 16-byte aligned; out: bf16 [T, Hq, D], contiguous, outside the
- * memory of q, k, v, the decays and the states.  Requests of up to 16 new tokens run the recurrence as it stands,
+ * Once per layer.  q, k, v: bf16 [T, heads, D], 16-byte aligned; out: bf16 [T, Hq, D], contiguous; out and the
+ * states lie outside each other's memory and that of q, k, v and the decays.  Requests of up to 16 new tokens run the recurrence as it stands,
  * in fp32; longer ones in chunks of 128 tokens on the tensor cores, where the weights within a chunk and a copy
  * of the state enter the products as bf16 (out moves by about half a bf16 step of its terms; the states keep
- * fp32's accuracy).  Tokens hidden by causality have no part in a token's output, whatever they hold.
+ * fp32's accuracy).  Tokens hidden by causality have no part in a token's output, whatever they hold; an
+ * infinity in k may reach the outputs and states that see it as a NaN.
  */
 PVA_API pva_status attn_linear_forward(const pva_meta* meta, const pva_linear_args* args, const void* q, const void* k,
                                const void* v, void* out, void* stream);

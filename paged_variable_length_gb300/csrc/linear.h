@@ -14,11 +14,15 @@
 
 namespace pva {
 
-constexpr int kStepTokens = 16;   // most new tokens of a request that runs token by token
 constexpr int kChunk = 128;       // tokens of a tensor-core chunk
 constexpr uint32_t kErrState = PVA_DEVERR_STATE;
 // Log decays below this are taken as this: e^-110 is 0 in fp32, and -inf - -inf is never formed.
 constexpr float kLeastLogDecay = -110.f;
+
+// Most new tokens of a request that runs token by token, between the lengths where the tensor cores catch up: 11 tokens
+// of 64 requests of 32/8 heads of 128 (9 tokens 53 us for 63, 16 tokens 90 for 63), 15 of one such (12.8 us), 23 of
+// 64 requests of 16/16 heads of 64 (16 tokens 33 us for 44, 24 tokens 46).  Their results keep fp32's accuracy.
+constexpr int kStepTokens = 16;
 
 // A segment of a long request: tokens tok0 .. tok0 + ntok - 1.
 struct LinItem {
@@ -34,11 +38,11 @@ struct LinItem {
 static_assert(sizeof(LinItem) == 32, "LinItem is one 32-byte record");
 
 // Tokens of a segment.  A long request is cut where its batch's heads and requests alone would leave SMs idle: the
-// long requests' tokens dealt out evenly to as many segments as there are SMs for a kv head each, kLeastSegment
-// at least.  A cut costs a first pass over K and V (about a third of the whole), so a request that is not longer
-// than two such shares stays whole: 8 prompts of 256-4096 tokens and 32 heads take 208 us cut at one share and 175
-// whole, one of 16001 tokens and 8 kv heads 1545 us whole and 126 cut.
-constexpr int kLeastSegment = 256;
+// long requests' tokens dealt out evenly to as many segments as there are SMs for a kv head each, a chunk at least
+// (with two at least a prompt of 700 tokens, 16/1 heads, took 29 us for 23, two of 750-1500, 28/4 heads, 43 for 38,
+// though two of 150-300 22 for 25).  A cut costs a first pass over K and V (about a third of the whole), so a request
+// that is not longer than two such shares stays whole: 8 prompts of 256-4096 tokens and 32 heads took 208 us cut at
+// one share and 175 whole, one of 16001 tokens and 8 kv heads 1545 us whole and 126 cut.
 constexpr int kWholeSegment = 1 << 30;
 #ifdef __CUDACC__
 __host__ __device__
@@ -46,7 +50,7 @@ __host__ __device__
 inline int segment_share(int64_t long_tokens, int kv_heads, int sms) {
     const int64_t segments = sms / kv_heads > 0 ? sms / kv_heads : 1;
     const int64_t n = ((long_tokens + segments - 1) / segments + kChunk - 1) / kChunk * kChunk;
-    return n < kLeastSegment ? kLeastSegment : n < kWholeSegment ? (int)n : kWholeSegment;
+    return n < kChunk ? kChunk : n < kWholeSegment ? (int)n : kWholeSegment;
 }
 #ifdef __CUDACC__
 __host__ __device__

@@ -145,14 +145,15 @@ pva_status check_linear(const LinHost* h, const pva_linear_args* a, const void* 
         (reinterpret_cast<uintptr_t>(a->log_decay) & 3u) != 0)
         return PVA_ERR_INVALID_ARG;
     if (T == 0) return PVA_OK;
-    // rows of q, k, v and states are read while others' results are written
-    const Span o = span_of(out, T, rq, rq);
+    // rows of q, k, v and states are read while others' results, out's and the states', are written
+    const Span o = span_of(out, T, rq, rq), sq = span_of(q, T, ld_q, rq), sk = span_of(k, T, ld_k, rk), sv = span_of(v, T, ld_v, rk);
     const int64_t decays = a->ld_decay ? (T - 1) * a->ld_decay + h->cfg.num_kv_heads : h->cfg.num_kv_heads;
     const uintptr_t g = reinterpret_cast<uintptr_t>(a->log_decay), st = reinterpret_cast<uintptr_t>(a->states);
     const Span states{st, st + (uintptr_t)(h->cfg.num_states * h->cfg.num_kv_heads * D * D * 4)};
-    if (meet(o, span_of(q, T, ld_q, rq)) || meet(o, span_of(k, T, ld_k, rk)) || meet(o, span_of(v, T, ld_v, rk)) ||
-        meet(o, Span{g, g + (uintptr_t)(decays * 4)}) || meet(o, states))
-        return PVA_ERR_INVALID_ARG;
+    const Span sg{g, g + (uintptr_t)(decays * 4)};
+    if (meet(o, states)) return PVA_ERR_INVALID_ARG;
+    for (const Span& x : {sq, sk, sv, sg})
+        if (meet(o, x) || meet(states, x)) return PVA_ERR_INVALID_ARG;
     return PVA_OK;
 }
 
