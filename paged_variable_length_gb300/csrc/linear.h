@@ -44,6 +44,7 @@ static_assert(sizeof(LinItem) == 32, "LinItem is one 32-byte record");
 // that is not longer than two such shares stays whole: 8 prompts of 256-4096 tokens and 32 heads took 208 us cut at
 // one share and 175 whole, one of 16001 tokens and 8 kv heads 1545 us whole and 126 cut.
 constexpr int kWholeSegment = 1 << 30;
+constexpr int kWholeTokens = 4 * kChunk;
 #ifdef __CUDACC__
 __host__ __device__
 #endif
@@ -57,7 +58,7 @@ __host__ __device__
 #endif
 inline int segment_tokens(int64_t long_tokens, int longest, int kv_heads, int sms) {
     const int n = segment_share(long_tokens, kv_heads, sms);
-    return longest <= 2 * (int64_t)n ? kWholeSegment : n;
+    return longest <= 2 * (int64_t)n || longest <= kWholeTokens ? kWholeSegment : n;
 }
 
 // CTAs that share a kv head's q heads (two heads or more each), where the segments' kv heads are fewer than the SMs.

@@ -8,11 +8,12 @@
 // another, with the state in the registers of a warpgroup (fp32, a row of S a thread) and every product's
 // accumulator in TMEM (two of Q K^T, so that the next head's runs while this one's weights are made):
 //   warps 0-3    P: a row of Q K^T a thread, times e^{-c_j - r} up to the diagonal, to bf16 in TMEM (the A
-//                operand of P V, which adds to Q S); then the row of O, times scale e^{c_i + r}, to bf16 in HBM;
+//                operand of P V, which adds to Q S);
 //   warps 4-7    S <- e^{c_end} S + (w K)^T V, and e^{-r} S as bf16 in shared memory for the next chunk's Q S;
-//   warps 8-15   w K, as three bf16 parts that together hold all 24 bits of the fp32 product (so that the
+//   warps 8-11   w K, as three bf16 parts that together hold all 24 bits of the fp32 product (so that the
 //                fp32 state keeps its own), 16 tokens at a time; also zero the rows of V behind the request's
 //                last token, and note whether V holds an infinity or a NaN;
+//   warps 12-15  the rows of O, times scale e^{c_i + r}, to bf16 in HBM (in the states pass w K too);
 //   warp 16      issues the MMAs of the outputs, warp 17 the state's; warp 18 loads Q, K and V (TMA, 128-byte
 //                swizzle); warp 19 sums the decays (in 64 bits: differences of far sums keep their bits).
 // Roundings to bf16: P and the copy of S, each half a step of the term it scales; out.
@@ -46,9 +47,10 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kMmaWarp = 16, kStateMmaWarp = 17, kLoadWarp = 18, kDecayWarp = 19;
 // Registers a thread: launched with 96, the state's warpgroup rises to what the others give away
-// (88 + 184 + 2 x 64 + 80 = 5 x 96, so the increase never waits for registers that are not there).
-constexpr int kRegsLaunch = 96, kRegsP = 88, kRegsState = 184, kRegsScale = 64, kRegsCtrl = 80;
-static_assert(kRegsP + kRegsState + 2 * kRegsScale + kRegsCtrl == 5 * kRegsLaunch, "register split must balance");
+// (72 + 184 + 64 + 80 + 80 = 5 x 96, so the increase never waits for registers that are not there).
+constexpr int kRegsLaunch = 96, kRegsP = 72, kRegsState = 184, kRegsScale = 64, kRegsO = 80, kRegsCtrl = 80;
+static_assert(kRegsP + kRegsState + kRegsScale + kRegsO + kRegsCtrl == 5 * kRegsLaunch && kRegsScale <= kRegsO,
+              "register split must balance");
 constexpr int kRegion = kChunk * 128;  // 128 rows of 128 bytes (64 bf16 columns), swizzled
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColP = 0, kColO = 256, kColState = 384;  // TMEM columns (two buffers of Q K^T)
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using L = SmemMap<D, STATES>;
     constexpr uint32_t KH = L::kHalvesK, KS = KH / 2;
+    constexpr int kScaleWarps = STATES ? 8 : 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Bars bars;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&b->q_empty[s], 1);
             dev::mbar_init(&b->v_full[s], 1);
             dev::mbar_init(&b->v_empty[s], STATES ? 1 : 2);
-            dev::mbar_init(&b->v_ok[s], 8);
+            dev::mbar_init(&b->v_ok[s], kScaleWarps);
             dev::mbar_init(&b->p_full[s], 1);
             dev::mbar_init(&b->p_ready[s], 4);
             dev::mbar_init(&b->dec_full[s], 1);
@@ -547,10 +550,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                     seg_decay[(int64_t)(x.it.base + x.it.seg + 1) * Hkv + x.kvh] = exp2f((float)total);
             }
         }
+    } else if (!STATES && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsO));
+        if constexpr (!STATES) {
+        // ============================================================== O to memory, a row a thread
+        const int row = threadIdx.x - 384, first = row & ~3;
+        const uint32_t t_o = tmem + kColO + ((uint32_t)((warp & 3) * 32) << 16);
+        const int64_t step = (int64_t)p.num_qo_heads * D;
+        uint32_t n = 0, h = 0;
+        for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
+            const Unit un = unit_of<STATES>(items, u, p, parts);
+            for (int tok = un.it.tok0, left = un.it.ntok; ok && left > 0; ++n, tok += kChunk, left -= kChunk) {
+                const int st = n & 1;
+                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
+                const float ci = b->c[st][row];
+                const float factor = p.scale * dev::fast_exp2(b->deep[st] != 0 ? fminf(fmaxf(ci, -kDeep), kDeep) : ci + b->r[st]);
+                arrive_warp(&b->dec_empty[st]);
+                // (four lanes turn 4 x 4 chunks of 16 bytes among them, so that a row's 64 bytes go out together: by each
+                // thread's own row, 16 bytes at a time, it took 3800 cycles)
+                uint16_t* dst = p.out + ((int64_t)(tok + first) * p.num_qo_heads + un.kvh * p.group + un.g0) * D + 8 * (lane & 3);
+                for (int g = un.g0; g < un.g1; ++g, ++h, dst += D) {
+                    if (!(ok = wait.warp(&b->o_ready, h & 1))) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int x = 0; x < D / 32; ++x) {
+                        float o[32];
+                        tc::tmem_ld32_async(t_o + 32 * x, o);
+                        tc::tmem_wait_ld_regs(o);
+                        if (x == D / 32 - 1) {
+                            tc::fence_before_sync();
+                            arrive_warp(&b->o_free);
+                        }
+                        uint32_t w[4][4];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float y0, y1;
+                            fmul2(y0, y1, o[2 * i], o[2 * i + 1], factor, factor);
+                            w[i >> 2][i & 3] = dev::pack_bf16x2(y0, y1);
+                        }
+#pragma unroll
+                        for (int m = 1; m <= 2; m *= 2) {
+                            const bool up = (lane & m) != 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (e & m) continue;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[e][i] : w[e | m][i], m);
+                                    if (up) w[e][i] = got;
+                                    else w[e | m][i] = got;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (first + e < left)
+                                *reinterpret_cast<uint4*>(dst + e * step + 32 * x) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScale));
         // ============================================================== w K in three bf16 parts; a look at V
-        // Two warps make a part of 16 tokens: pair i (of four) the parts i and i + 4.
+        // Two warps make a part of 16 tokens: pair i the parts i, i + kScaleWarps / 2 and so on.
         const int wq = warp - 8, pair = wq >> 1;
         const int r0 = (wq & 1) * 8 + (lane >> 3), cc = lane & 7;  // first token of a part's, 16-byte chunk of its row
         uint32_t n = 0;
@@ -560,8 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = n & 1, nval = min(kChunk, ntok - c * kChunk);
                 uint8_t* V = smem + L::kV + st * L::kTile;
                 if (!(ok = wait.warp(&b->v_full[st], (n >> 1) & 1))) break;
-                {   // half a row of V a lane (D 64: a quarter of one in either half)
-                    const int row = wq * 16 + (lane >> 1);
+#pragma unroll 1
+                for (int x0 = wq; x0 < 8; x0 += kScaleWarps) {  // half a row of V a lane (D 64: a quarter of one in either half)
+                    const int row = x0 * 16 + (lane >> 1);
                     constexpr int kEach = D / 16;
                     uint4* at[kEach];
 #pragma unroll
@@ -582,14 +648,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < kEach; ++x) *at[x] = make_uint4(0, 0, 0, 0);
                     }
                     const int any = __any_sync(0xffffffffu, is_odd(odd));
-                    if (lane == 0) b->v_bad[st][wq] = any;
-                    if (nval < kChunk) tc::fence_proxy_async_smem();
-                    arrive_warp(&b->v_ok[st]);
+                    if (lane == 0) b->v_bad[st][x0] = any;
                 }
+                if (nval < kChunk) tc::fence_proxy_async_smem();
+                arrive_warp(&b->v_ok[st]);
                 if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
                 const uint8_t* K = smem + L::kK + (n % KS) * L::kTile;
 #pragma unroll 1
-                for (int s = pair; s < kParts; s += 4) {
+                for (int s = pair; s < kParts; s += kScaleWarps / 2) {
                     const uint32_t half = 2 * (n % KS) + (s >= 4);
                     if (!(ok = wait.warp(&b->k_full[half], (n / KS) & 1))) break;
                     const int held = (int)(n * kParts + s) - L::kStagesW;  // the part that its stage held
@@ -766,101 +832,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsP));  // (in the states pass too: the split counts on it)
         if constexpr (!STATES) {
-        // ============================================================== P and O, a row a thread
+        // ============================================================== P, a row a thread
         const int row = threadIdx.x;
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const uint32_t t_o = tmem + kColO + lane_base;
         uint32_t n = 0, h = 0;
-        // the head whose O is still to be written: its first token, how many, and the factor of this row
-        bool pending = false;
-        int o_tok = 0, o_left = 0, o_head = 0;
-        float o_factor = 0.f;
-        // O of head h - 1.  Four lanes turn 4 x 4 chunks of 16 bytes among them, so that a row's 64 bytes go out together
-        // (by each thread's own row, 16 bytes at a time, it took 3800 cycles).
-        auto write_o = [&]() -> bool {
-            if (!wait.warp(&b->o_ready, (h - 1) & 1)) return false;
-            tc::fence_after_sync();
-            const int first = row & ~3;
-            uint16_t* dst = p.out + ((int64_t)(o_tok + first) * p.num_qo_heads + o_head) * D + 8 * (lane & 3);
-            const int64_t step = (int64_t)p.num_qo_heads * D;
-#pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
-                float o[32];
-                tc::tmem_ld32_async(t_o + 32 * x, o);
-                tc::tmem_wait_ld_regs(o);
-                if (x == D / 32 - 1) {
-                    tc::fence_before_sync();
-                    arrive_warp(&b->o_free);
-                }
-                uint32_t w[4][4];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float y0, y1;
-                    fmul2(y0, y1, o[2 * i], o[2 * i + 1], o_factor, o_factor);
-                    w[i >> 2][i & 3] = dev::pack_bf16x2(y0, y1);
-                }
-#pragma unroll
-                for (int m = 1; m <= 2; m *= 2) {
-                    const bool up = (lane & m) != 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (e & m) continue;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[e][i] : w[e | m][i], m);
-                            if (up) w[e][i] = got;
-                            else w[e | m][i] = got;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (first + e < o_left)
-                        *reinterpret_cast<uint4*>(dst + e * step + 32 * x) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
-                __syncwarp();
-            }
-            return true;
-        };
-        // a head after the other: its unit, its chunk's sums and flags
-        int k = 0, tok = 0, left = 0, head0 = 0, heads = 0, g = 0, st = 0;  // tokens: the chunk's first, the unit's left
-        bool bad = false, deep = false, last = false;
-        float ci = 0.f, ri = 0.f;
-        while (true) {
-            if (g == heads) {  // the next chunk
-                if (h > 0) {
-                    arrive_warp(&b->dec_empty[st]);
-                    ++n, tok += kChunk, left -= kChunk;
-                }
-                if (left <= 0) {
-                    const int u = unit_at(k++, n_units);
-                    last = u < 0;
-                    if (!last) {
-                        const Unit un = unit_of<STATES>(items, u, p, parts);
-                        tok = un.it.tok0, left = un.it.ntok, head0 = un.kvh * p.group + un.g0, heads = un.g1 - un.g0;
-                    }
-                }
-                if (!last) {
-                    g = 0, st = n & 1;
-                    if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1) && wait.warp(&b->v_ok[st], (n >> 1) & 1))) break;
-                    bad = v_is_bad(b, st), deep = b->deep[st] != 0;
-                    ci = b->c[st][row], ri = deep ? fminf(fmaxf(ci, -kDeep), kDeep) : ci + b->r[st];
-                }
-            }
-            // this head's weights and, behind them, the head before's O: before them if they are late, or need O
-            // themselves
-            const bool o_first = pending && (last || deep || bad || !seen_warp(&b->p_full[h & 1], (h >> 1) & 1));
-#pragma unroll 1
-            for (int step = 0; ok && step < 2; ++step) {
-                if ((step == 0) == o_first) {
-                    if (pending) ok = write_o();
-                } else if (!last) {
+        for (int k = 0, u; ok && (u = unit_at(k, n_units)) >= 0; ++k) {
+            const Unit un = unit_of<STATES>(items, u, p, parts);
+            const int nch = chunks_of(un.it.ntok);
+            for (int c = 0; ok && c < nch; ++c, ++n) {
+                const int st = n & 1;
+                if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1) && wait.warp(&b->v_ok[st], (n >> 1) & 1))) break;
+                const bool bad = v_is_bad(b, st), deep = b->deep[st] != 0;
+                const float ci = b->c[st][row], up = deep ? ci - fminf(fmaxf(ci, -kDeep), kDeep) : 0.f;
+                const float* other = deep ? b->c[st] : b->f[st];
+                for (int g = un.g0; g < un.g1; ++g, ++h) {
                     const uint32_t t_p = tmem + kColP + 128 * (h & 1) + lane_base;
                     if (!(ok = wait.warp(&b->p_full[h & 1], (h >> 1) & 1))) break;
                     tc::fence_after_sync();
                     // 32 keys at a time; those past the warp's own rows have no weight.  (The packed weights of
                     // block x lie in columns 16 x .. of the scores, which are read by then.)
-                    const float up = ci - ri;
-                    const float* other = deep ? b->c[st] : b->f[st];
 #pragma unroll 1
                     for (int x = 0; x < kChunk / 32; ++x) {
                         uint32_t pk[16];
@@ -899,17 +889,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (bad || (deep && __any_sync(0xffffffffu, up != 0.f))) {
                         if (!(ok = wait.warp(&b->qs_full, h & 1))) break;
                         tc::fence_after_sync();
-                        finish_rows<D>(t_o, t_p, smem + L::kV + st * L::kTile, row, deep ? dev::fast_exp2(up) : 1.f, bad);
+                        finish_rows<D>(tmem + kColO + lane_base, t_p, smem + L::kV + st * L::kTile, row,
+                                       deep ? dev::fast_exp2(up) : 1.f, bad);
                     }
                     tc::fence_before_sync();
                     arrive_warp(&b->p_ready[h & 1]);
                 }
+                if (ok) arrive_warp(&b->dec_empty[st]);
             }
-            if (!ok || last) break;
-            pending = true;
-            o_factor = p.scale * dev::fast_exp2(ri);
-            o_tok = tok, o_left = left, o_head = head0 + g;
-            ++g, ++h;
         }
         }
     }

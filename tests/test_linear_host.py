@@ -70,6 +70,27 @@ def test_prepare_refuses_on_the_host(lib):
         assert prepare(**kw) == 1, kw
 
 
+def test_what_the_binding_of_prepare_refuses(lib):
+    cfg, batch = pva.make_linear_config(8, 2, 64, 10, 4, 64), 3
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    room = torch.empty(1024, dtype=torch.uint8)
+    room = room[-room.data_ptr() % 256:]
+
+    def prepare(**kw):
+        a = {**dict(cu=i32(batch + 1), lens=i32(batch), ins=i32(batch), outs=i32(batch)), **kw}
+        try:
+            pva.attn_linear_prepare(cfg, a["cu"], a["lens"], a["ins"], a["outs"], batch, 9, 0,
+                                    room, stream=0)
+        except pva.PvaError as e:
+            return e.status
+        return 0
+
+    assert prepare() != 1 and prepare(ins=None, outs=None) != 1      # (no device, or the workspace is too small)
+    for name, n in (("cu", batch + 1), ("lens", batch), ("ins", batch), ("outs", batch)):
+        for bad in (i32(n - 1), i32(n).long(), i32(2 * n)[::2], i32(n).float()):
+            assert prepare(**{name: bad}) == 1, name
+
+
 T, HQ, HKV, D = 5, 4, 2, 64
 
 
