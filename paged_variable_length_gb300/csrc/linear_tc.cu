@@ -83,7 +83,7 @@ struct SmemMap {
 
 struct Bars {
     uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[2], v_empty[2], v_ok[2];
-    uint64_t p_full[2], p_ready[2], qs_full, o_ready, o_free;
+    uint64_t p_full[2], p_ready[2], qs_full[2], o_ready, o_free;
     uint64_t w_full[kParts], w_empty[kParts], ds_full, ds_free, s_full, s_empty;
     uint64_t dec_full[2], dec_empty[2], drain[2];
     alignas(16) float c[2][kChunk];  // sums of the log decays up to each token of the chunk, in log2 units
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&b->v_ok[s], kScaleWarps);
             dev::mbar_init(&b->p_full[s], 1);
             dev::mbar_init(&b->p_ready[s], 4);
+            dev::mbar_init(&b->qs_full[s], 1);
             dev::mbar_init(&b->dec_full[s], 1);
             dev::mbar_init(&b->dec_empty[s], STATES ? 12 : 16);
         }
@@ -292,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&b->w_full[s], 2);
             dev::mbar_init(&b->w_empty[s], 1);
         }
-        dev::mbar_init(&b->qs_full, 1);
         dev::mbar_init(&b->o_ready, 1);
         dev::mbar_init(&b->o_free, 4);
         dev::mbar_init(&b->ds_full, 1);
@@ -335,8 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool more = false;
                 int next_left = 0, next_heads = 0;
                 auto inputs_seen = [&] {
+                    // (both halves of K: copies need not land in the order in which they were begun)
                     return seen_warp(&b->q_full[qh & 1], (qh >> 1) & 1) &&
-                           (qg > 0 || seen_warp(&b->k_full[2 * (qn % KS) + 1], (qn / KS) & 1));
+                           (qg > 0 || (seen_warp(&b->k_full[2 * (qn % KS) + 1], (qn / KS) & 1) &&
+                                       seen_warp(&b->k_full[2 * (qn % KS)], (qn / KS) & 1)));
                 };
                 // (the weights that lay in this buffer were read by the P V of two heads before, issued already)
                 auto inputs_there = [&] {
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if (!ok) break;
                                     tc::fence_after_sync();
                                     products<D>(tmem + kColO, q_lo + ((h & 1) * L::kTile >> 4), s_lo, false, id_v);
-                                    tc::mma_commit_warp(&b->qs_full);
+                                    tc::mma_commit_warp(&b->qs_full[h & 1]);
                                     tc::mma_commit_warp(&b->q_empty[h & 1]);
                                     if (g == G - 1) tc::mma_commit_warp(&b->s_empty);
                                 } else if (step == 3) {
@@ -887,7 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc::tmem_wait_st();
                     if (bad || (deep && __any_sync(0xffffffffu, up != 0.f))) {
-                        if (!(ok = wait.warp(&b->qs_full, h & 1))) break;
+                        // (two barriers: of the heads in between nobody waits for it)
+                        if (!(ok = wait.warp(&b->qs_full[h & 1], (h >> 1) & 1))) break;
                         tc::fence_after_sync();
                         finish_rows<D>(tmem + kColO + lane_base, t_p, smem + L::kV + st * L::kTile, row,
                                        deep ? dev::fast_exp2(up) : 1.f, bad);

@@ -35,6 +35,21 @@ def test_long_requests(heads, lens, cached, gate):
     assert torch.equal(c.states, again)
 
 
+@pytest.mark.parametrize("heads,lens", [((32, 8, 128), [16001]), ((28, 4, 128), [1400, 700, 1100, 500]),
+                                        ((16, 16, 64), [900, 800, 850, 600, 500, 700, 300])], ids=["long", "prompts", "64"])
+def test_many_runs_are_the_same(heads, lens):
+    """Bit for bit, with the work of every SM's roles in as many orders as the runs make."""
+    c = Case(heads, lens, [0] * len(lens), gate="token", seed=11)
+    c.log_decay *= 0.05
+    was, want = c.run()
+    c.check(was, want)
+    after = c.states.clone()
+    for _ in range(40):
+        c.states.copy_(was)
+        assert torch.equal(c.forward(), want) and torch.equal(c.states, after)
+    assert pva.attn_get_device_status(c.eng.meta) == 0
+
+
 def test_scale_and_many_requests():
     g = torch.Generator().manual_seed(3)
     lens = [int(n) for n in torch.randint(0, 40, (300,), generator=g)]
@@ -411,3 +426,55 @@ def test_hybrid_layers_back_to_back():
     for i in range(layers):
         assert torch.equal(outs[i], alone[i][0]), f"layer {i}"
         assert torch.equal(pools[i], alone[i][1] if i % 2 else pools[i]) and torch.equal(states[i], states[i] if i % 2 else alone[i][2])
+
+
+# ------------------------------------------------------------------ large sizes
+
+def test_states_past_32_bit_offsets():
+    """Slots of a pool of more than 2^31 elements, read and written by both forms: as in a small pool."""
+    lens, cached = [200, 3, 17], [5, 4, 0]
+    small = Case((32, 32, 128), lens, cached, in_place=False)
+    was, want = small.run()
+    after = small.states.clone()
+    n = (1 << 31) // (32 * 128 * 128) + 40
+    big = Case((32, 32, 128), lens, cached, in_place=False)
+    big.num_states, big.states = n, torch.empty(n, 32, 128, 128, device=DEV)
+    big.eng = pva.LinearAttention(32, 32, 128, n, 3, big.T)
+    shift = n - small.num_states
+    big.state_in, big.state_out = small.state_in + shift, small.state_out + shift
+    big.states[shift:] = was
+    big.prepare()
+    out = big.forward()
+    assert pva.attn_get_device_status(big.eng.meta) == 0
+    assert torch.equal(out, want) and torch.equal(big.states[shift:], after)
+
+
+def test_tokens_past_32_bit_offsets():
+    """The last requests of a batch of more than 2^31 elements of q: as in a batch of their own."""
+    heads, tail = (64, 1, 128), [200, 5]
+    first = (1 << 31) // (64 * 128) + 1000
+    alone = Case(heads, tail, [3, 2], gate="token")
+    was, want = alone.run()
+    T = first + sum(tail)
+    q, k, v = (torch.empty(T, h, 128, dtype=torch.bfloat16, device=DEV).fill_(0.01) for h in (64, 1, 1))
+    q[first:], k[first:], v[first:] = alone.q, alone.k, alone.v
+    decay = torch.full((T, 1), -0.01, device=DEV)
+    decay[first:] = alone.log_decay
+    states = torch.cat((was, torch.zeros_like(was[:1])))
+    eng = pva.LinearAttention(64, 1, 128, states.shape[0], 3, T)
+    slot = was.shape[0]
+    ins = torch.cat((i32(slot), alone.state_in))
+    eng.prepare(i32(0, first, first + 200, T), i32(first, 203, 7), T, ins, ins)
+    qn, kn = eng.norm_rope(q, k, norm=pva.QKNorm(), rope=pva.Rope(torch.zeros(first, 128, device=DEV) + 1.0))
+    out = eng.forward(q, k, v, decay, states)
+    assert pva.attn_get_device_status(eng.meta) == 0
+    assert torch.equal(out[first:], want) and torch.equal(states[:slot], alone.states)
+    rope = pva.Rope(torch.ones(400, 128, device=DEV))
+    alone.prepare()
+    qs, ks = alone.eng.norm_rope(alone.q, alone.k, norm=pva.QKNorm(), rope=rope)
+    assert torch.equal(qn[first:], qs) and torch.equal(kn[first:], ks)
+    # the first one's: q, k and v of one value, so o_t = scale D x^2 v sum_{s <= t} e^{-0.01 (t - s)}
+    x = float(torch.tensor(0.01, dtype=torch.bfloat16))
+    for t in (0, 1000, first - 1):
+        ref = 128 ** 0.5 * x ** 3 * (1 - 2.718281828459045 ** (-0.01 * (t + 1))) / (1 - 2.718281828459045 ** -0.01)
+        assert bool(((out[t].double() - ref).abs() <= 2.0 ** -6 * ref).all())
