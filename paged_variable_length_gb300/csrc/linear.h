@@ -61,6 +61,22 @@ inline int segment_tokens(int64_t long_tokens, int longest, int kv_heads, int sm
     return longest <= 2 * (int64_t)n || longest <= kWholeTokens ? kWholeSegment : n;
 }
 
+// Whether a batch's layer calls launch the states pass and the scan: known on the host from its bounds alone (the long
+// requests have all tokens but kStepTokens of each short one at most).
+inline bool may_cut(int64_t total_tokens, int64_t batch, int longest_bound, int kv_heads, int sms) {
+    const int64_t least = total_tokens - kStepTokens * batch;
+    return segment_tokens(least > 0 ? least : 0, longest_bound, kv_heads, sms) < kWholeSegment;
+}
+
+// What the plan goes by: it cuts only where those two kernels run, since the main pass starts a request's later
+// segments from what they leave.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int planned_segment_tokens(bool cuts_run, int64_t long_tokens, int longest, int kv_heads, int sms) {
+    return cuts_run ? segment_tokens(long_tokens, longest, kv_heads, sms) : kWholeSegment;
+}
+
 // CTAs that share a kv head's q heads (two heads or more each), where the segments' kv heads are fewer than the SMs.
 // Each of them finds the state for itself: two chunks of 700-1500 tokens, 28/4 heads, take 49 us, with one CTA a kv
 // head 70.
@@ -104,6 +120,7 @@ struct LinPlanParams {
     int32_t group;
     int32_t num_kv_heads;
     int32_t sm_count;
+    int32_t may_cut;           // LinHost's
     int64_t num_states;
     uint8_t* ws;
     LinLayout lay;

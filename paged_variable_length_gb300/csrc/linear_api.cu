@@ -252,9 +252,7 @@ pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_s
     h.total_tokens = total_tokens;
     h.max_q_len = max_q_len > 0 && max_q_len < total_tokens ? max_q_len : (total_tokens > 0 ? total_tokens : 1);
     h.sm_count = sms;
-    // (the long requests have all tokens but kStepTokens of each short one at most)
-    const int64_t least = (int64_t)total_tokens - (int64_t)kStepTokens * batch;
-    h.may_cut = segment_tokens(least > 0 ? least : 0, h.max_q_len, cfg->num_kv_heads, sms) < kWholeSegment ? 1 : 0;
+    h.may_cut = may_cut(total_tokens, batch, h.max_q_len, cfg->num_kv_heads, sms) ? 1 : 0;
     h.cu = cu_seqlens_q;
     h.seqlens = cache_seqlens;
     h.ws = static_cast<uint8_t*>(workspace);
@@ -270,6 +268,7 @@ pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_s
     pp.group = cfg->num_qo_heads / cfg->num_kv_heads;
     pp.num_kv_heads = cfg->num_kv_heads;
     pp.sm_count = sms;
+    pp.may_cut = h.may_cut;
     pp.num_states = cfg->num_states;
     pp.ws = h.ws;
     pp.lay = h.lay;

@@ -28,7 +28,7 @@ constexpr int kBuckets = 256;  // segments sorted by chunks (more: the first buc
 // no one claimed is told by that request's own out slot being another.
 __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlanParams p) {
     __shared__ int32_t hist[kBuckets], first[kBuckets];
-    __shared__ int32_t n_items, n_pre, n_segs, n_cut, longest, n_long;
+    __shared__ int32_t n_items, n_pre, n_segs, n_cut, longest;
     __shared__ unsigned long long long_tokens;
     __shared__ uint32_t all_err;
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(p.ws + p.lay.header);
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
     LinItem* cuts = reinterpret_cast<LinItem*>(p.ws + p.lay.cut_items);
     const int tid = threadIdx.x, B = p.batch;
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
-    if (tid == 0) n_items = n_pre = n_segs = n_cut = longest = n_long = 0, long_tokens = 0, all_err = 0;
+    if (tid == 0) n_items = n_pre = n_segs = n_cut = longest = 0, long_tokens = 0, all_err = 0;
 
     uint32_t err = 0;
     for (int i = tid; i < B; i += kPlanThreads) {
@@ -103,17 +103,17 @@ __global__ void __launch_bounds__(kPlanThreads) linear_plan_kernel(const LinPlan
         return *n > kStepTokens && req_state[i].x != -2;
     };
     if (!fatal) {
+        // (those that are skipped too: how the others are cut, and so their bits, does not depend on them)
         for (int i = tid; i < B; i += kPlanThreads) {
-            int n;
-            if (!is_long(i, &n)) continue;
+            const int n = p.cu[i + 1] - p.cu[i];
+            if (n <= kStepTokens) continue;
             atomicMax(&longest, n);
-            atomicAdd(&n_long, 1);
             atomicAdd(&long_tokens, (unsigned long long)n);
         }
         __syncthreads();
     }
     // how a request is cut: chunks of a segment, and segments
-    const int seg_tokens = segment_tokens((int64_t)long_tokens, longest, p.num_kv_heads, p.sm_count);
+    const int seg_tokens = planned_segment_tokens(p.may_cut, (int64_t)long_tokens, longest, p.num_kv_heads, p.sm_count);
     auto cut = [&](int n, int* per) -> int {
         const int chunks = (n + kChunk - 1) / kChunk;
         const int want = (int)(((int64_t)n + seg_tokens - 1) / seg_tokens);
