@@ -395,7 +395,8 @@ PVA_API pva_status attn_forward_norm_rope(const pva_meta* meta, const pva_qk_nor
  * both be NULL, or k and k_out.  An output is its own input (when that is contiguous, as one token's
  * always is) or lies outside the memory from the first to the last element of q and of k, and outside
  * the other output.  A token whose position lies outside the table sets PVA_DEVERR_POSITION and nothing
- * of it is written.
+ * of it is written.  It only reads the plan (but for the error word), so it may run beside other calls of
+ * the same meta, on another stream.
  */
 PVA_API pva_status attn_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const pva_rope* rope, const void* q,
                           const void* k, void* q_out, void* k_out, void* stream);

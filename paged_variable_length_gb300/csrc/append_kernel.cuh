@@ -177,9 +177,11 @@ __global__ void __launch_bounds__(kThreads, MODE == kPart ? (NORM ? 4 : 5) : NOR
     // attention kernels that follow set up behind it (as behind the store kernel)
     dev::grid_dep_wait();
     dev::grid_dep_launch();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-        hdr->pad[0] = 0;  // decode kernel work counter
-        hdr->pad[1] = 0;  // prefill kernel work counter
+    if constexpr (KV != kFlat) {  // (without a pool no attention follows, and one of the same plan may be running)
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+            hdr->pad[0] = 0;  // decode kernel work counter
+            hdr->pad[1] = 0;  // prefill kernel work counter
+        }
     }
     const uint32_t errors = hdr->error_bits;
     const int lane = threadIdx.x & 31, j = lane % LR, sub = lane / LR;
