@@ -395,7 +395,8 @@ PVA_API pva_status attn_forward_norm_rope(const pva_meta* meta, const pva_qk_nor
  * both be NULL, or k and k_out.  An output is its own input (when that is contiguous, as one token's
  * always is) or lies outside the memory from the first to the last element of q and of k, and outside
  * the other output.  A token whose position lies outside the table sets PVA_DEVERR_POSITION and nothing
- * of it is written.  It only reads the plan (but for the error word), so it may run beside other calls of
+ * of it is written (attn_linear_forward of such a k_out takes what lies there into its states: the call
+ * below that does both does not).  It only reads the plan (but for the error word), so it may run beside other calls of
  * the same meta, on another stream.
  */
 PVA_API pva_status attn_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const pva_rope* rope, const void* q,
@@ -466,7 +467,9 @@ PVA_API pva_status attn_linear_forward(const pva_meta* meta, const pva_linear_ar
 /*
  * attn_norm_rope of q and k into q_rot and k_rot, then attn_linear_forward of those: a linear layer's call
  * from projections to output.  norm may be NULL.  q, k and v have rope's strides (args' are ignored); q_rot and
- * k_rot lie outside the memory of v, the decays, the states and out as well.
+ * k_rot lie outside the memory of v, the decays, the states and out as well.  A token whose position lies
+ * outside the table sets PVA_DEVERR_POSITION; its rows of q_rot and k_rot become 0, so that its output is 0 and
+ * (with a finite v) it adds nothing to its request's state, which decays by its log decay as ever.
  */
 PVA_API pva_status attn_linear_forward_norm_rope(const pva_meta* meta, const pva_linear_args* args,
                                          const pva_qk_norm* norm, const pva_rope* rope, const void* q,

@@ -233,7 +233,18 @@ __global__ void __launch_bounds__(kThreads, MODE == kPart ? (NORM ? 4 : 5) : NOR
         const int pos = rp.positions != nullptr ? rp.positions[t] : index;
         if (pos < 0 || pos >= rp.max_positions) {
             if (lane == 0) dev::set_error(&hdr->error_bits, kErrPosition);
-            return;  // (every warp of the token: nothing of it is written)
+            if constexpr (KV == kFlat) {
+                if (rp.zero_refused) {
+                    const float none[16] = {};
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int row = row0 + r * RW + sub;
+                        if (row < Hq) store_bf16(rp.q_out + (t * Hq + row) * D, none, e0, e1);
+                        else if (row < rows) store_bf16(rp.k_out + (t * Hkv + row - Hq) * D, none, e0, e1);
+                    }
+                }
+            }
+            return;  // (every warp of the token: nothing else of it is written)
         }
         const float* cs = rp.cos_sin + (int64_t)pos * rot;
         auto take = [&](int at, int pair) {  // four pairs' values

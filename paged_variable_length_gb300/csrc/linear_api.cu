@@ -110,7 +110,7 @@ pva_status check_norm_rope(const BatchView& v, const pva_qk_norm* norm, const pv
 }
 
 pva_status launch_flat(const BatchView& v, const pva_qk_norm* norm, const pva_rope* rope, const void* q, const void* k,
-                       void* q_out, void* k_out, cudaStream_t s) {
+                       void* q_out, void* k_out, bool zero_refused, cudaStream_t s) {
     ForwardParams fp{};
     fp.k = static_cast<const uint16_t*>(k);
     fp.v = fp.k;  // (never read: there are no rows of v)
@@ -130,6 +130,7 @@ pva_status launch_flat(const BatchView& v, const pva_qk_norm* norm, const pva_ro
     rp.ld_k = rope->ld_k;
     rp.batch = v.batch;
     rp.sm_count = v.sm_count;
+    rp.zero_refused = zero_refused ? 1 : 0;
     set_rotation(rope, norm, &rp);
     return launch_norm_rope(fp, rp, v.head_dim, s) == cudaSuccess ? PVA_OK : PVA_ERR_CUDA;
 }
@@ -309,7 +310,8 @@ pva_status attn_linear_forward_norm_rope(const pva_meta* meta, const pva_linear_
     for (const Span& o : {span_of(q_rot, T, rq, rq), span_of(k_rot, T, rk, rk)})
         if (meet(o, sv) || meet(o, sg) || meet(o, ss)) return PVA_ERR_INVALID_ARG;
     if (T == 0) return PVA_OK;
-    st = launch_flat(view, norm, rope, q, k, q_rot, k_rot, static_cast<cudaStream_t>(stream));
+    // (a refused token's rows become 0: what lay in q_rot and k_rot must not enter a state that is kept)
+    st = launch_flat(view, norm, rope, q, k, q_rot, k_rot, true, static_cast<cudaStream_t>(stream));
     if (st != PVA_OK) return st;
     return launch_linear(h, args, q_rot, k_rot, v, out, rq, rk, rope->ld_v, static_cast<cudaStream_t>(stream));
 }
@@ -321,7 +323,7 @@ pva_status attn_norm_rope(const pva_meta* meta, const pva_qk_norm* norm, const p
     const pva_status st = check_norm_rope(v, norm, rope, q, k, q_out, k_out);
     if (st != PVA_OK) return st;
     if (v.total_tokens == 0) return PVA_OK;
-    return launch_flat(v, norm, rope, q, k, q_out, k_out, static_cast<cudaStream_t>(stream));
+    return launch_flat(v, norm, rope, q, k, q_out, k_out, false, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -269,6 +269,7 @@ struct RopeParams {
     const float* k_gain;
     float eps;
     uint16_t* k_out;             // without a pool: [T, Hkv, D] contiguous, or null: q alone
+    int32_t zero_refused;        // without a pool: rows of a token whose position lies outside the table become 0
 };
 
 // Host view of a prepared batch, stored inside pva_meta::opaque.

@@ -593,7 +593,8 @@ def attn_linear_forward(meta: Meta, q, k, v, log_decay, states, out, stream=None
 
 def attn_linear_forward_norm_rope(meta: Meta, norm: QKNorm | None, rope: Rope | None, q, k, v, q_rot, k_rot, log_decay,
                                   states, out, stream=None) -> None:
-    """attn_norm_rope of q and k into q_rot and k_rot, then attn_linear_forward of those."""
+    """attn_norm_rope of q and k into q_rot and k_rot, then attn_linear_forward of those.  A token whose position lies
+    outside the table is reported, and its q and k count as 0."""
     b = meta.batch or meta.of_batch()
     rargs, nargs = _rotation(rope, norm, q, k, v, b)
     args = _linear_args(b, log_decay, states, (0, 0, 0), "attn_linear_forward_norm_rope")
