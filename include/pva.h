@@ -446,8 +446,9 @@ PVA_API pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32
                                size_t workspace_bytes, void* stream, pva_meta* meta);
 
 typedef struct pva_linear_args {
-    const float* log_decay;     /* DEVICE fp32 [Hkv], or [total_tokens, Hkv] with ld_decay: natural logs, -inf (the
-                                   state is dropped) to 0; larger ones grow the state, as far as fp32 holds it */
+    const float* log_decay;     /* DEVICE fp32 [Hkv], or [total_tokens, Hkv] with ld_decay: natural logs, -inf to
+                                   0; up to -110 the state is dropped, whatever it held (infinities and NaN too);
+                                   above 0 it grows, as far as fp32 holds it */
     int64_t ld_decay;           /* 0: one value a head; else elements between tokens, at least Hkv */
     int64_t ld_q, ld_k, ld_v;   /* elements between consecutive tokens (multiples of 8); heads are contiguous */
     float* states;              /* DEVICE fp32 [num_states, Hkv, D, D], 16-byte aligned, updated in place */

@@ -16,8 +16,9 @@ namespace pva {
 
 constexpr int kChunk = 128;       // tokens of a tensor-core chunk
 constexpr uint32_t kErrState = PVA_DEVERR_STATE;
-// Log decays below this are taken as this: e^-110 is 0 in fp32, and -inf - -inf is never formed.
-constexpr float kLeastLogDecay = -110.f;
+// A log decay up to this drops the state, whatever it holds (e^-110 is 0 in fp32, but 0 times an infinity or a NaN is a
+// NaN): what lies before the token has no part in anything from it on.
+constexpr float kDropLogDecay = -110.f;
 
 // Most new tokens of a request that runs token by token, between the lengths where the tensor cores catch up: 11 tokens
 // of 64 requests of 32/8 heads of 128 (9 tokens 53 us for 63, 16 tokens 90 for 63), 15 of one such (12.8 us), 23 of
@@ -103,7 +104,7 @@ struct LinLayout {
     size_t cut_items;   // LinItem [max_segs]: the first segments of requests that are cut
     size_t seg_state;   // fp32 [max_segs][Hkv][D/4 (columns)][D (rows)][4]: a request's entry 0: a copy of its start; s:
                         // segment s - 1's end from zero, after the scan the request's state there
-    size_t seg_decay;   // fp32 [max_segs][Hkv]: entry s: the decay over segment s - 1
+    size_t seg_decay;   // fp32 [max_segs][Hkv]: entry s: the decay over segment s - 1, -1: a token of it drops the state
     size_t total;
     int32_t max_items;
     int32_t max_segs;

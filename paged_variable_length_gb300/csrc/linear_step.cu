@@ -281,7 +281,15 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
     int buf = 0;
     for (int t = 0; t < n; ++t) {
         const int64_t tok = c0 + t;
-        const float lam = expf(gw < kLeastLogDecay ? kLeastLogDecay : gw);
+        const bool drop = gw <= kDropLogDecay;
+        const float lam = drop ? 0.f : expf(gw);
+        if (drop) {
+            // (in place, as a branch: as assignments the compiler kept two forms of the token's work, 97 registers for 80, and
+            // 64 decodes of 32 heads took 49 us for 42)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                asm volatile("mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;" : "+f"(S[i].x), "+f"(S[i].y), "+f"(S[i].z), "+f"(S[i].w));
+        }
         const float v[4] = {bf_lo(vw[0]), bf_hi(vw[0]), bf_lo(vw[1]), bf_hi(vw[1])};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
 // ---------------------------------------------------------------- K12: the scan over a request's segments
 //
 // Entry i of a request's segment states, i >= 2, holds the end of segment i - 1 from zero: X_i; it becomes that
-// segment's end from the request's start, S_i = (decay over segment i - 1) S_{i-1} + X_i.  Four elements of a state a
+// segment's end from the request's start, S_i = (decay over segment i - 1) S_{i-1} + X_i (X_i alone where that drops it).  Four elements of a state a
 // thread, every segment's in turn, four loads in flight.  Bound: the L2's latency (18 segments of 8 heads of 128 x 128:
 // 18 MB in 7.3 us; each segment's CTAs summing what lies before it took up to 20).
 constexpr int kScanThreads = 256;
@@ -372,6 +380,7 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinPara
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (i + j < it.nseg) {
+                    if (f[j] < 0.f) S = make_float4(0.f, 0.f, 0.f, 0.f);  // (dropped)
                     S.x = fmaf(f[j], S.x, y[j].x), S.y = fmaf(f[j], S.y, y[j].y);
                     S.z = fmaf(f[j], S.z, y[j].z), S.w = fmaf(f[j], S.w, y[j].w);
                     s[(i + j) * step] = S;

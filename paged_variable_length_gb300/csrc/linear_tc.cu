@@ -21,7 +21,8 @@
 // r (a whole number of powers of two) is 0, or halfway in a chunk whose sums go further than 2^60, so that weights stay
 // within 2^+-60: up to sums of 2^120 (0.65 a token).  In chunks beyond that ("deep") row i's weights are
 // e^{c_i - r_i - c_j} with r_i = c_i held to +-40 (log2), its part of Q S is scaled by e^{c_i - r_i} in TMEM before
-// P V adds to it, and O takes e^{r_i}.  (With an r of 0 alone a prompt of 16 k tokens, 8 kv heads, took 135 us for 126.)
+// P V adds to it, and O takes e^{r_i}.  A chunk with a token that drops the state (a log decay of -inf) is deep too: its
+// sums start anew there, and to the tokens from it on the keys before it and S are hidden, whatever they hold.  (With an r of 0 alone a prompt of 16 k tokens, 8 kv heads, took 135 us for 126.)
 // Weight 0 times an infinity or a NaN of V behind the diagonal would reach the chunk's
 // earlier tokens, so a chunk with one takes P V row by row on the CUDA cores, over the keys that each row sees.
 //
@@ -61,6 +62,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColP = 0, kColO = 256, kColState = 384;  // TMEM columns (two buffers of Q K^T)
 constexpr float kReach = 60.f;            // largest power (log2) that enters the weights of a chunk with one r
 constexpr float kDeep = 40.f;             // the same of one with an r for each row
+constexpr int kDrops = 2;                 // in the place of "deep"
 constexpr int kPart = 16;                 // tokens of a staged part of w K
 constexpr int kParts = kChunk / kPart;
 constexpr int kPartRegion = kPart * 128;  // 16 rows of 128 bytes
@@ -93,9 +95,11 @@ struct Bars {
     uint64_t dec_full[2], dec_empty[2], drain[2];
     alignas(16) float c[2][kChunk];  // sums of the log decays up to each token of the chunk, in log2 units
     alignas(16) float f[2][kChunk];  // 2^(-c_j - r)
-    float w[2][kChunk];              // 2^(c_end - c_j); 0 behind the last token
-    float end[2], r[2], down[2];     // 2^c_end; r (log2); 2^-r
-    int32_t deep[2];                 // no r will do
+    float w[2][kChunk];              // 2^(c_end - c_j); -0 (the key counts as 0) behind the last token and of what is dropped
+    float end[2], r[2], down[2];     // 2^c_end (-1: the state is dropped); r (log2); 2^-r
+    int32_t deep[2];                 // no r will do; kDrops: a token drops the state
+    int32_t last[2];                 // (kDrops) the last token that does
+    alignas(4) int8_t first[2][kChunk];  // (kDrops) the same up to each token, -1: none; what lies before it is hidden from it
     alignas(16) int32_t v_bad[2][8];
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -248,6 +252,119 @@ __device__ __noinline__ void finish_rows(uint32_t t_o, uint32_t t_p, const uint8
             __syncwarp();
         }
         tc::tmem_st32(t_o + 32 * x, o);
+    }
+    tc::tmem_wait_st();
+}
+
+// What a token that drops the state needs lies in functions of its own, out of the roles' way: on the same box the 8
+// prompts take 167 us and 12 chunks of D 64 32.5, without any of it 165 and 31.1, with all of it in the roles' loops
+// 173 and 34.7.
+
+// The decay warp's part of a chunk with such tokens (or with NaN decays): the sums start anew at each.  g: the first
+// token's log decay, of ntok; returns whether there are any.  (In line behind that warp's own: as a call it cost the
+// prompts another 3 us.)
+__device__ __forceinline__ bool sums_with_drops(Bars* b, int st, const float* g, int64_t ld, int ntok) {
+    const int lane = threadIdx.x & 31;
+    double sum[4], y = 0.0;
+    int first[4], f = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = 4 * lane + i < ntok ? g[(4 * lane + i) * ld] : 0.f;
+        const bool drop = x <= kDropLogDecay;
+        y = drop ? 0.0 : y + (double)x * 1.4426950408889634074;
+        if (drop) f = 4 * lane + i;
+        sum[i] = y, first[i] = f;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const double z = __shfl_up_sync(0xffffffffu, y, d);
+        const int before = __shfl_up_sync(0xffffffffu, f, d);
+        if (lane >= d && f < 0) y += z, f = before;
+    }
+    const double up = __shfl_up_sync(0xffffffffu, y, 1), end = __shfl_sync(0xffffffffu, y, 31);
+    const int up_first = __shfl_up_sync(0xffffffffu, f, 1), last = __shfl_sync(0xffffffffu, f, 31);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (lane > 0 && first[i] < 0) sum[i] += up, first[i] = up_first;
+        const int t = 4 * lane + i;
+        b->c[st][t] = (float)sum[i];
+        b->w[st][t] = t >= last && t < ntok ? dev::fast_exp2((float)(end - sum[i])) : -0.f;
+        b->first[st][t] = (int8_t)first[i];
+    }
+    if (lane == 0) {
+        b->end[st] = last >= 0 ? -1.f : dev::fast_exp2((float)end);
+        b->deep[st] = last >= 0 ? kDrops : 1;
+        b->last[st] = last;
+        b->r[st] = 0.f;
+        b->down[st] = 1.f;
+    }
+    return last >= 0;
+}
+
+// An infinity or a NaN in this warp's 16 rows of V (`odd`: in the lane's part of one): where a later token drops the state
+// the row becomes 0, since its weight of 0 would not keep it from the state.
+template <int D>
+__device__ __noinline__ bool hide_odd_rows(Bars* b, uint8_t* V, int row, bool odd, int st, uint32_t parity) {
+    if (!__all_sync(0xffffffffu, phase_done(&b->dec_full[st], parity, b->wait_limit))) return false;
+    if (b->deep[st] != kDrops) return true;
+    if (odd && row < b->last[st]) {
+#pragma unroll 1
+        for (int ch = (threadIdx.x & 1) * (D / 16), e = ch + D / 16; ch < e; ++ch)
+            *reinterpret_cast<uint4*>(V + (ch >> 3) * kRegion + row * 128 + (((ch ^ row) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+    }
+    tc::fence_proxy_async_smem();
+    return true;
+}
+
+// finish_rows for a chunk with tokens that drop the state: this row's weights of the keys before `first` become 0, and
+// so does its part of Q S where there is one; and (an infinity or a NaN in V) the product with V over the keys up to
+// `last`, -1: the tensor cores add it.  V comes from memory: in shared memory odd rows may be 0.
+template <int D>
+__device__ __noinline__ void drop_rows(uint32_t t_o, uint32_t t_p, const uint16_t* V, int64_t ld_v, int row, int last, int first,
+                                       float part) {
+#pragma unroll 1
+    for (int x = 0; x <= row >> 5; ++x) {
+        float w[16];
+        uint32_t y[16];
+        tc::tmem_ld16_async(t_p + 16 * x, w);
+        tc::tmem_wait_ld16_regs(w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = 32 * x + 2 * i;
+            y[i] = __float_as_uint(w[i]) & (j >= first ? 0xFFFFFFFFu : j + 1 >= first ? 0xFFFF0000u : 0u);
+        }
+        tc::tmem_st16u(t_p + 16 * x, y);
+    }
+    tc::tmem_wait_st();
+#pragma unroll 1
+    for (int x = 0; x < D / 16; ++x) {  // (16 columns at a time: with 32 it needs more registers than its warps have)
+        float o[16];
+        uint32_t y16[16];
+        tc::tmem_ld16_async(t_o + 16 * x, o);
+        tc::tmem_wait_ld16_regs(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = first < 0 ? o[i] * part : 0.f;
+#pragma unroll 1
+        for (int j = 0; j <= last; ++j) {
+            const uint32_t w2 = tc::tmem_ld1(t_p + j / 2);
+            const float w = (j & 1) ? hi_f32(w2) : lo_f32(w2);
+            if (j <= row && j >= first) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 y = __ldg(reinterpret_cast<const uint4*>(V + j * ld_v + 16 * x + 8 * e));
+                    const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[8 * e + 2 * i] = fmaf(w, lo_f32(v[i]), o[8 * e + 2 * i]);
+                        o[8 * e + 2 * i + 1] = fmaf(w, hi_f32(v[i]), o[8 * e + 2 * i + 1]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y16[i] = __float_as_uint(o[i]);
+        tc::tmem_st16u(t_o + 16 * x, y16);
     }
     tc::tmem_wait_st();
 }
@@ -497,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Unit x = unit_of<STATES>(items, u, p, parts);
                 const int nch = chunks_of(x.it.ntok);
                 double total = 0.0;  // of the unit
+                bool dropped = false;
                 float g4[4];
                 auto load = [&](int c) {
 #pragma unroll
@@ -510,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     double sum[4], y = 0.0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        y += (double)(g4[i] < kLeastLogDecay ? kLeastLogDecay : g4[i]) * 1.4426950408889634074;
+                        y += (double)(g4[i] <= kDropLogDecay ? -INFINITY : g4[i]) * 1.4426950408889634074;
                         sum[i] = y;
                     }
                     if (c + 1 < nch) load(c + 1);
@@ -528,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) {
                         cf[i] = (float)(before + sum[i]);
                         least = fminf(least, cf[i]), most = fmaxf(most, cf[i]);
-                        if (cf[i] != cf[i]) most = INFINITY;  // (a NaN: deep)
+                        if (cf[i] != cf[i]) most = INFINITY;  // (a NaN)
                     }
 #pragma unroll
                     for (int d = 1; d < 32; d *= 2) {
@@ -542,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         b->c[st][4 * lane + i] = cf[i];
                         b->f[st][4 * lane + i] = dev::fast_exp2(-cf[i] - r);
                         b->w[st][4 * lane + i] =
-                            c * kChunk + 4 * lane + i < x.it.ntok ? dev::fast_exp2((float)(end - (before + sum[i]))) : 0.f;
+                            c * kChunk + 4 * lane + i < x.it.ntok ? dev::fast_exp2((float)(end - (before + sum[i]))) : -0.f;
                     }
                     if (lane == 0) {
                         b->end[st] = dev::fast_exp2((float)end);
@@ -550,11 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         b->r[st] = deep ? 0.f : r;
                         b->down[st] = deep ? 1.f : dev::fast_exp2(-r);
                     }
+                    if (__builtin_expect(!(least > -INFINITY && most < INFINITY), 0)) {  // (what lies there by now is written again)
+                        const float* g = p.log_decay + (p.ld_decay ? (int64_t)(x.it.tok0 + c * kChunk) * p.ld_decay : 0) + x.kvh;
+                        dropped |= sums_with_drops(b, st, g, p.ld_decay, x.it.ntok - c * kChunk);
+                    }
                     arrive_warp(&b->dec_full[st]);
                     total += end;
                 }
                 if (STATES && ok && lane == 0)
-                    seg_decay[(int64_t)(x.it.base + x.it.seg + 1) * Hkv + x.kvh] = exp2f((float)total);
+                    seg_decay[(int64_t)(x.it.base + x.it.seg + 1) * Hkv + x.kvh] = dropped ? -1.f : exp2f((float)total);
             }
         }
     } else if (!STATES && warp >= 12) {
@@ -656,7 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int any = __any_sync(0xffffffffu, is_odd(odd));
                     if (lane == 0) b->v_bad[st][x0] = any;
+                    if (__builtin_expect(any, 0) && !(ok = hide_odd_rows<D>(b, V, row, is_odd(odd), st, (n >> 1) & 1))) break;
                 }
+                if (!ok) break;
                 if (nval < kChunk) tc::fence_proxy_async_smem();
                 arrive_warp(&b->v_ok[st]);
                 if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1))) break;
@@ -672,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int x = z % L::kHalves, r = r0 + 4 * (z / L::kHalves), row = s * kPart + r;
                         const float w = b->w[st][row];
                         uint4 y = *reinterpret_cast<const uint4*>(K + x * kRegion + row * 128 + (((cc ^ row) & 7) << 4));
-                        if (row >= nval) y = make_uint4(0, 0, 0, 0);  // (whatever lies there times 0)
+                        if (__float_as_int(w) < 0) y = make_uint4(0, 0, 0, 0);  // (whatever lies there times 0)
                         const uint32_t e[4] = {y.x, y.y, y.z, y.w};
                         uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
@@ -807,6 +931,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::fence_proxy_async_smem();
                     arrive_warp(&b->s_full);
                 }
+                if (__builtin_expect(end < 0.f, 0)) {  // (dropped)
+#pragma unroll
+                    for (int x = 0; x < D; ++x) S[x >> 5][x & 31] = 0.f;
+                }
                 if (!(ok = wait.warp(&b->ds_full, n & 1))) break;
                 tc::fence_after_sync();
 #pragma unroll
@@ -849,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; ok && c < nch; ++c, ++n) {
                 const int st = n & 1;
                 if (!(ok = wait.warp(&b->dec_full[st], (n >> 1) & 1) && wait.warp(&b->v_ok[st], (n >> 1) & 1))) break;
-                const bool bad = v_is_bad(b, st), deep = b->deep[st] != 0;
+                const bool bad = v_is_bad(b, st), deep = b->deep[st] != 0, drops = b->deep[st] == kDrops;
                 const float ci = b->c[st][row], up = deep ? ci - fminf(fmaxf(ci, -kDeep), kDeep) : 0.f;
                 const float* other = deep ? b->c[st] : b->f[st];
                 for (int g = un.g0; g < un.g1; ++g, ++h) {
@@ -893,12 +1021,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::tmem_st16u(t_p + 16 * x, pk);
                     }
                     tc::tmem_wait_st();
-                    if (bad || (deep && __any_sync(0xffffffffu, up != 0.f))) {
+                    if (bad || (deep && (drops || __any_sync(0xffffffffu, up != 0.f)))) {
                         // (two barriers: of the heads in between nobody waits for it)
                         if (!(ok = wait.warp(&b->qs_full[h & 1], (h >> 1) & 1))) break;
                         tc::fence_after_sync();
-                        finish_rows<D>(tmem + kColO + lane_base, t_p, smem + L::kV + st * L::kTile, row,
-                                       deep ? dev::fast_exp2(up) : 1.f, bad);
+                        if (drops)
+                            drop_rows<D>(tmem + kColO + lane_base, t_p, p.v + (un.it.tok0 + c * (int64_t)kChunk) * p.ld_v + un.kvh * D, p.ld_v,
+                                         row, bad ? min(row | 31, un.it.ntok - c * kChunk - 1) : -1, b->first[st][row], dev::fast_exp2(up));
+                        else
+                            finish_rows<D>(tmem + kColO + lane_base, t_p, smem + L::kV + st * L::kTile, row,
+                                           deep ? dev::fast_exp2(up) : 1.f, bad);
                     }
                     tc::fence_before_sync();
                     arrive_warp(&b->p_ready[h & 1]);
