@@ -11,6 +11,8 @@
 // starts of long requests that several CTAs of the tensor-core kernel behind it work on.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "device_utils.cuh"
 #include "linear.h"
 
@@ -229,13 +231,20 @@ struct StepShape {
     static constexpr int kWarps = kThreads / 32;
 };
 
+// Where the warps' parts of the heads' results meet: two buffers.
 template <int D, int P>
-__global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(const LinParams p) {
+struct StepSums {
+    alignas(16) float at[2][StepShape<D, P>::kWarps][kHeadsAtOnce][StepShape<D, P>::kCols];
+};
+
+template <int D, int P>
+__device__ __noinline__ void steps_with_drops(const LinParams& p, StepSums<D, P>& red);
+
+// DROPS: some token of the request is known to drop the state.
+template <int D, int P, bool DROPS>
+__device__ __forceinline__ void steps(const LinParams& p, StepSums<D, P>& red) {
     using L = StepShape<D, P>;
     constexpr int R = L::kRows, H = kHeadsAtOnce;
-    __shared__ alignas(16) float red[2][L::kWarps][H][L::kCols];
-    dev::grid_dep_wait();
-    dev::grid_dep_launch();
     const int req = blockIdx.y, kvh = blockIdx.x / P, col0 = (blockIdx.x % P) * L::kCols;
     const uint32_t errors = reinterpret_cast<const PlanHeader*>(p.ws + p.lay.header)->error_bits;
     const int2 slots = reinterpret_cast<const int2*>(p.ws + p.lay.req_state)[req];
@@ -279,66 +288,82 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
 #pragma unroll
     for (int h = 0; h < H; ++h) load_head(h, c0, h);
     int buf = 0;
-    for (int t = 0; t < n; ++t) {
-        const int64_t tok = c0 + t;
-        const bool drop = gw <= kDropLogDecay;
-        const float lam = drop ? 0.f : expf(gw);
-        if (drop) {
-            // (in place, as a branch: as assignments the compiler kept two forms of the token's work, 97 registers for 80, and
-            // 64 decodes of 32 heads took 49 us for 42)
+    auto tokens = [&](auto drops) {
+        for (int t = 0; t < n; ++t) {
+            const int64_t tok = c0 + t;
+            const float lam = expf(gw);
+            if constexpr (decltype(drops)::value) {
+                if (gw <= kDropLogDecay) {
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-                asm volatile("mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;" : "+f"(S[i].x), "+f"(S[i].y), "+f"(S[i].z), "+f"(S[i].w));
-        }
-        const float v[4] = {bf_lo(vw[0]), bf_hi(vw[0]), bf_lo(vw[1]), bf_hi(vw[1])};
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float k = (i & 1) ? bf_hi(kw[i / 2]) : bf_lo(kw[i / 2]);
-            S[i].x = fmaf(k, v[0], lam * S[i].x);
-            S[i].y = fmaf(k, v[1], lam * S[i].y);
-            S[i].z = fmaf(k, v[2], lam * S[i].z);
-            S[i].w = fmaf(k, v[3], lam * S[i].w);
-        }
-        if (t + 1 < n) load_token(tok + 1);
-        for (int h0 = 0; h0 < p.group; h0 += H, buf ^= 1) {
-            const int heads = min(H, p.group - h0);
-            const bool same = h0 + H < p.group;  // the next heads are this token's
-            const int next0 = same ? h0 + H : t + 1 < n ? 0 : p.group;
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float x = (i & 1) ? bf_hi(qw[h][i / 2]) : bf_lo(qw[h][i / 2]);
-                    o.x = fmaf(x, S[i].x, o.x);
-                    o.y = fmaf(x, S[i].y, o.y);
-                    o.z = fmaf(x, S[i].z, o.z);
-                    o.w = fmaf(x, S[i].w, o.w);
+                    for (int i = 0; i < R; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
-                load_head(h, same ? tok : tok + 1, next0 + h);
-                if (h >= heads) continue;
-#pragma unroll
-                for (int m = L::kLanes; m < 32; m *= 2) {
-                    o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
-                    o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
-                    o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
-                    o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
-                }
-                if (lane < L::kLanes) *reinterpret_cast<float4*>(&red[buf][warp][h][col]) = o;
             }
-            __syncthreads();
-            // (the other buffer is written before the next barrier: nobody is more than one ahead)
-            for (int x = tid; x < heads * L::kCols / 2; x += L::kThreads) {
-                const int h = x / (L::kCols / 2), c = 2 * (x % (L::kCols / 2));
-                float a = 0.f, b = 0.f;
+            const float v[4] = {bf_lo(vw[0]), bf_hi(vw[0]), bf_lo(vw[1]), bf_hi(vw[1])};
 #pragma unroll
-                for (int w = 0; w < L::kWarps; ++w) {
-                    const float2 y = *reinterpret_cast<const float2*>(&red[buf][w][h][c]);
-                    a += y.x, b += y.y;
-                }
-                *reinterpret_cast<uint32_t*>(p.out + (tok * p.num_qo_heads + kvh * p.group + h0 + h) * D + col0 + c) =
-                    dev::pack_bf16x2(a * p.scale, b * p.scale);
+            for (int i = 0; i < R; ++i) {
+                const float k = (i & 1) ? bf_hi(kw[i / 2]) : bf_lo(kw[i / 2]);
+                S[i].x = fmaf(k, v[0], lam * S[i].x);
+                S[i].y = fmaf(k, v[1], lam * S[i].y);
+                S[i].z = fmaf(k, v[2], lam * S[i].z);
+                S[i].w = fmaf(k, v[3], lam * S[i].w);
             }
+            if (t + 1 < n) load_token(tok + 1);
+            for (int h0 = 0; h0 < p.group; h0 += H, buf ^= 1) {
+                const int heads = min(H, p.group - h0);
+                const bool same = h0 + H < p.group;  // the next heads are this token's
+                const int next0 = same ? h0 + H : t + 1 < n ? 0 : p.group;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const float x = (i & 1) ? bf_hi(qw[h][i / 2]) : bf_lo(qw[h][i / 2]);
+                        o.x = fmaf(x, S[i].x, o.x);
+                        o.y = fmaf(x, S[i].y, o.y);
+                        o.z = fmaf(x, S[i].z, o.z);
+                        o.w = fmaf(x, S[i].w, o.w);
+                    }
+                    load_head(h, same ? tok : tok + 1, next0 + h);
+                    if (h >= heads) continue;
+#pragma unroll
+                    for (int m = L::kLanes; m < 32; m *= 2) {
+                        o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+                        o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+                        o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+                        o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+                    }
+                    if (lane < L::kLanes) *reinterpret_cast<float4*>(&red.at[buf][warp][h][col]) = o;
+                }
+                __syncthreads();
+                // (the other buffer is written before the next barrier: nobody is more than one ahead)
+                for (int x = tid; x < heads * L::kCols / 2; x += L::kThreads) {
+                    const int h = x / (L::kCols / 2), c = 2 * (x % (L::kCols / 2));
+                    float a = 0.f, b = 0.f;
+#pragma unroll
+                    for (int w = 0; w < L::kWarps; ++w) {
+                        const float2 y = *reinterpret_cast<const float2*>(&red.at[buf][w][h][c]);
+                        a += y.x, b += y.y;
+                    }
+                    *reinterpret_cast<uint32_t*>(p.out + (tok * p.num_qo_heads + kvh * p.group + h0 + h) * D + col0 + c) =
+                        dev::pack_bf16x2(a * p.scale, b * p.scale);
+                }
+            }
+        }
+    };
+    if constexpr (DROPS) {
+        tokens(std::true_type{});
+    } else {
+        // Requests with a token that drops the state, whatever it holds, take a loop that looks at each token's decay: in one loop for
+        // all 12 tokens of 64 requests, 16 heads of 64, took 33 us for 28, 64 decodes of 32 heads of 128 49 for 42.  For
+        // D 64 that loop is a function of its own (in line 32 us), for D 128 it is not (a token of 64 requests, 32 heads, 44 us).
+        const float g = lane < n ? p.log_decay[(p.ld_decay ? (c0 + lane) * p.ld_decay : 0) + kvh] : 0.f;
+        if (!__any_sync(0xffffffffu, g <= kDropLogDecay)) {
+            tokens(std::false_type{});
+        } else if constexpr (D == 64) {
+            steps_with_drops<D, P>(p, red);
+            return;
+        } else {
+            tokens(std::true_type{});
         }
     }
     if (slots.y >= 0) {
@@ -346,6 +371,19 @@ __global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(
 #pragma unroll
         for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(dst + i * D) = S[i];
     }
+}
+
+template <int D, int P>
+__device__ __noinline__ void steps_with_drops(const LinParams& p, StepSums<D, P>& red) {
+    steps<D, P, true>(p, red);
+}
+
+template <int D, int P>
+__global__ void __launch_bounds__(StepShape<D, P>::kThreads) linear_step_kernel(const __grid_constant__ LinParams p) {
+    __shared__ StepSums<D, P> red;
+    dev::grid_dep_wait();
+    dev::grid_dep_launch();
+    steps<D, P, false>(p, red);
 }
 
 // ---------------------------------------------------------------- K12: the scan over a request's segments
