@@ -365,7 +365,8 @@ PVA_API pva_status attn_forward_rope(const pva_meta* meta, const pva_rope* rope,
 /*
  * Norm of each head of q and k, before the rotation: a head row x becomes x / sqrt(mean(x^2) + eps) *
  * gain, in fp32 (so are the squares and their sum: a row with elements beyond about 2^60 overflows them
- * and becomes 0, as one whose squares vanish beside eps does).
+ * and becomes 0, as one whose squares vanish beside eps does; with an eps of 0 a row whose squares vanish
+ * altogether, below about 2^-75, becomes infinities, and its zeros NaN).
  */
 typedef struct pva_qk_norm {
     const float* q_gain;        /* DEVICE fp32 [head_dim], 16-byte aligned, for every q head; NULL: ones */
@@ -434,10 +435,12 @@ PVA_API size_t attn_linear_workspace_size(const pva_linear_config* cfg);
  *                  array as state_in updates states in place; other slots keep the old ones (checkpoints, drafts
  *                  that may be dropped), and several requests may go on from one.  NULL: no state is kept.
  *   max_q_len      as there; a batch with max_q_len <= 16 launches no tensor-core kernel
- *   workspace      device, at least attn_linear_workspace_size(cfg) bytes, 256-byte aligned
+ *   workspace      device, at least attn_linear_workspace_size(cfg) bytes, 256-byte aligned, not used
+ *                  concurrently by another prepare or forward (layers of one plan run one after another)
  * A slot outside [-1, num_states), a state_out slot of two requests, and a state_out slot that another request
  * goes on from set PVA_DEVERR_STATE: of the requests at fault (those that would write, in the last case the
- * writer) nothing is written.  Requests without new tokens neither read nor write a state.
+ * writer) nothing is written, and the others' results are bit for bit what they are without the fault.
+ * Requests without new tokens neither read nor write a state.
  * The arrays must stay unchanged until the last call using `meta`.
  */
 PVA_API pva_status attn_linear_prepare(const pva_linear_config* cfg, const int32_t* cu_seqlens_q,
@@ -456,11 +459,13 @@ typedef struct pva_linear_args {
 
 /*
  * Once per layer.  q, k, v: bf16 [T, heads, D], 16-byte aligned; out: bf16 [T, Hq, D], contiguous; out and the
- * states lie outside each other's memory and that of q, k, v and the decays.  Requests of up to 16 new tokens run the recurrence as it stands,
- * in fp32; longer ones in chunks of 128 tokens on the tensor cores, where the weights within a chunk and a copy
- * of the state enter the products as bf16 (out moves by about half a bf16 step of its terms; the states keep
- * fp32's accuracy).  Tokens hidden by causality have no part in a token's output, whatever they hold; an
- * infinity in k may reach the outputs and states that see it as a NaN.
+ * states lie outside each other's memory and that of q, k, v and the decays.  Requests of up to 16 new tokens run
+ * the recurrence as it stands, in fp32; longer ones in chunks of 128 tokens on the tensor cores, where the weights
+ * within a chunk and a copy of the state enter the products as bf16: out moves by about half a bf16 step of its
+ * terms (and where a chunk's decays sum to thousands by up to as much again), the states keep fp32's accuracy.
+ * Scores q . k and states enter those products times up to 2^60, so beyond some 2^60 they may overflow there.
+ * Tokens hidden by causality or by a later token that drops the state have no part in an output or a state,
+ * whatever they hold; an infinity in k or v may reach the outputs and states that see it as a NaN.
  */
 PVA_API pva_status attn_linear_forward(const pva_meta* meta, const pva_linear_args* args, const void* q, const void* k,
                                const void* v, void* out, void* stream);

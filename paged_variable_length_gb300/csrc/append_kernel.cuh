@@ -6,7 +6,8 @@
 // eps): fp32 throughout, the squares summed 16 to a lane and then over the row's lanes by shuffles,
 // x * r rounded before the gain.  v passes.  The norm takes no pass of its own: the row is in
 // registers already (16.6 k tokens of 32/8 heads of 128 into a bf16 pool, 410 MB, take 70 us with it,
-// 5.8 TB/s, and 65 without; q and k of 9.1 k tokens without a pool, 300 MB, 55 us, 5.5 TB/s).
+// 5.8 TB/s, and 62 without; into E4M3 84 and 75, for 55 of bytes: its 16 divisions a lane and row stand in the way; into
+// MXFP4 70 and 59 for 53; q and k of 9.1 k tokens without a pool, 300 MB, 55 us, 5.5 TB/s).
 //
 // For token t at position p and pair i < rot/2, with c = cos_sin[p][i], s = cos_sin[p][rot/2+i]:
 //   y1 = x1 c - x2 s,  y2 = x2 c + x1 s
@@ -165,7 +166,7 @@ __device__ __forceinline__ void store_mx(uint8_t* row, const float (&y)[16], int
 // KV: PVA_KV_BF16, PVA_KV_E4M3, PVA_KV_MXFP4 or kFlat.  NORM: q and k are normed first.  R: row steps a warp takes
 // (each 512 elements); a warp serves one token.  (Without a norm kPart alone needs its registers bounded: five blocks an SM, 52.8 us for
 // the append and read-back above with rot = 3/4 D, against 56.0 unbounded and 58.6 at six; 0 leaves
-// the others unbounded, a bound of 1 cost the bf16 append 5 us.  With a norm five for all but kPart: 16 k
+// the others unbounded, a bound of 1 cost the bf16 append 5 us.  With a norm five for all but kPart: 15.3 k
 // tokens of 32/8 heads into E4M3 76 us, unbounded 84, rot = D/2 into bf16 67 and 74, q and k of 9.1 k tokens without a
 // pool 54.6 and 57.9, at six 60.7.)
 template <int D, int KV, int MODE, int R, bool NORM>

@@ -21,8 +21,8 @@ constexpr uint32_t kErrState = PVA_DEVERR_STATE;
 constexpr float kDropLogDecay = -110.f;
 
 // Most new tokens of a request that runs token by token, between the lengths where the tensor cores catch up: 11 tokens
-// of 64 requests of 32/8 heads of 128 (9 tokens 53 us for 63, 16 tokens 90 for 63), 15 of one such (12.8 us), 23 of
-// 64 requests of 16/16 heads of 64 (16 tokens 33 us for 44, 24 tokens 46).  Their results keep fp32's accuracy.
+// of 64 requests of 32/8 heads of 128 (9 tokens 53 us for 60, 16 tokens 88 for 60), 16 of one such (13 us), 23 of
+// 64 requests of 16/16 heads of 64 (16 tokens 34 us for 46, 24 tokens 48).  Their results keep fp32's accuracy.
 constexpr int kStepTokens = 16;
 
 // A segment of a long request: tokens tok0 .. tok0 + ntok - 1.
@@ -40,10 +40,11 @@ static_assert(sizeof(LinItem) == 32, "LinItem is one 32-byte record");
 
 // Tokens of a segment.  A long request is cut where its batch's heads and requests alone would leave SMs idle: the
 // long requests' tokens dealt out evenly to as many segments as there are SMs for a kv head each, a chunk at least
-// (with two at least a prompt of 700 tokens, 16/1 heads, took 29 us for 23, two of 750-1500, 28/4 heads, 43 for 38,
-// though two of 150-300 22 for 25).  A cut costs a first pass over K and V (about a third of the whole), so a request
-// that is not longer than two such shares stays whole: 8 prompts of 256-4096 tokens and 32 heads took 208 us cut at
-// one share and 175 whole, one of 16001 tokens and 8 kv heads 1545 us whole and 126 cut.
+// (with two at least a prompt of 700 tokens, 16/1 heads, takes 29 us for 22, two of 750-1500, 28/4 heads, 37 for 30,
+// two of 150-300 the same 28.5).  A cut costs a first pass over K and V (about a third of the whole), so a batch
+// whose longest request is not longer than two such shares, or than kWholeTokens, stays whole (8 prompts of 256-4096
+// tokens and 32 heads take 169 us cut at one share and 168 whole; one of 16001 tokens and 8 kv heads 677 whole and 112
+// cut).  In any other every request longer than a share is cut, so that none keeps the others' SMs waiting.
 constexpr int kWholeSegment = 1 << 30;
 constexpr int kWholeTokens = 4 * kChunk;
 #ifdef __CUDACC__
@@ -79,8 +80,8 @@ inline int planned_segment_tokens(bool cuts_run, int64_t long_tokens, int longes
 }
 
 // CTAs that share a kv head's q heads (two heads or more each), where the segments' kv heads are fewer than the SMs.
-// Each of them finds the state for itself: two chunks of 700-1500 tokens, 28/4 heads, take 49 us, with one CTA a kv
-// head 70.
+// Each of them finds the state for itself: two prompts of 500 tokens, 28/4 heads, take 39 us, with one CTA a kv
+// head 67; one, 16/1 heads, 26 and 126.
 #ifdef __CUDACC__
 __host__ __device__
 #endif

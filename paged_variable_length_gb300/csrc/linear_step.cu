@@ -7,7 +7,7 @@
 // against 2 KiB of activations); 64 requests of 32 heads, a token each: 270 MB in 42 us, 6.4 TB/s.  A thread
 // keeps four columns of some rows in registers, so that a warp's accesses are whole rows and every load of the state
 // is in flight before the first is used.  Of several tokens the next one's k, v and q are loaded while one is worked
-// on (16 tokens of 64 requests, 32/8 heads: 90 us, without 103; of 4 requests 14, without 22).  It also copies the
+// on (16 tokens of 64 requests, 32/8 heads: when it came in 90 us for 103, of 4 requests 14 for 22; now 88 and 13).  It also copies the
 // starts of long requests that several CTAs of the tensor-core kernel behind it work on.
 #include <cuda_runtime.h>
 
@@ -437,7 +437,7 @@ template <int D>
 cudaError_t launch_step_d(const LinParams& p, cudaStream_t s) {
     // 64 columns a CTA, 8 rows a thread: its state and what is on its way take some 80 registers, three CTAs of 256 threads
     // an SM (a token of 64 requests, 32 heads of 128: 42 us, with 32 columns 45, with all 128 too).  32 columns where
-    // that would leave half the SMs without work (4 requests of 8 heads of 128: 2.3 us for 2.8, of 16 tokens 13.8 for 19).
+    // that would leave half the SMs without work (4 requests of 8 heads of 128: 2.3 us for 2.8, of 16 tokens 13.4 for 19).
     constexpr int P = D / 64;
     const int64_t heads = (int64_t)p.batch * p.num_kv_heads;
     return 2 * heads > p.sm_count ? launch_step<D, P>(p, s) : launch_step<D, 2 * P>(p, s);

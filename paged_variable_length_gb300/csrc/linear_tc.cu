@@ -15,24 +15,29 @@
 //                last token, and note whether V holds an infinity or a NaN;
 //   warps 12-15  the rows of O, times scale e^{c_i + r}, to bf16 in HBM (in the states pass w K too);
 //   warp 16      issues the MMAs of the outputs, warp 17 the state's; warp 18 loads Q, K and V (TMA, 128-byte
-//                swizzle); warp 19 sums the decays (in 64 bits: differences of far sums keep their bits).
-// Roundings to bf16: P and the copy of S, each half a step of the term it scales; out.
+//                swizzle); warp 19 sums the decays (in 64 bits; the state's weights are formed of
+//                differences of those, the outputs' of the sums rounded to fp32).
+// Roundings to bf16: P and the copy of S, each half a step of the term it scales; out.  (8 prompts of normal values: out
+// is 2.35e-3 of its norm off, which is what the plain form makes with those two roundings, and 1.66e-3 with the last
+// alone.)  The sums' roundings move an output's weights by 2^-23 ln 2 of the chunk's sum (log2): 2e-5 at 2^8, 1.7e-3 at the
+// 20 000 that 128 tokens can come to.
 //
 // r (a whole number of powers of two) is 0, or halfway in a chunk whose sums go further than 2^60, so that weights stay
 // within 2^+-60: up to sums of 2^120 (0.65 a token).  In chunks beyond that ("deep") row i's weights are
 // e^{c_i - r_i - c_j} with r_i = c_i held to +-40 (log2), its part of Q S is scaled by e^{c_i - r_i} in TMEM before
 // P V adds to it, and O takes e^{r_i}.  A chunk with a token that drops the state (a log decay of -inf) is deep too: its
-// sums start anew there, and to the tokens from it on the keys before it and S are hidden, whatever they hold.  (With an r of 0 alone a prompt of 16 k tokens, 8 kv heads, took 135 us for 126.)
+// sums start anew there, and to the tokens from it on the keys before it and S are hidden, whatever they hold.  (With an r of
+// 0 alone a prompt of 16 k tokens, 8 kv heads, takes 117 us for 112.)
 // Weight 0 times an infinity or a NaN of V behind the diagonal would reach the chunk's
 // earlier tokens, so a chunk with one takes P V row by row on the CUDA cores, over the keys that each row sees.
 //
 // States pass: only w K, V and the state update; the segments' own states and decays go to the workspace, where
 // the scan (K12) makes of them the states that the main pass starts its segments from.
 //
-// Measured: 8 prompts of 0.5-3.7 k tokens, 32 heads of 128, 165 us (561 MB, 3.4 TB/s; tensor pipe 34 % of active
-// cycles), 16 k tokens of 32/8 heads 110 us with the states pass (24) and the scan (7).  Bound: the roles' hand-offs, some
-// 200 cycles each, a dozen in a row a chunk, and the fetching of instructions.  (O in warps of their own: with the warps of P
-// writing it the prompts took 170 us, the 16 k tokens 122.)
+// Measured: 8 prompts of 0.5-3.7 k tokens, 32 heads of 128, 168 us (561 MB, 3.3 TB/s; tensor pipe 33 % of active
+// cycles), 16 k tokens of 32/8 heads 112 us with the states pass (26) and the scan (8).  Bound: the roles' hand-offs, some
+// 200 cycles each, a dozen in a row a chunk, and the fetching of instructions.  (O in warps of their own: when they came in,
+// the prompts went from 170 us, with the warps of P writing it, to 165, the 16 k tokens from 122 to 110.)
 //
 // Every wait is bounded; a timeout sets PVA_DEVERR_TIMEOUT and the CTA winds down (outstanding copies
 // and MMAs waited for, TMEM freed) without trapping.

@@ -21,7 +21,8 @@ def i32(*x):
     ((32, 32, 64), [1500] * 3, {0: 5, 2: 5}),           # two requests at one slot
     ((16, 4, 128), [3000, 5, 2500, 700], {2: 99}),      # a batch that is cut
     ((16, 4, 128), [3000, 5, 2500, 700], {0: 99, 2: 99}),
-], ids=["two", "eight", "clash", "cut", "cut-longest"])
+    ((64, 8, 64), [200] * 9, {i: -2 for i in range(1, 7)}),      # the others' q heads shared by more CTAs than without the fault
+], ids=["two", "eight", "clash", "cut", "cut-longest", "parts"])
 def test_long_requests_beside_skipped_ones(heads, lens, bad, hint):
     """Requests with bad state slots are skipped; how the others are cut, and their bits, do not depend on them,
     whatever an earlier batch left in the workspace."""
